@@ -73,18 +73,17 @@ BF16_PEAK_TFLOPS = 2500.0  # MI355X dense bf16 MFMA, TFLOP/s
 # the HBM-bytes summary under profiles/).
 # Valid only for the kernel source they were taken with: reported as null
 # once the ping-pong kernel's source changes (gemm_source_hash).
-GEMM_TRAFFIC = {"bytes": 1.2248e+09 + 4.7087e+07, "gemm_source_sha256": "ed4c14be68341a65"}
+GEMM_TRAFFIC = {"bytes": 1.2248e+09 + 4.7087e+07, "gemm_source_sha256": "892fdb7779718f21"}
 
 
 def gemm_source_hash():
-    """SHA-256 prefix of the ping-pong kernel's source (its section of
-    gemm.hip, from its header comment to the skinny kernel's, and the shared
-    tile helpers): the traffic figure stays valid while these are unchanged."""
+    """SHA-256 prefix of the ping-pong kernel's source (its body's header, from
+    its header comment on, and the shared tile helpers): the traffic figure
+    stays valid while these are unchanged."""
     import hashlib
     csrc = os.path.join(ROOT, "w8a8_fp8_block_amd", "csrc")
-    g = open(os.path.join(csrc, "gemm.hip")).read()
-    i, j = g.index("// Ping-pong kernel:"), g.index("// Skinny kernel for decode")
-    text = g[i:j] + open(os.path.join(csrc, "mfma_common.h")).read()
+    g = open(os.path.join(csrc, "gemm_pp.h")).read()
+    text = g[g.index("// Ping-pong kernel:"):] + open(os.path.join(csrc, "mfma_common.h")).read()
     return hashlib.sha256(text.encode()).hexdigest()[:16]
 
 

@@ -2,7 +2,9 @@
 
     python -m w8a8_fp8_block_amd.build
 
-hipcc cross-compiles for gfx950 without a GPU present.  Flags:
+hipcc cross-compiles for gfx950 without a GPU present.  The sources compile
+in parallel, each to an object of its own, and are linked into one library.
+Flags:
   -O3 --offload-arch=gfx950           the only target
   -Xclang -target-feature -Xclang -packed-fp32-ops
                                       keep the compiler from emitting packed
@@ -19,6 +21,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -27,9 +31,10 @@ LIB_PATH = os.path.join(HERE, "libfp8q.so")
 SOURCES = ["fp8q_api.hip", "quant.hip", "relayout.hip", "gemm.hip", "gemm_bf16.hip", "dequant.hip",
            "ffn.hip", "clock.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+JOBS = 8
 
 FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wall", "-Wno-unused-function", "-Wno-unknown-pragmas",
@@ -37,9 +42,7 @@ FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB_PATH + ".tmp"
-    cmd = [HIPCC, *FLAGS, *[os.path.join(CSRC, s) for s in SOURCES], "-o", tmp]
+def _run(cmd, verbose: bool):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -49,6 +52,15 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(JOBS) as pool:
+        out = [os.path.join(objs, s + ".o") for s in SOURCES]
+        list(pool.map(lambda so: _run([HIPCC, *FLAGS, "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+                      zip(SOURCES, out)))
+        _run([HIPCC, "--offload-arch=gfx950", "-shared", *out, "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 
