@@ -556,6 +556,121 @@ fp8q_status fp8q_ffn(const uint16_t *x_bf16, const uint8_t *w_gate,
                      size_t workspace_bytes, uint32_t M, uint32_t H, uint32_t I,
                      int variant, hipStream_t stream);
 
+/* -------------------------------------------------- expert routing */
+
+/* A sparse FFN sends each of T tokens to top_k of E experts.  A slot is one
+ * (token, choice): s = t*top_k + j, R = T*top_k of them.  The grouping of the
+ * slots by expert that every call below shares:
+ *   order    [R] int32: the slots sorted by expert, stable (slot order within
+ *            an expert); slots without an expert (id outside 0..E-1) come last
+ *   pos      [R] int32: the inverse, order[pos[s]] = s
+ *   offsets  [E+1] int32: offsets[e] = slots of experts below e, so that
+ *            expert e holds the sorted rows offsets[e] .. offsets[e+1]-1
+ * All of it stays on the device: the calls that use it size their launches
+ * for any distribution and never read it on the host.  Results do not depend
+ * on scheduling (no atomics). */
+#define FP8Q_MAX_EXPERTS 512
+#define FP8Q_MAX_TOP_K 32
+
+/* Top-k routing of router logits, and the grouping:
+ *   logits    [T,E] fp32 (logits_bf16 = 0) or bf16 (1), read only.  -inf and
+ *             NaN are never chosen; +inf counts as the largest finite value
+ *   ids       [T,top_k] int32 out: each token's experts by falling logit,
+ *             ties to the lowest index; -1 where fewer than top_k can be chosen
+ *   weights   [T,top_k] fp32 out: exp(l - lmax) over the sum of the same over
+ *             the chosen experts (renormalize = 1) or all of them (0); 0 for
+ *             id -1.  fp32 throughout
+ *   order, pos, offsets   out, as above
+ *   workspace of fp8q_moe_route_workspace_bytes(T, E, top_k) bytes (may be NULL
+ *             when that is 0: one launch up to 64 tokens, else two); contents
+ *             undefined on return; calls in flight must not share it
+ * 1 <= E <= FP8Q_MAX_EXPERTS, 1 <= top_k <= min(E, FP8Q_MAX_TOP_K),
+ * T*top_k < 2^31, T*E < 2^32.  Errors: FP8Q_ERR_SHAPE for those and a short
+ * workspace, FP8Q_ERR_VARIANT for flags other than 0/1, and as everywhere.
+ * T == 0 writes the empty grouping's offsets (zeros). */
+fp8q_status fp8q_moe_route(const void *logits, int logits_bf16, int32_t *ids,
+                           float *weights, int32_t *order, int32_t *pos,
+                           int32_t *offsets, void *workspace,
+                           size_t workspace_bytes, uint32_t T, uint32_t E,
+                           uint32_t top_k, int renormalize, hipStream_t stream);
+size_t fp8q_moe_route_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k);
+
+/* The grouping alone, from n given ids [n] int32 (a router of the caller's own,
+ * or the experts of one rank: ids outside 0..groups-1 are slots of no group).
+ * 1 <= groups <= FP8Q_MAX_EXPERTS, n < 2^31; order and pos [n], offsets
+ * [groups+1].  Workspace and errors as above; n == 0 as T == 0. */
+fp8q_status fp8q_group_rows(const int32_t *ids, int32_t *order, int32_t *pos,
+                            int32_t *offsets, void *workspace,
+                            size_t workspace_bytes, uint32_t n, uint32_t groups,
+                            hipStream_t stream);
+size_t fp8q_group_rows_workspace_bytes(uint32_t n, uint32_t groups);
+
+/* out[t] = bf16_rne( sum over j, in order, of weights[t][j] * y[pos[t][j]] ) in
+ * fp32: the experts' outputs y [R,H] bf16 (sorted rows) back to the tokens.
+ * Slots without an expert add nothing; a token with none gets zeros.
+ * H % 8 == 0, T*top_k < 2^31, R*H < 2^32. */
+fp8q_status fp8q_moe_combine(const uint16_t *y_bf16, const float *weights,
+                             const int32_t *pos, const int32_t *offsets,
+                             uint16_t *out_bf16, uint32_t T, uint32_t E,
+                             uint32_t top_k, uint32_t H, hipStream_t stream);
+
+/* --------------------------------------- products grouped by expert */
+
+/* fp8q_gemm_blockscaled with each sorted row's own expert's weights:
+ *   out[p,n] = bf16_rne( sum_kb a_scale_km[kb*Ap + r] * w_scale[e][n/128][kb]
+ *                        * sum_{j<128} dec(a[r,128kb+j]) * dec(w[e][n,128kb+j]) )
+ *   r = order[p] / top_k  (order NULL: r = p), offsets[e] <= p < offsets[e+1]
+ *   a_e4m3       [a_rows,K] codes, a_scale_km [K/128, Ap] K-major scales,
+ *                Ap = ceil16(a_rows).  With order: the tokens' rows (a_rows =
+ *                T), each read by its top_k slots; without: rows already in
+ *                sorted order (a_rows = R)
+ *   w_e4m3       [E,N,K], w_scale [E,N/128,K/128]
+ *   out_bf16     [R,N]: rows of no expert (p >= offsets[E]) are left as they are
+ *   kernel       0 automatic (fp8q_gemm_grouped_select), 1 weight streaming,
+ *                2 128x128 tiles, 3 256x128 tiles; 2 and 3 give the same
+ *                results, 1 may differ in the order of the fp32 sums
+ * N % 128 == 0, K % 128 == 0, 1 <= E <= FP8Q_MAX_EXPERTS; element counts of a,
+ * out and one expert's weights below 2^32 (the whole of w may be larger).
+ * Plans that are not groupings give unspecified rows, in bounds. */
+fp8q_status fp8q_gemm_grouped(const uint8_t *a_e4m3, const float *a_scale_km,
+                              const uint8_t *w_e4m3, const float *w_scale,
+                              const int32_t *offsets, const int32_t *order,
+                              uint16_t *out_bf16, uint32_t a_rows, uint32_t R,
+                              uint32_t E, uint32_t top_k, uint32_t N, uint32_t K,
+                              int kernel, hipStream_t stream);
+/* Kernel fp8q_gemm_grouped takes with kernel 0 for R rows in E groups (by the
+ * mean rows a group).  Pure host function; 0 if E == 0. */
+int fp8q_gemm_grouped_select(uint32_t R, uint32_t E);
+
+/* The experts' FFN, the sparse sibling of fp8q_ffn:
+ *   out[t] = bf16( sum_j weights[t][j] * y[pos[t][j]] )        (fp8q_moe_combine)
+ *   y[p]   = bf16( down_e( quant( h[p] ) ) ),  h = bf16( silu(gate_e) * up_e ),
+ *   gate_e = bf16( quant(x[r]) . Wg[e]^T ), up_e alike, r = order[p] / top_k
+ * with every intermediate in the format it has in fp8q_ffn.
+ *   x_bf16 [T,H]; weights [T,top_k] fp32; order, pos, offsets from
+ *   fp8q_moe_route or fp8q_group_rows
+ *   w_gate, w_up [E,I,H] with scales [E,I/128,H/128]; w_down [E,H,I] with
+ *   scales [E,H/128,I/128]
+ *   out_bf16 [T,H]
+ *   workspace of fp8q_moe_ffn_workspace_bytes(...) bytes, 16-byte aligned
+ *   variant  0 automatic, 1 fused gate/up kernel, 2 separate gate and up;
+ *            0 takes 1 from a mean of fp8q_moe_ffn's own threshold of rows an
+ *            expert (fp8q_moe_ffn_select)
+ * H % 128 == 0, I % 128 == 0.  x is quantized once a token.  Limits as
+ * fp8q_gemm_grouped (with R = T*top_k rows of H and of I). */
+fp8q_status fp8q_moe_ffn(const uint16_t *x_bf16, const float *weights,
+                         const int32_t *order, const int32_t *pos,
+                         const int32_t *offsets, const uint8_t *w_gate,
+                         const float *w_gate_scale, const uint8_t *w_up,
+                         const float *w_up_scale, const uint8_t *w_down,
+                         const float *w_down_scale, uint16_t *out_bf16,
+                         void *workspace, size_t workspace_bytes, uint32_t T,
+                         uint32_t E, uint32_t top_k, uint32_t H, uint32_t I,
+                         int variant, hipStream_t stream);
+int fp8q_moe_ffn_select(uint32_t T, uint32_t E, uint32_t top_k);
+size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k,
+                                    uint32_t H, uint32_t I, int variant);
+
 /* ------------------------------------------------- measurement support */
 
 /* Clock stamp, for measuring the sustained shader clock over a region of a

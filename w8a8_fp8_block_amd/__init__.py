@@ -18,6 +18,12 @@ Names match the C entry points:
   fp8q_ffn_gate_up(x_q, x_scale_km, w_gate, w_gate_scale, w_up, w_up_scale, h, h_scale_km)
   fp8q_ffn(x, w_gate, w_gate_scale, w_up, w_up_scale, w_down, w_down_scale, out,
            workspace, variant=0)
+  fp8q_moe_route(logits, ids, weights, order, pos, offsets, workspace, renormalize=True)
+  fp8q_group_rows(ids, order, pos, offsets, workspace)
+  fp8q_gemm_grouped(a, a_scale_km, w, w_scale, offsets, out, order=None, top_k=1, kernel=0)
+  fp8q_moe_ffn(x, weights, order, pos, offsets, w_gate, w_gate_scale, w_up, w_up_scale,
+               w_down, w_down_scale, out, workspace, variant=0)
+  fp8q_moe_combine(y, weights, pos, offsets, out)
   fp8q_m_pad(m), fp8q_quant_select(M, K, cu_count), ...
 
 Dtypes: bf16 tensors may be torch.bfloat16 or torch.uint16/int16 views;
@@ -94,6 +100,16 @@ _SIGS = {
     "fp8q_ffn_select": (_I, [_U, _U, _U]),
     "fp8q_ffn_workspace_bytes": (ctypes.c_size_t, [_U, _U, _U, _I]),
     "fp8q_ffn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _U, _U, _U, _I, _P]),
+    "fp8q_moe_route": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _SZ, _U, _U, _U, _I, _P]),
+    "fp8q_moe_route_workspace_bytes": (_SZ, [_U, _U, _U]),
+    "fp8q_group_rows": (_I, [_P, _P, _P, _P, _P, _SZ, _U, _U, _P]),
+    "fp8q_group_rows_workspace_bytes": (_SZ, [_U, _U]),
+    "fp8q_moe_combine": (_I, [_P, _P, _P, _P, _P, _U, _U, _U, _U, _P]),
+    "fp8q_gemm_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _U, _U, _U, _U, _U, _U, _I, _P]),
+    "fp8q_gemm_grouped_select": (_I, [_U, _U]),
+    "fp8q_moe_ffn": (_I, [_P] * 13 + [_SZ, _U, _U, _U, _U, _U, _I, _P]),
+    "fp8q_moe_ffn_select": (_I, [_U, _U, _U]),
+    "fp8q_moe_ffn_workspace_bytes": (_SZ, [_U, _U, _U, _U, _U, _I]),
 }
 
 _lib = None
@@ -381,6 +397,131 @@ def fp8q_ffn(x, w_gate, w_gate_scale, w_up, w_up_scale, w_down, w_down_scale, ou
                          _ptr(w_down), _ptr(w_down_scale), _ptr(out), _ptr(workspace),
                          workspace.numel() * workspace.element_size(), M, H, I, variant,
                          _stream(stream)))
+
+
+def _int32(t, what):
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{what} must be int32, got {t.dtype}")
+    return _ptr(t)
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _grouping(order, pos, offsets, R, E):
+    """Pointers of a grouping of R slots into E groups (each may be None)."""
+    for t, n, what in ((order, R, "order"), (pos, R, "pos"), (offsets, E + 1, "offsets")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{what} has {t.numel()} elements, {n} needed")
+    return [0 if t is None else _int32(t, w) for t, w in ((order, "order"), (pos, "pos"), (offsets, "offsets"))]
+
+
+def fp8q_moe_route_workspace_bytes(T: int, E: int, top_k: int) -> int:
+    return int(lib().fp8q_moe_route_workspace_bytes(T, E, top_k))
+
+
+def fp8q_moe_route(logits, ids, weights, order, pos, offsets, workspace, renormalize: bool = True,
+                   stream=None):
+    """Top-k routing of logits [T,E] (float32 or bfloat16) and the grouping of
+    the T*top_k slots by expert.  Out: ids [T,top_k] int32, weights [T,top_k]
+    float32, order and pos [T*top_k] int32, offsets [E+1] int32; workspace: a
+    device tensor of fp8q_moe_route_workspace_bytes(T, E, top_k) bytes, or
+    None when that is 0."""
+    import torch
+    T, E = _dims(logits, 2)
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    T2, k = _dims(ids, 2)
+    if T2 != T or _dims(weights, 2) != (T, k):
+        raise ValueError("logits, ids and weights disagree in shape")
+    if weights.dtype != torch.float32:
+        raise TypeError(f"weights must be float32, got {weights.dtype}")
+    o, p, f = _grouping(order, pos, offsets, T * k, E)
+    _check(lib().fp8q_moe_route(_ptr(logits), int(logits.dtype == torch.bfloat16), _int32(ids, "ids"),
+                               _ptr(weights), o, p, f, _optr(workspace), _nbytes(workspace), T, E, k,
+                               int(bool(renormalize)), _stream(stream)))
+
+
+def fp8q_group_rows_workspace_bytes(n: int, groups: int) -> int:
+    return int(lib().fp8q_group_rows_workspace_bytes(n, groups))
+
+
+def fp8q_group_rows(ids, order, pos, offsets, workspace, stream=None):
+    """The grouping of given ids (any shape, int32) into offsets.numel() - 1
+    groups; ids outside them come last.  workspace: a device tensor of
+    fp8q_group_rows_workspace_bytes(n, groups) bytes, or None when that is 0."""
+    n, groups = ids.numel(), offsets.numel() - 1
+    o, p, f = _grouping(order, pos, offsets, n, groups)
+    _check(lib().fp8q_group_rows(_int32(ids, "ids"), o, p, f, _optr(workspace), _nbytes(workspace), n,
+                                groups, _stream(stream)))
+
+
+def fp8q_moe_combine(y, weights, pos, offsets, out, stream=None):
+    """out [T,H] = the weighted sum of each token's rows of y [T*top_k,H]
+    (sorted rows, bf16), weights [T,top_k] float32."""
+    T, k = _dims(weights, 2)
+    R, H = _dims(y, 2)
+    if R != T * k or _dims(out, 2) != (T, H):
+        raise ValueError("y, weights and out disagree in shape")
+    E = offsets.numel() - 1
+    _, p, f = _grouping(None, pos, offsets, R, E)
+    _check(lib().fp8q_moe_combine(_ptr(y), _ptr(weights), p, f, _ptr(out), T, E, k, H, _stream(stream)))
+
+
+def fp8q_gemm_grouped_select(R: int, E: int) -> int:
+    """Kernel fp8q_gemm_grouped runs with kernel=0 for R rows in E groups:
+    1 weight streaming, 2 128x128 tiles, 3 256x128 tiles."""
+    return int(lib().fp8q_gemm_grouped_select(R, E))
+
+
+def fp8q_gemm_grouped(a, a_scale_km, w, w_scale, offsets, out, order=None, top_k: int = 1,
+                      kernel: int = 0, stream=None):
+    """out [R,N] = each sorted row times its expert's weights w [E,N,K] (block
+    scales [E,N/128,K/128]).  With order, sorted row p reads activation row
+    order[p] // top_k of a [R/top_k,K]; without, row p of a [R,K].  a_scale_km:
+    K-major scales of a's rows.  Rows past offsets[E] are left as they are."""
+    rows, K = _dims(a, 2)
+    E, N, K2 = _dims(w, 3)
+    R, N2 = _dims(out, 2)
+    if K2 != K or N2 != N:
+        raise ValueError("a, w and out disagree in shape")
+    if _dims(w_scale, 3) != (E, N // 128, K // 128) or _dims(a_scale_km, 2) != (K // 128, (rows + 15) // 16 * 16):
+        raise ValueError("a scale tensor's shape does not match")
+    o, _, f = _grouping(order, None, offsets, R, E)
+    _check(lib().fp8q_gemm_grouped(_ptr(a), _ptr(a_scale_km), _ptr(w), _ptr(w_scale), f, o, _ptr(out), rows,
+                                  R, E, top_k, N, K, kernel, _stream(stream)))
+
+
+def fp8q_moe_ffn_select(T: int, E: int, top_k: int) -> int:
+    """Variant fp8q_moe_ffn runs with variant=0: 1 fused gate/up, 2 separate."""
+    return int(lib().fp8q_moe_ffn_select(T, E, top_k))
+
+
+def fp8q_moe_ffn_workspace_bytes(T: int, E: int, top_k: int, H: int, I: int, variant: int = 0) -> int:
+    return int(lib().fp8q_moe_ffn_workspace_bytes(T, E, top_k, H, I, variant))
+
+
+def fp8q_moe_ffn(x, weights, order, pos, offsets, w_gate, w_gate_scale, w_up, w_up_scale, w_down,
+                 w_down_scale, out, workspace, variant: int = 0, stream=None):
+    """The experts' FFN: out [T,H] = the weighted sum over each token's experts
+    of down(quant(bf16(silu(gate) * up))) of x [T,H].  weights [T,top_k]
+    float32 and the grouping as from fp8q_moe_route; w_gate, w_up [E,I,H],
+    w_down [E,H,I]; workspace: a device byte tensor of
+    fp8q_moe_ffn_workspace_bytes(T, E, top_k, H, I, variant)."""
+    T, H = _dims(x, 2)
+    T2, k = _dims(weights, 2)
+    E, I, H2 = _dims(w_gate, 3)
+    if T2 != T or H2 != H or _dims(w_up, 3) != (E, I, H) or _dims(w_down, 3) != (E, H, I) or _dims(out, 2) != (T, H):
+        raise ValueError("x, the weights and out disagree in shape")
+    if not (_dims(w_gate_scale, 3) == _dims(w_up_scale, 3) == (E, I // 128, H // 128)
+            and _dims(w_down_scale, 3) == (E, H // 128, I // 128)):
+        raise ValueError("a scale tensor's shape does not match")
+    o, p, f = _grouping(order, pos, offsets, T * k, E)
+    _check(lib().fp8q_moe_ffn(_ptr(x), _ptr(weights), o, p, f, _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up),
+                             _ptr(w_up_scale), _ptr(w_down), _ptr(w_down_scale), _ptr(out), _optr(workspace),
+                             _nbytes(workspace), T, E, k, H, I, variant, _stream(stream)))
 
 
 def fp8q_default_select_params(cu_count: int) -> SelectParams:

@@ -525,10 +525,76 @@ fp8q_status check_ffn_shape(const char* fn, uint32_t M, uint32_t H, uint32_t I) 
   return FP8Q_OK;
 }
 
+// ---- experts ----
+fp8q_status check_groups(const char* fn, uint32_t E) {
+  if (E == 0 || E > kMaxExperts)
+    return fail(FP8Q_ERR_SHAPE, "%s: %u groups (1..%u)", fn, E, kMaxExperts);
+  return FP8Q_OK;
+}
+
+fp8q_status check_slots(const char* fn, uint32_t T, uint32_t top_k) {
+  if (top_k == 0 || top_k > kMaxTopK) return fail(FP8Q_ERR_SHAPE, "%s: top_k=%u (1..%u)", fn, top_k, kMaxTopK);
+  if ((uint64_t)T * top_k > 0x7FFFFFFFull)
+    return fail(FP8Q_ERR_SHAPE, "%s: T*top_k=%llu exceeds 2^31-1", fn, (unsigned long long)T * top_k);
+  return FP8Q_OK;
+}
+
+// A grouped product's rows, columns and depth: a [a_rows,K], out [R,N].
+fp8q_status check_grouped(const char* fn, uint32_t a_rows, uint32_t R, uint32_t N, uint32_t K) {
+  fp8q_status st = check_mk(fn, a_rows, K);
+  if (st != FP8Q_OK) return st;
+  st = check_n(fn, R, N, K);
+  if (st != FP8Q_OK) return st;
+  if ((uint64_t)m_pad16(a_rows) * K > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: ceil16(rows)*K exceeds 2^32-1", fn);
+  // the largest grid: one row tile of 16 a row at most, one column tile of 16
+  if ((uint64_t)R * (N / 16) > 0x7FFFFFFFull)
+    return fail(FP8Q_ERR_SHAPE, "%s: %u rows of %u columns are too many tiles", fn, R, N);
+  return FP8Q_OK;
+}
+
+fp8q_status check_workspace(const char* fn, const void* workspace, size_t have, uint64_t need) {
+  if (need == 0) return FP8Q_OK;
+  REQUIRE_PTR(workspace);
+  if (have < need)
+    return fail(FP8Q_ERR_SHAPE, "%s: workspace of %llu bytes, %llu needed", fn, (unsigned long long)have,
+                (unsigned long long)need);
+  return FP8Q_OK;
+}
+
+// fp8q_moe_ffn's automatic choice: the fused gate/up kernel (128-row tiles)
+// from this mean of rows an expert.
+constexpr uint32_t kMoeFusedMinRows = 48;
+
+int moe_ffn_auto(uint32_t T, uint32_t E, uint32_t top_k) {
+  return (uint64_t)T * top_k >= (uint64_t)kMoeFusedMinRows * E ? 1 : 2;
+}
+
+// Workspace of fp8q_moe_ffn: regions in this order, each on a 256-byte boundary.
+struct MoeWorkspace {
+  uint64_t xq, xs, hq, hs, g, u, y, total;
+};
+
+MoeWorkspace moe_workspace(uint32_t T, uint32_t top_k, uint32_t H, uint32_t I, int variant) {
+  const uint64_t R = (uint64_t)T * top_k, Rp = (R + 15) / 16 * 16;
+  MoeWorkspace w;
+  uint64_t o = 0;
+  w.xq = o; o = align256(o + (uint64_t)T * H);
+  w.xs = o; o = align256(o + (uint64_t)m_pad16(T) * (H / kGroup) * 4);
+  w.hq = o; o = align256(o + R * I);
+  w.hs = o; o = align256(o + Rp * (I / kGroup) * 4);
+  w.g = w.u = 0;
+  if (variant == 2) {
+    w.g = o; o = align256(o + R * I * 2);
+    w.u = o; o = align256(o + R * I * 2);
+  }
+  w.y = o; o = align256(o + R * H * 2);
+  w.total = o;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
-
 uint32_t fp8q_m_pad(uint32_t m) { return m_pad16(m); }
 
 const char* fp8q_last_error(void) { return g_err; }
@@ -1052,6 +1118,195 @@ fp8q_status fp8q_ffn(const uint16_t* x_bf16, const uint8_t* w_gate, const float*
   }
   if (st != FP8Q_OK) return st;
   return run_gemm_ws(fn, hq, hs_km, w_down, w_down_scale, out_bf16, part, M, H, I, stream);
+}
+
+fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int32_t* ids, float* weights,
+                           int32_t* order, int32_t* pos, int32_t* offsets, void* workspace,
+                           size_t workspace_bytes, uint32_t T, uint32_t E, uint32_t top_k,
+                           int renormalize, hipStream_t stream) {
+  const char* fn = "fp8q_moe_route";
+  if (logits_bf16 < 0 || logits_bf16 > 1 || renormalize < 0 || renormalize > 1)
+    return fail(FP8Q_ERR_VARIANT, "%s: logits_bf16=%d, renormalize=%d (0 or 1)", fn, logits_bf16, renormalize);
+  fp8q_status st = check_groups(fn, E);
+  if (st != FP8Q_OK) return st;
+  st = check_slots(fn, T, top_k);
+  if (st != FP8Q_OK) return st;
+  if (top_k > E) return fail(FP8Q_ERR_SHAPE, "%s: top_k=%u of %u experts", fn, top_k, E);
+  if ((uint64_t)T * E > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: T*E exceeds 2^32-1", fn);
+  REQUIRE_PTR(offsets);
+  if (T > 0) {
+    REQUIRE_PTR(logits);
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(weights);
+    REQUIRE_PTR(order);
+    REQUIRE_PTR(pos);
+  }
+  st = check_workspace(fn, workspace, workspace_bytes, route_workspace_bytes(T, E));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_route(logits, logits_bf16 != 0, ids, weights, order, pos, offsets, workspace,
+                                   T, E, top_k, renormalize != 0, stream));
+}
+
+size_t fp8q_moe_route_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k) {
+  if (E == 0 || E > kMaxExperts || top_k == 0 || top_k > kMaxTopK) return 0;
+  return (size_t)route_workspace_bytes(T, E);
+}
+
+fp8q_status fp8q_group_rows(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* offsets,
+                            void* workspace, size_t workspace_bytes, uint32_t n, uint32_t groups,
+                            hipStream_t stream) {
+  const char* fn = "fp8q_group_rows";
+  fp8q_status st = check_groups(fn, groups);
+  if (st != FP8Q_OK) return st;
+  st = check_slots(fn, n, 1);
+  if (st != FP8Q_OK) return st;
+  REQUIRE_PTR(offsets);
+  if (n > 0) {
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(order);
+    REQUIRE_PTR(pos);
+  }
+  st = check_workspace(fn, workspace, workspace_bytes, group_workspace_bytes(n, groups));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_group_rows(ids, order, pos, offsets, workspace, n, groups, stream));
+}
+
+size_t fp8q_group_rows_workspace_bytes(uint32_t n, uint32_t groups) {
+  if (groups == 0 || groups > kMaxExperts) return 0;
+  return (size_t)group_workspace_bytes(n, groups);
+}
+
+fp8q_status fp8q_moe_combine(const uint16_t* y_bf16, const float* weights, const int32_t* pos,
+                             const int32_t* offsets, uint16_t* out_bf16, uint32_t T, uint32_t E,
+                             uint32_t top_k, uint32_t H, hipStream_t stream) {
+  const char* fn = "fp8q_moe_combine";
+  fp8q_status st = check_groups(fn, E);
+  if (st != FP8Q_OK) return st;
+  st = check_slots(fn, T, top_k);
+  if (st != FP8Q_OK) return st;
+  if (H == 0 || H % 8 != 0) return fail(FP8Q_ERR_SHAPE, "%s: H=%u is not a positive multiple of 8", fn, H);
+  if ((uint64_t)T * top_k * H > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: T*top_k*H exceeds 2^32-1", fn);
+  REQUIRE_PTR(y_bf16);
+  REQUIRE_PTR(weights);
+  REQUIRE_PTR(pos);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(out_bf16);
+  if (T == 0) return ok();
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_combine(y_bf16, weights, pos, offsets, out_bf16, T, E, top_k, H, stream));
+}
+
+int fp8q_gemm_grouped_select(uint32_t R, uint32_t E) { return E == 0 ? 0 : group_gemm_auto(R, E); }
+
+fp8q_status fp8q_gemm_grouped(const uint8_t* a_e4m3, const float* a_scale_km, const uint8_t* w_e4m3,
+                              const float* w_scale, const int32_t* offsets, const int32_t* order,
+                              uint16_t* out_bf16, uint32_t a_rows, uint32_t R, uint32_t E, uint32_t top_k,
+                              uint32_t N, uint32_t K, int kernel, hipStream_t stream) {
+  const char* fn = "fp8q_gemm_grouped";
+  if (kernel < 0 || kernel > 3) return fail(FP8Q_ERR_VARIANT, "%s: kernel %d out of range", fn, kernel);
+  fp8q_status st = check_groups(fn, E);
+  if (st != FP8Q_OK) return st;
+  st = check_slots(fn, R, 1);
+  if (st != FP8Q_OK) return st;
+  if (top_k == 0 || top_k > kMaxTopK) return fail(FP8Q_ERR_SHAPE, "%s: top_k=%u (1..%u)", fn, top_k, kMaxTopK);
+  st = check_grouped(fn, a_rows, R, N, K);
+  if (st != FP8Q_OK) return st;
+  if (order == nullptr ? a_rows != R : (uint64_t)a_rows * top_k != R)
+    return fail(FP8Q_ERR_SHAPE, "%s: %u activation rows for %u sorted rows of top_k=%u", fn, a_rows, R, top_k);
+  REQUIRE_PTR(a_e4m3);
+  REQUIRE_PTR(a_scale_km);
+  REQUIRE_PTR(w_e4m3);
+  REQUIRE_PTR(w_scale);
+  REQUIRE_PTR(offsets);
+  if (order != nullptr && !aligned16(order)) return fail(FP8Q_ERR_ALIGN, "%s: order is not 16-byte aligned", fn);
+  REQUIRE_PTR(out_bf16);
+  if (R == 0) return ok();
+  uint32_t cus = 0;
+  st = check_device(fn, &cus);
+  if (st != FP8Q_OK) return st;
+  if (kernel == 0) kernel = group_gemm_auto(R, E);
+  return launched(fn, launch_gemm_grouped(a_e4m3, a_scale_km, w_e4m3, w_scale, out_bf16, offsets, order,
+                                          top_k, a_rows, R, E, N, K, cus, kernel, stream));
+}
+
+int fp8q_moe_ffn_select(uint32_t T, uint32_t E, uint32_t top_k) {
+  return E == 0 || E > kMaxExperts || top_k == 0 || top_k > kMaxTopK ? -1 : moe_ffn_auto(T, E, top_k);
+}
+
+size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k, uint32_t H, uint32_t I,
+                                    int variant) {
+  if (variant < 0 || variant > 2 || H == 0 || H % kGroup != 0 || I == 0 || I % kGroup != 0 || E == 0 ||
+      E > kMaxExperts || top_k == 0 || top_k > kMaxTopK)
+    return 0;
+  if (variant == 0) variant = moe_ffn_auto(T, E, top_k);
+  return (size_t)moe_workspace(T, top_k, H, I, variant).total;
+}
+
+fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int32_t* order,
+                         const int32_t* pos, const int32_t* offsets, const uint8_t* w_gate,
+                         const float* w_gate_scale, const uint8_t* w_up, const float* w_up_scale,
+                         const uint8_t* w_down, const float* w_down_scale, uint16_t* out_bf16,
+                         void* workspace, size_t workspace_bytes, uint32_t T, uint32_t E, uint32_t top_k,
+                         uint32_t H, uint32_t I, int variant, hipStream_t stream) {
+  const char* fn = "fp8q_moe_ffn";
+  if (variant < 0 || variant > 2) return fail(FP8Q_ERR_VARIANT, "%s: variant %d out of range", fn, variant);
+  fp8q_status st = check_groups(fn, E);
+  if (st != FP8Q_OK) return st;
+  st = check_slots(fn, T, top_k);
+  if (st != FP8Q_OK) return st;
+  if (H == 0 || H % kGroup != 0) return fail(FP8Q_ERR_SHAPE, "%s: H=%u is not a positive multiple of 128", fn, H);
+  const uint32_t R = T * top_k;
+  st = check_grouped(fn, T, R, I, H);
+  if (st != FP8Q_OK) return st;
+  st = check_grouped(fn, R, R, H, I);
+  if (st != FP8Q_OK) return st;
+  REQUIRE_PTR(x_bf16);
+  REQUIRE_PTR(weights);
+  REQUIRE_PTR(order);
+  REQUIRE_PTR(pos);
+  REQUIRE_PTR(offsets);
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_gate_scale);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(w_up_scale);
+  REQUIRE_PTR(w_down);
+  REQUIRE_PTR(w_down_scale);
+  REQUIRE_PTR(out_bf16);
+  if (T == 0) return ok();
+  if (variant == 0) variant = moe_ffn_auto(T, E, top_k);
+  const MoeWorkspace w = moe_workspace(T, top_k, H, I, variant);
+  st = check_workspace(fn, workspace, workspace_bytes, w.total);
+  if (st != FP8Q_OK) return st;
+  uint32_t cus = 0;
+  st = check_device(fn, &cus);
+  if (st != FP8Q_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t *xq = ws + w.xq, *hq = ws + w.hq;
+  float *xs = reinterpret_cast<float*>(ws + w.xs), *hs = reinterpret_cast<float*>(ws + w.hs);
+  uint16_t* y = reinterpret_cast<uint16_t*>(ws + w.y);
+  const int kernel = group_gemm_auto(R, E);
+  // x is quantized once a token, whatever the number of its experts
+  st = run_quant(fn, x_bf16, xq, nullptr, xs, T, H, 0, stream);
+  if (st != FP8Q_OK) return st;
+  if (variant == 1) {
+    st = launched(fn, launch_group_ffn_gate_up(xq, xs, w_gate, w_gate_scale, w_up, w_up_scale, hq, hs, offsets,
+                                               order, top_k, T, R, E, H, I, stream));
+  } else {
+    uint16_t *g = reinterpret_cast<uint16_t*>(ws + w.g), *u = reinterpret_cast<uint16_t*>(ws + w.u);
+    st = launched(fn, launch_group_gate_and_up(xq, xs, w_gate, w_gate_scale, w_up, w_up_scale, g, u, offsets,
+                                               order, top_k, T, R, E, H, I, cus, kernel, stream));
+    if (st == FP8Q_OK) st = launched(fn, launch_silu_mul_quant(g, u, hq, hs, R, I, stream));
+  }
+  if (st != FP8Q_OK) return st;
+  st = launched(fn, launch_gemm_grouped(hq, hs, w_down, w_down_scale, y, offsets, nullptr, 1, R, R, E, H, I, cus,
+                                        kernel, stream));
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_combine(y, weights, pos, offsets, out_bf16, T, E, top_k, H, stream));
 }
 
 }  // extern "C"

@@ -139,6 +139,51 @@ hipError_t launch_ffn_gate_up(const uint8_t* x, const float* x_s_km, const uint8
                               uint8_t* hq, float* hs_km, uint32_t M, uint32_t H, uint32_t I,
                               hipStream_t s);
 
+// ---- expert routing (route.hip) ----
+constexpr uint32_t kMaxExperts = 512, kMaxTopK = 32;
+// Top-k choice of each token with softmax weights, and the grouping of the
+// slots t * top_k + j by expert: order (stable; slots without an expert last),
+// pos (its inverse), offsets [E + 1].  workspace: route_workspace_bytes.
+uint64_t route_workspace_bytes(uint32_t T, uint32_t E);
+hipError_t launch_route(const void* logits, bool bf16, int32_t* ids, float* weights, int32_t* order,
+                        int32_t* pos, int32_t* offsets, void* workspace, uint32_t T, uint32_t E,
+                        uint32_t top_k, bool renorm, hipStream_t s);
+// The grouping alone, of n given ids (outside 0 .. groups-1: no group).
+uint64_t group_workspace_bytes(uint32_t n, uint32_t groups);
+hipError_t launch_group_rows(const int32_t* ids, int32_t* order, int32_t* pos, int32_t* offsets,
+                             void* workspace, uint32_t n, uint32_t groups, hipStream_t s);
+// out[t] = bf16(sum_j weights[t][j] * y[pos[t][j]]), H % 8 == 0.
+hipError_t launch_combine(const uint16_t* y, const float* weights, const int32_t* pos,
+                          const int32_t* offsets, uint16_t* out, uint32_t T, uint32_t E,
+                          uint32_t top_k, uint32_t H, hipStream_t s);
+
+// ---- products grouped by expert (grouped.hip) ----
+// Sorted rows p of expert e (offsets[e] <= p < offsets[e + 1]) read activation
+// row order[p] / per_row (order NULL: row p) of a_rows; weights w [E, N, K]
+// with block scales [E, N/128, K/128]; out [R, N].  Kernel ids: 1 weight
+// streaming, 2 128 x 128 tiles, 3 ping-pong 256 x 128 tiles; group_gemm_auto
+// picks by the mean rows an expert.
+int group_gemm_auto(uint32_t R, uint32_t E);
+hipError_t launch_gemm_grouped(const uint8_t* a, const float* a_s_km, const uint8_t* w,
+                               const float* w_s, uint16_t* out, const int32_t* offsets,
+                               const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
+                               uint32_t E, uint32_t N, uint32_t K, uint32_t cus, int kernel,
+                               hipStream_t s);
+// Gate and up of the same rows in one launch, bf16 out [R, I] each.
+hipError_t launch_group_gate_and_up(const uint8_t* x, const float* x_s_km, const uint8_t* w_gate,
+                                    const float* ws_gate, const uint8_t* w_up, const float* ws_up,
+                                    uint16_t* gate, uint16_t* up, const int32_t* offsets,
+                                    const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
+                                    uint32_t E, uint32_t H, uint32_t I, uint32_t cus, int kernel,
+                                    hipStream_t s);
+// Gate, up, SiLU and requantization in one kernel: codes hq [R, I] and K-major
+// scales hs_km [I/128, ceil16(R)] (rows of no expert are left as they are).
+hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const uint8_t* w_gate,
+                                    const float* ws_gate, const uint8_t* w_up, const float* ws_up,
+                                    uint8_t* hq, float* hs_km, const int32_t* offsets,
+                                    const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
+                                    uint32_t E, uint32_t H, uint32_t I, hipStream_t s);
+
 // Clock stamps (measurement support): n one-wave workgroups each write
 // {XCD id, HW_ID, shader clock counter, 100 MHz counter} to dst[4*i .. 4*i+3].
 hipError_t launch_clock_stamp(unsigned long long* dst, uint32_t n, hipStream_t s);

@@ -138,7 +138,7 @@ __global__ __launch_bounds__(512) void gemm_pp_kernel(
 template <int STAGES, bool ROW, bool FFN = false>
 hipError_t launch_pp_cfg(const uint8_t* a, const float* a_s_km, const uint8_t* w, const float* w_s,
                          uint16_t* out, uint32_t M, uint32_t N, uint32_t K, hipStream_t s,
-                         FfnArgs ffn = FfnArgs{nullptr, nullptr, nullptr, nullptr}) {
+                         FfnArgs ffn = FfnArgs{nullptr, nullptr, nullptr, nullptr, 0}) {
   using C = PpCfg<STAGES, ROW, FFN>;
   constexpr uint32_t BNO = FFN ? kGroup : C::BN;  // output columns per tile
   if (N % BNO != 0) return hipErrorInvalidValue;
@@ -1187,7 +1187,7 @@ hipError_t launch_ffn_gate_up(const uint8_t* x, const float* x_s_km, const uint8
                               uint8_t* hq, float* hs_km, uint32_t M, uint32_t H, uint32_t I,
                               hipStream_t s) {
   return launch_pp_cfg<3, false, true>(x, x_s_km, w_gate, ws_gate, nullptr, M, I, H, s,
-                                       FfnArgs{w_up, ws_up, hq, hs_km});
+                                       FfnArgs{w_up, ws_up, hq, hs_km, m_pad16(M)});
 }
 
 hipError_t launch_splitk_128(const uint8_t* a, const float* a_s_km, const uint8_t* w,

@@ -62,12 +62,13 @@ struct PpCfg {
 
 // Second weight operand and outputs of the FFN mode: W/Ws are the gate
 // weights and their block scales, these the up weights and scales, the
-// intermediate's codes [M,N] and its K-major scales [N/128, Mp].
+// intermediate's codes [M,N] and its K-major scales [N/128, Mp_h].
 struct FfnArgs {
   const uint8_t* w_up;
   const float* ws_up;
   uint8_t* hq;
   float* hs;
+  uint32_t Mp_h;  // row stride of hs
 };
 
 // FFN-mode epilogue, after the main loop (all direct loads of this wave
@@ -93,8 +94,7 @@ template <int TM, int TN>
 __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* smem,
                                              const FfnArgs& ffn, uint32_t wave, uint32_t lane,
                                              uint32_t mrow0, uint32_t ncol0, uint32_t nb,
-                                             uint32_t M, uint32_t N, uint32_t Mp,
-                                             uint32_t pad_end) {
+                                             uint32_t M, uint32_t N, uint32_t pad_end) {
   static_assert(TM == 4 && TN == 4, "64x64 wave tile");
   uint32_t* park = reinterpret_cast<uint32_t*>(smem);                // [8][4][64][4] u32: 32 KB
   uint32_t* rmax = reinterpret_cast<uint32_t*>(smem + 32 * 1024);    // [8][2][16] u32
@@ -174,7 +174,7 @@ __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* 
         *reinterpret_cast<uint32_t*>(ffn.hq + (uint64_t)m * N + ncol0 + tn * 16 + 4 * q4) =
             encode4(q + 4 * tn);
     }
-    if ((wave & 1) == 0 && q4 == 0 && m < pad_end) ffn.hs[(uint64_t)nb * Mp + m] = (m < M) ? sc : 0.0f;
+    if ((wave & 1) == 0 && q4 == 0 && m < pad_end) ffn.hs[(uint64_t)nb * ffn.Mp_h + m] = (m < M) ? sc : 0.0f;
   }
 }
 
@@ -440,7 +440,7 @@ __device__ __forceinline__ void gemm_pp_body(
   for (int j = NP - kPromoteDist; j < NP; ++j) acc[j / TN][j % TN] += p[j & 3] * sc_tail;
   if constexpr (FFN) {
     ffn_epilogue<TM, TN>(acc, smem, ffn, wave, lane, m0 + wm * C::WM, n0 + (wn & 1) * C::WN, nb,
-                         M, N, Mp, rows.pad_end(Mp));
+                         M, N, rows.pad_end(Mp));
     return;
   }
   if constexpr (ROW) {
