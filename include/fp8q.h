@@ -671,6 +671,39 @@ int fp8q_moe_ffn_select(uint32_t T, uint32_t E, uint32_t top_k);
 size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k,
                                     uint32_t H, uint32_t I, int variant);
 
+/* -------------------------- low-rank adapters beside the projection */
+
+/* fp8q_proj with a low-rank adapter of each row's own, many in one call (rows of
+ * different requests share the projection's weights):
+ *   out[m] = bf16_rne( proj(quant(x))[m] + lora_scale[a] * (x[m] . A[a]^T) . B[a]^T )
+ *   a = adapter_ids[m]; rows whose id lies outside 0..adapters-1 are the
+ *   projection alone
+ * with x in bf16 for the adapter, the sums in fp32 (x . A^T is kept in fp32 and
+ * enters the second product as two bf16 terms, about 16 bits), one rounding.
+ *   lora_a       [adapters,rank,K] bf16, lora_b [adapters,N,rank] bf16,
+ *                lora_scale [adapters] fp32, adapter_ids [M] int32, read only;
+ *                an adapter of smaller rank is padded with zeros
+ *   workspace    fp8q_proj_lora_workspace_bytes(M, N, K, rank) bytes; contents
+ *                undefined on return; calls in flight must not share it
+ *   the other arguments as for fp8q_proj
+ * 8 <= rank <= FP8Q_MAX_LORA_RANK, rank % 8 == 0, adapters >= 1; element counts
+ * of one adapter's A and B below 2^32 (the stacks may be larger).  Rows of one
+ * request next to one another read its adapter once a row tile; any order
+ * is right.  Errors: FP8Q_ERR_SHAPE for those and a short workspace, otherwise
+ * as fp8q_proj. */
+#define FP8Q_MAX_LORA_RANK 128
+fp8q_status fp8q_proj_lora(const uint16_t *x_bf16, const uint8_t *w_e4m3,
+                           const float *w_scale, const uint16_t *lora_a,
+                           const uint16_t *lora_b, const float *lora_scale,
+                           const int32_t *adapter_ids, uint16_t *out_bf16,
+                           uint8_t *act_q_scratch, float *act_scale_scratch,
+                           float *act_scale_km_scratch, void *workspace,
+                           size_t workspace_bytes, uint32_t M, uint32_t N,
+                           uint32_t K, uint32_t adapters, uint32_t rank,
+                           hipStream_t stream);
+size_t fp8q_proj_lora_workspace_bytes(uint32_t M, uint32_t N, uint32_t K,
+                                      uint32_t rank);
+
 /* ------------------------------------------------- measurement support */
 
 /* Clock stamp, for measuring the sustained shader clock over a region of a

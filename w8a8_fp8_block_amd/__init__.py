@@ -24,6 +24,8 @@ Names match the C entry points:
   fp8q_moe_ffn(x, weights, order, pos, offsets, w_gate, w_gate_scale, w_up, w_up_scale,
                w_down, w_down_scale, out, workspace, variant=0)
   fp8q_moe_combine(y, weights, pos, offsets, out)
+  fp8q_proj_lora(x, w, w_scale, lora_a, lora_b, lora_scale, adapter_ids, out, act_q, act_scale,
+                 act_scale_km, workspace)
   fp8q_m_pad(m), fp8q_quant_select(M, K, cu_count), ...
 
 Dtypes: bf16 tensors may be torch.bfloat16 or torch.uint16/int16 views;
@@ -109,6 +111,8 @@ _SIGS = {
     "fp8q_gemm_grouped_select": (_I, [_U, _U]),
     "fp8q_moe_ffn": (_I, [_P] * 13 + [_SZ, _U, _U, _U, _U, _U, _I, _P]),
     "fp8q_moe_ffn_select": (_I, [_U, _U, _U]),
+    "fp8q_proj_lora": (_I, [_P] * 12 + [_SZ, _U, _U, _U, _U, _U, _P]),
+    "fp8q_proj_lora_workspace_bytes": (_SZ, [_U, _U, _U, _U]),
     "fp8q_moe_ffn_workspace_bytes": (_SZ, [_U, _U, _U, _U, _U, _I]),
 }
 
@@ -522,6 +526,33 @@ def fp8q_moe_ffn(x, weights, order, pos, offsets, w_gate, w_gate_scale, w_up, w_
     _check(lib().fp8q_moe_ffn(_ptr(x), _ptr(weights), o, p, f, _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up),
                              _ptr(w_up_scale), _ptr(w_down), _ptr(w_down_scale), _ptr(out), _optr(workspace),
                              _nbytes(workspace), T, E, k, H, I, variant, _stream(stream)))
+
+
+def fp8q_proj_lora_workspace_bytes(M: int, N: int, K: int, rank: int) -> int:
+    return int(lib().fp8q_proj_lora_workspace_bytes(M, N, K, rank))
+
+
+def fp8q_proj_lora(x, w, w_scale, lora_a, lora_b, lora_scale, adapter_ids, out, act_q, act_scale,
+                   act_scale_km, workspace, stream=None):
+    """fp8q_proj plus each row's low-rank adapter: out[m] = proj(x)[m] +
+    lora_scale[a] * (x[m] . lora_a[a]^T) . lora_b[a]^T, a = adapter_ids[m]
+    (outside 0..n-1: none).  lora_a [n,rank,K], lora_b [n,N,rank] bf16,
+    lora_scale [n] float32, adapter_ids [M] int32; workspace: a device byte
+    tensor of fp8q_proj_lora_workspace_bytes(M, N, K, rank)."""
+    import torch
+    M, K = _dims(x, 2)
+    N, K2 = _dims(w, 2)
+    n, R, K3 = _dims(lora_a, 3)
+    if K2 != K or K3 != K or _dims(lora_b, 3) != (n, N, R) or _dims(out, 2) != (M, N):
+        raise ValueError("x, w, the adapters and out disagree in shape")
+    if lora_scale.numel() != n or adapter_ids.numel() != M:
+        raise ValueError("lora_scale or adapter_ids has the wrong length")
+    if lora_scale.dtype != torch.float32:
+        raise TypeError(f"lora_scale must be float32, got {lora_scale.dtype}")
+    _check(lib().fp8q_proj_lora(_ptr(x), _ptr(w), _ptr(w_scale), _ptr(lora_a), _ptr(lora_b), _ptr(lora_scale),
+                               _int32(adapter_ids, "adapter_ids"), _ptr(out), _ptr(act_q), _ptr(act_scale),
+                               _ptr(act_scale_km), _optr(workspace), _nbytes(workspace), M, N, K, n, R,
+                               _stream(stream)))
 
 
 def fp8q_default_select_params(cu_count: int) -> SelectParams:

@@ -1309,4 +1309,62 @@ fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int
   return launched(fn, launch_combine(y, weights, pos, offsets, out_bf16, T, E, top_k, H, stream));
 }
 
+size_t fp8q_proj_lora_workspace_bytes(uint32_t M, uint32_t N, uint32_t K, uint32_t rank) {
+  if (N == 0 || N % kGroup != 0 || K == 0 || K % kGroup != 0 || rank == 0 || rank > kMaxLoraRank || rank % 8 != 0)
+    return 0;
+  return (size_t)(align256(lora_workspace_bytes(M, K, rank)) +
+                  splitk_workspace(M, N, splitk_auto(M, N, K, current_cus())));
+}
+
+fp8q_status fp8q_proj_lora(const uint16_t* x_bf16, const uint8_t* w_e4m3, const float* w_scale,
+                           const uint16_t* lora_a, const uint16_t* lora_b, const float* lora_scale,
+                           const int32_t* adapter_ids, uint16_t* out_bf16, uint8_t* act_q_scratch,
+                           float* act_scale_scratch, float* act_scale_km_scratch, void* workspace,
+                           size_t workspace_bytes, uint32_t M, uint32_t N, uint32_t K, uint32_t adapters,
+                           uint32_t rank, hipStream_t stream) {
+  const char* fn = "fp8q_proj_lora";
+  fp8q_status st = check_mk(fn, M, K);
+  if (st != FP8Q_OK) return st;
+  st = check_n(fn, M, N, K);
+  if (st != FP8Q_OK) return st;
+  if ((uint64_t)m_pad16(M) * K > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: Mp*K exceeds 2^32-1", fn);
+  if (rank == 0 || rank > kMaxLoraRank || rank % 8 != 0)
+    return fail(FP8Q_ERR_SHAPE, "%s: rank=%u (a multiple of 8 up to %u)", fn, rank, kMaxLoraRank);
+  if (adapters == 0) return fail(FP8Q_ERR_SHAPE, "%s: no adapters", fn);
+  if ((uint64_t)rank * K > kMaxElems || (uint64_t)rank * N > kMaxElems)
+    return fail(FP8Q_ERR_SHAPE, "%s: rank*K or rank*N exceeds 2^32-1", fn);
+  REQUIRE_PTR(x_bf16);
+  REQUIRE_PTR(w_e4m3);
+  REQUIRE_PTR(w_scale);
+  REQUIRE_PTR(lora_a);
+  REQUIRE_PTR(lora_b);
+  REQUIRE_PTR(lora_scale);
+  REQUIRE_PTR(adapter_ids);
+  REQUIRE_PTR(out_bf16);
+  REQUIRE_PTR(act_q_scratch);
+  REQUIRE_PTR(act_scale_scratch);
+  REQUIRE_PTR(act_scale_km_scratch);
+  if (M == 0) return ok();
+  const uint32_t cus = current_cus();  // as the size query
+  const uint32_t splits = splitk_auto(M, N, K, cus);
+  const uint64_t vbytes = align256(lora_workspace_bytes(M, K, rank));
+  st = check_workspace(fn, workspace, workspace_bytes, vbytes + splitk_workspace(M, N, splits));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  if ((uint64_t)M * (K / kGroup) <= kFusedKmajorMaxGroups) {
+    st = run_quant(fn, x_bf16, act_q_scratch, act_scale_scratch, act_scale_km_scratch, M, K, 0, stream);
+  } else {
+    st = run_quant(fn, x_bf16, act_q_scratch, act_scale_scratch, nullptr, M, K, 0, stream);
+    if (st == FP8Q_OK) st = launched(fn, launch_relayout(act_scale_scratch, act_scale_km_scratch, M, K, stream));
+  }
+  if (st != FP8Q_OK) return st;
+  st = launched(fn, launch_lora_shrink(x_bf16, lora_a, adapter_ids, workspace, M, K, adapters, rank, stream));
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_lora_gemm(act_q_scratch, act_scale_km_scratch, w_e4m3, w_scale, out_bf16, workspace,
+                                       reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + vbytes), lora_b,
+                                       lora_scale, adapter_ids, M, N, K, adapters, rank, cus,
+                                       gemm_auto_kernel(M, N, cus), splits, stream));
+}
+
 }  // extern "C"

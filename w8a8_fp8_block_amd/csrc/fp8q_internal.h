@@ -77,6 +77,9 @@ hipError_t launch_splitk_128(const uint8_t* a, const float* a_s_km, const uint8_
                              const float* w_s, uint16_t* out, float* part, uint32_t M,
                              uint32_t N, uint32_t K, uint32_t splits, uint32_t cus,
                              hipStream_t s);
+// The reduction alone: out = bf16(sum of part [splits, M, N] in split order).
+hipError_t launch_splitk_reduce(const float* part, uint16_t* out, uint32_t M, uint32_t N,
+                                uint32_t splits, hipStream_t s);
 // Stream-K form of the 256x128 ping-pong kernel (block-scaled weights): cus
 // persistent workgroups (a multiple of 8, at most the device's CUs); whole
 // tiles in data-parallel rounds, the last partial round's tiles cut along K
@@ -183,6 +186,20 @@ hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const
                                     uint8_t* hq, float* hs_km, const int32_t* offsets,
                                     const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
                                     uint32_t E, uint32_t H, uint32_t I, hipStream_t s);
+
+// ---- low-rank adapters beside the projection (lora.hip) ----
+constexpr uint32_t kMaxLoraRank = 128;
+// v = x . A^T of the rows with an adapter, into workspace (lora_workspace_bytes).
+uint64_t lora_workspace_bytes(uint32_t M, uint32_t K, uint32_t rank);
+hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, void* workspace,
+                              uint32_t M, uint32_t K, uint32_t adapters, uint32_t rank, hipStream_t s);
+// The block-scaled GEMM (kernel ids of launch_gemm: 1, 2 or 5; splits >= 2:
+// its split form with part [splits, M, N]) plus scale * v . B^T.
+hipError_t launch_lora_gemm(const uint8_t* a, const float* a_s_km, const uint8_t* w, const float* w_s,
+                            uint16_t* out, const void* workspace, float* part, const uint16_t* lora_b,
+                            const float* lora_scale, const int32_t* ids, uint32_t M, uint32_t N, uint32_t K,
+                            uint32_t adapters, uint32_t rank, uint32_t cus, int kernel, uint32_t splits,
+                            hipStream_t s);
 
 // Clock stamps (measurement support): n one-wave workgroups each write
 // {XCD id, HW_ID, shader clock counter, 100 MHz counter} to dst[4*i .. 4*i+3].

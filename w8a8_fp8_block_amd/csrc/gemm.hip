@@ -19,6 +19,7 @@
 #include <atomic>
 #include <chrono>
 #include "gemm_pp.h"
+#include "gemm_skinny.h"
 
 namespace fp8q {
 namespace {
@@ -114,13 +115,7 @@ hipError_t launch_splitk_128_t(const uint8_t* a, const float* a_s_km, const uint
                      ? launch_splitk_cfg<3>(a, a_s_km, w, w_s, part, M, N, K, splits, s)
                      : launch_splitk_cfg<2>(a, a_s_km, w, w_s, part, M, N, K, splits, s);
   if (e != hipSuccess) return e;
-  const uint64_t quads = (uint64_t)M * N / 4;
-  const uint64_t blocks = (quads + 255) / 256;
-  const uint32_t grid = (uint32_t)(blocks < 4096 ? blocks : 4096);
-  splitk_reduce_kernel<<<dim3(grid), dim3(256), 0, s>>>(reinterpret_cast<const v4f*>(part),
-                                                          reinterpret_cast<uint2*>(out), quads,
-                                                          splits);
-  return hipGetLastError();
+  return launch_splitk_reduce(part, out, M, N, splits, s);
 }
 
 template <int STAGES, bool ROW, bool FFN>
@@ -629,297 +624,21 @@ hipError_t launch_pp_sk_cfg(const uint8_t* a, const float* a_s_km, const uint8_t
   return hipGetLastError();
 }
 
-// ------------------------------------------------------------------------
-// Skinny kernel for decode and small-batch widths.  Rows come in tiles of
-// 16*TM <= 64 (grid dimension y; beyond 64 rows every row tile streams the
-// weights again, mostly from the last-level cache).  The projection is then
-// bound by streaming the weight matrix once, and the weight bytes must be
-// spread evenly over the CUs: with one workgroup per 16 output columns
-// (384 workgroups at N = 6144 on 256 CUs) half the CUs stream twice as much
-// as the others.  So the grid has one workgroup per CU and workgroup w owns
-// the contiguous column range [c0, c0 + cw), cw = N/grid rounded to 4
-// columns, covered by ceil(cw/16) MFMA tiles of 16 columns (the last one
-// partial: its missing weight rows are zero fragments, its missing columns
-// are not stored).  The NWV waves take interleaved K blocks (wave w: blocks
-// w, w+NWV, ...) for all of the workgroup's tiles; each wave issues the loads
-// of U blocks before consuming any, the activation fragments of a block are
-// loaded once for all tiles, and the NWV partial tiles are summed through
-// LDS in wave order.
-// ------------------------------------------------------------------------
-// SPLIT: the K blocks are cut into gridDim.z contiguous ranges; workgroup
-// (w, y, z) sums range z and stores its fp32 partial tile to part[z][M][N],
-// which splitk_reduce_kernel adds in split order (block-scaled weights only).
 template <int TM, int TN, int NWV, int U, bool ROW, bool SPLIT = false>
 __global__ __launch_bounds__(64 * NWV) void gemm_skinny_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t M, uint32_t N, uint32_t K,
     uint32_t Mp, uint32_t units_base, uint32_t units_rem, float* __restrict__ part = nullptr) {
-  static_assert(!(SPLIT && ROW), "split form for block-scaled weights only");
-  // partial sums of the waves (dynamic LDS: NWV*TN*TM KB)
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  v4f(*red)[TN][TM][64] = reinterpret_cast<v4f(*)[TN][TM][64]>(smem);
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = blockIdx.x;
-  // this workgroup's columns, in units of 4
-  const uint32_t c0 = 4 * (w * units_base + min(w, units_rem));
-  const uint32_t c1 = c0 + 4 * (units_base + (w < units_rem ? 1u : 0u));
-  const uint32_t nt = (c1 - c0 + 15) / 16;
-  const uint32_t G = K / kGroup;
-  const uint32_t l16 = lane & 15, kq = 32 * (lane >> 4);  // this lane's byte offset in a K block
-  // operand rows: weight row c0 + 16t + l16 (zero beyond c1), activation row 16tm + l16
-  const uint8_t* wrow[TN];
-  bool wok[TN];
-  uint32_t wsi[TN];  // weight-scale row of this lane's four output columns
-#pragma unroll
-  for (int t = 0; t < TN; ++t) {
-    const uint32_t r = c0 + 16 * t + l16;
-    wok[t] = r < c1;
-    wrow[t] = W + (uint64_t)min(r, N - 1) * K + kq;
-    wsi[t] = min(c0 + 16 * t + 4 * (lane >> 4), N - 1) / kGroup * G;
-  }
-  const uint32_t m0 = blockIdx.y * (16 * TM);  // this workgroup's rows
-  const uint8_t* arow[TM];
-  uint32_t srow[TM];
-#pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const uint32_t m = m0 + tm * 16 + l16;
-    arow[tm] = A + (uint64_t)min(m, M - 1) * K + kq;
-    srow[tm] = min(m, Mp - 1);
-  }
-
-  v4f acc[TN][TM];
-#pragma unroll
-  for (int t = 0; t < TN; ++t)
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) acc[t][tm] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-  // this workgroup's K blocks [kbeg, kend): all of them, or split z's range
-  const uint32_t kbeg = SPLIT ? blockIdx.z * G / gridDim.z : 0;
-  const uint32_t kend = SPLIT ? (blockIdx.z + 1) * G / gridDim.z : G;
-  for (uint32_t kb0 = kbeg + wave; kb0 < kend; kb0 += NWV * U) {
-    v8i wf[U][TN], af[U][TM];
-    float as[U][TM], ws[U][TN];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t k = kb0 + u * NWV;
-      if (k < kend) {
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          if ((uint32_t)t < nt) {
-            if (wok[t]) {
-              const u32x4* wp = reinterpret_cast<const u32x4*>(wrow[t] + (uint64_t)k * kGroup);
-              wf[u][t] = join(__builtin_nontemporal_load(wp), __builtin_nontemporal_load(wp + 1));
-            } else {
-              wf[u][t] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-            }
-            ws[u][t] = ROW ? 1.0f : Ws[wsi[t] + k];
-          }
-        }
-#pragma unroll
-        for (int tm = 0; tm < TM; ++tm) {
-          const u32x4* ap = reinterpret_cast<const u32x4*>(arow[tm] + (uint64_t)k * kGroup);
-          af[u][tm] = join(ap[0], ap[1]);
-          as[u][tm] = As[(uint64_t)k * Mp + srow[tm]];
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (kb0 + u * NWV < kend) {
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          if ((uint32_t)t < nt) {
-#pragma unroll
-            for (int tm = 0; tm < TM; ++tm) {
-              const v4f p = mfma_e4m3_128(wf[u][t], af[u][tm]);
-              acc[t][tm] += p * (as[u][tm] * ws[u][t]);
-            }
-          }
-        }
-      }
-    }
-  }
-
-#pragma unroll
-  for (int t = 0; t < TN; ++t)
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) red[wave][t][tm][lane] = acc[t][tm];
-  __syncthreads();
-  // waves share the final sums: wave v sums and stores tiles (t, tm) with
-  // t*TM + tm = v (mod NWV)
-#pragma unroll
-  for (int j = 0; j < TN * TM; ++j) {
-    const int t = j / TM, tm = j % TM;
-    if ((uint32_t)(j % NWV) == wave && (uint32_t)t < nt) {
-      v4f s = red[0][t][tm][lane];
-#pragma unroll
-      for (int v = 1; v < NWV; ++v) s += red[v][t][tm][lane];
-      const uint32_t m = m0 + tm * 16 + l16;
-      const uint32_t n = c0 + 16 * t + 4 * (lane >> 4);
-      if constexpr (ROW) {
-        if (n < c1) {
-          const float4 r = *reinterpret_cast<const float4*>(Ws + n);
-          s *= v4f{r.x, r.y, r.z, r.w};
-        }
-      }
-      if (m < M && n < c1) {
-        if constexpr (SPLIT)
-          *reinterpret_cast<v4f*>(part + ((uint64_t)blockIdx.z * M + m) * N + n) = s;
-        else
-          *reinterpret_cast<uint2*>(out + (uint64_t)m * N + n) = pack_bf16x4(s);
-      }
-    }
-  }
+  gemm_skinny_body<TM, TN, NWV, U, ROW, SPLIT>(A, As, W, Ws, out, M, N, K, Mp, units_base, units_rem,
+                                               part, NoEpilogue{});
 }
-
-// ------------------------------------------------------------------------
-// Decode-width kernel for the shapes whose per-workgroup weight slice fits
-// in LDS (up to 32 rows, 16*TM <= 32 activation rows, at most 8*GW K
-// blocks).  The projection streams the weight matrix once from HBM, and how
-// the weight bytes are read decides its speed: fragment-layout loads (lane
-// l: 32 bytes of row l%16, gemm_skinny_kernel) touch 16 rows K bytes apart
-// with every instruction, while direct-to-LDS loads of whole 1 KB row pieces,
-// all in flight at once, stream the same bytes about 1.6x faster (N = 6144,
-// K = 5120 on 256 CUs, the weight read alone from HBM: 6.8 us against 10.7
-// us).  Workgroup w owns the contiguous column range [c0, c0 + R) as in
-// gemm_skinny_kernel; it loads the R weight rows into LDS (each row's K bytes
-// contiguous and followed by a 16-byte pad, so that the 16 rows of an MFMA
-// fragment read fall in 16 different bank quads), and, into registers, the
-// activation fragments and the scales of the K blocks its waves take (wave
-// v: blocks v, v+8, ..., every row tile, as gemm_skinny_kernel), all before
-// the first wait.  Then the waves compute their blocks and add the 8 partial
-// tiles in wave order through LDS: the same products as gemm_skinny_kernel,
-// each wave's blocks added in an order rotated by the workgroup index.
-// Measured at N = 6144, K = 5120 (weights from HBM, graph-timed back-to-back
-// launches): 9.5 / 11.0 / 11.7 us at M = 16 / 17 / 25 against 12.6 / 14.0 /
-// 14.8 us for gemm_skinny_kernel.  What remains above the bare weight stream
-// is the activation reads (every workgroup reads all M x K activation bytes
-// through its vector memory unit ahead of its weight loads: 0.7 us at M = 16,
-// 2 us at M = 25) and the products, the reduction and the store after the
-// single wait (about 1.8 us).  Waiting for the weight loads stage by stage,
-// one K slot at a time, was slower: the barriers cost more than the overlap
-// gains.
-// ------------------------------------------------------------------------
-constexpr uint32_t kDecodeMaxRows = 32, kDecodeLds = 150 * 1024;
 
 template <int TM, int GW, bool ROW>
 __global__ __launch_bounds__(512) void gemm_decode_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t M, uint32_t N, uint32_t K,
     uint32_t Mp, uint32_t units_base, uint32_t units_rem) {
-  constexpr int NT = 2;  // 16-column MFMA tiles of the range (R <= 32)
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  const uint32_t lane = threadIdx.x & 63;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t w = blockIdx.x;
-  const uint32_t c0 = 4 * (w * units_base + min(w, units_rem));
-  const uint32_t R = 4 * (units_base + (w < units_rem ? 1u : 0u));  // columns = weight rows
-  const uint32_t G = K / kGroup, rowb = K + 16;
-  const uint32_t l16 = lane & 15, q = lane >> 4;
-
-  // this wave's activation fragments and scales (L2-resident: every
-  // workgroup reads them), and weight scales: issued first, ahead of the
-  // weight stream.  Slot j holds
-  // block wave + 8*((j + w) mod GW): the workgroups start their activation
-  // reads at different blocks, so that the 32 CUs of an XCD do not all ask
-  // its L2 for the same lines at once.
-  const uint32_t nb_last = N / kGroup - 1, rot = w % GW;
-  auto blk = [&](int j) __attribute__((always_inline)) -> uint32_t {
-    const uint32_t jr = (uint32_t)j + rot;
-    return wave + 8 * (jr >= (uint32_t)GW ? jr - GW : jr);
-  };
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, M * K);  // M * K < 2^31 here
-  v8i af[GW][TM];
-  float as[GW][TM], ws[GW][NT];
-#pragma unroll
-  for (int j = 0; j < GW; ++j) {
-    const uint32_t b = min(blk(j), G - 1);  // blocks past G: loaded, not used
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) {
-      // rows past M read at an offset beyond the buffer's range, which gives
-      // zeros without a memory request (not a load under a branch: that
-      // load would be waited for inside the branch, one L2 round trip per
-      // fragment)
-      const uint32_t m = 16 * tm + l16;
-      const uint32_t off = m < M ? m * K + b * kGroup + 32 * q : 0x80000000u;
-      af[j][tm] = join(__builtin_amdgcn_raw_buffer_load_b128(rA, off, 0, 0),
-                       __builtin_amdgcn_raw_buffer_load_b128(rA, off + 16, 0, 0));
-      as[j][tm] = As[(uint64_t)b * Mp + min(m, Mp - 1)];
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-      ws[j][t] = ROW ? 1.0f : Ws[min((c0 + 16 * t + 4 * q) / kGroup, nb_last) * G + b];
-  }
-  // the weight rows: piece p of row r is bytes [1024 p, 1024 p + 1024) (the
-  // last piece of a row may be shorter); loads dealt round robin to the waves
-  const __amdgpu_buffer_rsrc_t rW = make_rsrc(W + (uint64_t)c0 * K, R * K);
-  const uint32_t pieces = (K + 1023) / 1024, lds0 = lds_addr(smem);
-#pragma unroll 1
-  for (uint32_t i = wave; i < R * pieces; i += 8) {
-    const uint32_t r = i / pieces, p = i % pieces;
-    if (1024 * p + 16 * lane < K) dma16_at(rW, r * K + 1024 * p + 16 * lane, 0, lds0 + r * rowb + 1024 * p);
-  }
-  // the loaded registers are pinned here, before the wait: the compiler
-  // would otherwise sink loads into the compute branches below, after the
-  // barrier, and pay a second memory round trip there
-#pragma unroll
-  for (int j = 0; j < GW; ++j) {
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm)  // (16-byte operands: valid on the host pass too)
-      asm volatile("" ::"v"(af[j][tm].lo), "v"(af[j][tm].hi), "v"(as[j][tm]));
-#pragma unroll
-    for (int t = 0; t < NT; ++t) asm volatile("" ::"v"(ws[j][t]));
-  }
-  wait_vmcnt<0>();
-  wg_barrier();
-
-  // all weight fragments of this wave's blocks, then the products, then the
-  // promotions (no LDS or MFMA latency between dependent steps); blocks past
-  // G and rows past R give zero fragments
-  v8i wf[GW][NT];
-#pragma unroll
-  for (int j = 0; j < GW; ++j)
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const uint32_t r = 16 * t + l16, b = min(blk(j), G - 1);
-      const uint8_t* wr = smem + min(r, R - 1) * rowb + b * kGroup + 32 * q;
-      wf[j][t] = join(*reinterpret_cast<const u32x4*>(wr), *reinterpret_cast<const u32x4*>(wr + 16));
-      if (r >= R || blk(j) >= G) wf[j][t] = v8i{0, 0, 0, 0, 0, 0, 0, 0};
-    }
-  v4f acc[NT][TM];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) {
-      v4f p[GW];
-#pragma unroll
-      for (int j = 0; j < GW; ++j) p[j] = mfma_e4m3_128(wf[j][t], af[j][tm]);
-      acc[t][tm] = p[0] * (as[0][tm] * ws[0][t]);
-#pragma unroll
-      for (int j = 1; j < GW; ++j) acc[t][tm] += p[j] * (as[j][tm] * ws[j][t]);
-    }
-  wg_barrier();  // every wave done with the weight rows: LDS takes the partial tiles
-  v4f* red = reinterpret_cast<v4f*>(smem);
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) red[((wave * NT + t) * TM + tm) * 64 + lane] = acc[t][tm];
-  wg_barrier();
-  // waves share the final sums: wave v adds and stores tiles (t, tm) with
-  // t*TM + tm = v (mod 8), the partials in wave order
-  for (uint32_t jt = wave; jt < (uint32_t)(NT * TM); jt += 8) {
-    const uint32_t t = jt / TM, tm = jt % TM;
-    if (16 * t >= R) continue;
-    v4f sum = red[(t * TM + tm) * 64 + lane];
-    for (uint32_t v = 1; v < 8; ++v) sum += red[((v * NT + t) * TM + tm) * 64 + lane];
-    const uint32_t m = 16 * tm + l16, n = c0 + 16 * t + 4 * q;
-    if constexpr (ROW) {
-      if (n < c0 + R) {
-        const float4 rs = *reinterpret_cast<const float4*>(Ws + n);
-        sum *= v4f{rs.x, rs.y, rs.z, rs.w};
-      }
-    }
-    if (m < M && n < c0 + R) *reinterpret_cast<uint2*>(out + (uint64_t)m * N + n) = pack_bf16x4(sum);
-  }
+  gemm_decode_body<TM, GW, ROW>(A, As, W, Ws, out, M, N, K, Mp, units_base, units_rem, NoEpilogue{});
 }
 
 template <int TM, int GW, bool ROW>
@@ -937,20 +656,6 @@ hipError_t launch_decode_cfg(const uint8_t* a, const float* a_s_km, const uint8_
   gemm_decode_kernel<TM, GW, ROW><<<dim3(grid), dim3(512), lds, s>>>(
       a, a_s_km, w, w_s, out, M, N, K, m_pad16(M), base, rem);
   return hipGetLastError();
-}
-
-// Whether the decode kernel takes the shape (its limits: at most 32 rows and
-// kDecodeMaxRows columns a workgroup, 48 K blocks, the slice within
-// kDecodeLds), and then its template arguments and LDS bytes.
-bool decode_plan(uint32_t M, uint32_t K, uint32_t base, uint32_t rem, uint32_t& tm, uint32_t& gw,
-                 uint32_t& lds) {
-  const uint32_t rmax = 4 * (base + (rem ? 1 : 0)), g = (K / kGroup + 7) / 8;
-  const uint64_t l = std::max<uint64_t>((uint64_t)rmax * (K + 16), 8 * 2 * 2 * 64 * 16);
-  if (M > 32 || rmax > kDecodeMaxRows || g > 6 || l > kDecodeLds) return false;
-  tm = M <= 16 ? 1 : 2;
-  gw = g <= 2 ? 2 : g <= 4 ? 4 : g == 5 ? 5 : 6;
-  lds = (uint32_t)l;
-  return true;
 }
 
 // the decode kernel where its shape limits hold (else false)
@@ -976,43 +681,6 @@ bool launch_decode(const uint8_t* a, const float* a_s_km, const uint8_t* w, cons
 #undef FP8Q_DECODE
   return true;
 }
-
-// Registers of a skinny wave: about 4*TN*TM accumulators + 4*TN + 3*TM + 20
-// fixed, 9*TN + 9*TM per K block in flight.
-constexpr int skinny_fixed_regs(int tm, int tn) { return 4 * tn * tm + 4 * tn + 3 * tm + 20; }
-constexpr int skinny_block_regs(int tm, int tn) { return 9 * tn + 9 * tm; }
-// Two waves per SIMD wherever the partial sums of eight fit in 128 KB of LDS,
-// with the K blocks in flight that ~242 registers a wave leave (at least
-// one).  Measured against one wave per SIMD with more blocks in flight (cold
-// caches): TM = 2, TN = 6 (17-32 rows, N = 17408, K = 5120; two blocks
-// against four): 28.9 / 30.1 / 30.8 against 31.4 / 32.5 / 33.2 us at M = 17
-// / 25 / 32; TM = 4, TN = 4 (65-128 rows in 64-row tiles, 64 columns a
-// workgroup; one block against four): 78.4-80.3 against 87.1-90.0 us at
-// N = 5120, K = 17408 and 28.4-30.5 against 32.0-34.2 at N = 6144, K = 5120.
-constexpr bool skinny_two_per_simd(int tm, int tn) { return 8 * tn * tm <= 128; }
-// waves per workgroup: 8 where the rule above holds, else 4 where the
-// partial sums of 4 fit in 128 KB (one wave per SIMD), else 2
-constexpr int skinny_waves(int tm, int tn) {
-  return skinny_two_per_simd(tm, tn) ? 8 : (128 / (tn * tm) >= 4) ? 4 : 2;
-}
-// K blocks in flight per wave: what the register budget leaves (~200 a wave
-// at two waves per SIMD where eight waves' partial sums fit in 64 KB, as
-// first tuned; 242 for the wider configurations; ~440 at one wave per SIMD)
-constexpr int skinny_unroll(int tm, int tn) {
-  const int budget = skinny_waves(tm, tn) != 8 ? 440 : (64 / (tn * tm) >= 8) ? 200 : 242;
-  const int uf = (budget - skinny_fixed_regs(tm, tn)) / skinny_block_regs(tm, tn);
-  return uf > 8 ? 8 : uf < 1 ? 1 : uf;
-}
-// the template arguments the skinny dispatch picks: row tiles TM of 16 rows,
-// column tiles TN of 16 columns.  TM = 3 for 33-48 rows: against TM = 4 it
-// leaves the registers for two K blocks in flight at TN = 4 (one at TM =
-// 4) and loads a quarter fewer activation fragments; back to back over
-// rotating weights, M = 33 / 48: single pass 41.1 / 46.4 -> 36.7 / 42.9 us
-// at N = 5120, K = 17408 (3 splits 33.0 / 35.0 -> 30.3 / 32.8), 34.6 / 35.9
-// -> 31.8 / 33.4 at N = 17408, K = 5120, 16.3 / 17.8 -> 15.2 / 16.9 at
-// N = 6144, K = 5120.
-uint32_t skinny_tm(uint32_t M) { return M <= 16 ? 1 : M <= 32 ? 2 : M <= 48 ? 3 : 4; }
-uint32_t skinny_tn(uint32_t tn) { return tn <= 2 ? 2 : tn <= 4 ? 4 : tn <= 6 ? 6 : 8; }
 
 template <int TM, int TN, bool ROW, bool SPLIT = false>
 hipError_t launch_skinny_tn(const uint8_t* a, const float* a_s_km, const uint8_t* w,
@@ -1072,24 +740,6 @@ hipError_t launch_gemm_tiled_t(const uint8_t* a, const float* a_s_km, const uint
   }
 }
 
-// The skinny path's grid.  Up to 64 rows (one row tile): one workgroup per
-// CU, at most 128 columns each, at least 16.  Beyond (several row tiles,
-// each streaming the weights again): workgroups of 64 columns, so that a row
-// tile re-reads the activations once per 64 columns rather than once per CU
-// (measured at M = 128, N = 5120, K = 17408: 90 us with 64-column
-// workgroups, 108 us with one per CU, 117 us for the ping-pong kernel).
-// Workgroup w owns 4*(base + (w < rem)) columns; tn 16-column tiles at most.
-void skinny_grid(uint32_t M, uint32_t N, uint32_t cu_count, uint32_t& grid, uint32_t& base,
-                 uint32_t& rem, uint32_t& tn) {
-  const uint32_t units = N / 4;
-  grid = max(cu_count, (N + 127) / 128);
-  grid = max(1u, min(grid, N / 16));
-  if (M > 64) grid = N / 64;
-  base = units / grid;
-  rem = units % grid;
-  tn = (4 * (base + (rem ? 1 : 0)) + 15) / 16;
-}
-
 template <bool ROW>
 hipError_t launch_gemm_skinny_t(const uint8_t* a, const float* a_s_km, const uint8_t* w,
                                 const float* w_s, uint16_t* out, uint32_t M, uint32_t N,
@@ -1112,6 +762,17 @@ hipError_t launch_gemm_tiled(const uint8_t* a, const float* a_s_km, const uint8_
                              int cfg, bool row_scaled, hipStream_t s) {
   return row_scaled ? launch_gemm_tiled_t<true>(a, a_s_km, w, w_s, out, M, N, K, cfg, s)
                     : launch_gemm_tiled_t<false>(a, a_s_km, w, w_s, out, M, N, K, cfg, s);
+}
+
+hipError_t launch_splitk_reduce(const float* part, uint16_t* out, uint32_t M, uint32_t N,
+                                uint32_t splits, hipStream_t s) {
+  const uint64_t quads = (uint64_t)M * N / 4;
+  const uint64_t blocks = (quads + 255) / 256;
+  const uint32_t grid = (uint32_t)(blocks < 4096 ? blocks : 4096);
+  splitk_reduce_kernel<<<dim3(grid), dim3(256), 0, s>>>(reinterpret_cast<const v4f*>(part),
+                                                          reinterpret_cast<uint2*>(out), quads,
+                                                          splits);
+  return hipGetLastError();
 }
 
 bool decode_takes(uint32_t M, uint32_t N, uint32_t K, uint32_t cu_count) {
@@ -1159,12 +820,7 @@ bool launch_skinny_split(const uint8_t* a, const float* a_s_km, const uint8_t* w
     default: err = launch_skinny_tm<4, false, true>(a, a_s_km, w, w_s, nullptr, M, N, K, grid, base, rem, tn, s, splits, part); break;
   }
   if (err != hipSuccess) return true;
-  const uint64_t quads = (uint64_t)M * N / 4;
-  const uint64_t blocks = (quads + 255) / 256;
-  const uint32_t rgrid = (uint32_t)(blocks < 4096 ? blocks : 4096);
-  splitk_reduce_kernel<<<dim3(rgrid), dim3(256), 0, s>>>(reinterpret_cast<const v4f*>(part),
-                                                         reinterpret_cast<uint2*>(out), quads, splits);
-  err = hipGetLastError();
+  err = launch_splitk_reduce(part, out, M, N, splits, s);
   return true;
 }
 

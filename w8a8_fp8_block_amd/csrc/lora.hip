@@ -1,0 +1,311 @@
+// The projection with low-rank adapters of many requests on gfx950:
+//   out[m] = bf16( quant(x)[m] . W^T + scale[a] * (x[m] . A[a]^T) . B[a]^T ),
+// a = ids[m], rows without an adapter the projection alone.
+//
+// Two parts: a shrink kernel forms v = x . A^T (fp32, in parts of K), and the
+// projection's own GEMM kernels run with an epilogue that adds scale * v . B^T to
+// their fp32 accumulators (lora.h), so that the sum is rounded once and out is
+// written once.
+#include <atomic>
+
+#include "gemm_pp.h"
+#include "gemm_skinny.h"
+#include "lora.h"
+
+namespace fp8q {
+namespace {
+
+// ------------------------------------------------------------------------
+// Shrink: v[m, r] = sum_k x[m, k] * A[a][r, k] in fp32 from bf16.  A workgroup
+// takes 16 * TM rows and one part of K, its four waves a quarter of the part
+// each; blockIdx.z picks among the rows' distinct adapters (round robin).  Per
+// adapter every row's product is formed with 16x16x32 MFMAs, NR rank tiles of
+// 16, and the rows of that adapter are stored.  Bound by reading A (decode: a
+// few rows an adapter) or x (prompts); both are read in 64-byte pieces of a row
+// by four lanes.
+// ------------------------------------------------------------------------
+template <int TM, int NR>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t* __restrict__ x,
+                                                          const uint16_t* __restrict__ A,
+                                                          float* __restrict__ v, const int32_t* ids,
+                                                          uint32_t M, uint32_t K, uint32_t adapters,
+                                                          uint32_t rank, uint32_t ld, uint32_t parts) {
+  __shared__ v4f red[4][NR][64];
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t l16 = lane & 15, q = lane >> 4;
+  const uint32_t m0 = blockIdx.x * 16 * TM, part = blockIdx.y;
+  const uint32_t chunks = K / 32, piece = part * 4 + wave, pieces = parts * 4;
+  const uint32_t c0 = (uint32_t)((uint64_t)piece * chunks / pieces);
+  const uint32_t c1 = (uint32_t)((uint64_t)(piece + 1) * chunks / pieces);
+  const uint32_t row = m0 + lane;
+  uint32_t id = 0xFFFFFFFFu;
+  if (lane < 16 * TM && row < M) id = (uint32_t)ids[row];
+  if (id >= adapters) id = 0xFFFFFFFFu;
+  uint64_t left = __builtin_amdgcn_ballot_w64(id != 0xFFFFFFFFu);
+  for (uint32_t turn = 0; left; ++turn) {
+    const uint32_t l0 = (uint32_t)__builtin_ctzll(left);
+    const uint32_t ad = (uint32_t)__builtin_amdgcn_readlane((int)id, (int)l0);
+    const uint64_t mine = __builtin_amdgcn_ballot_w64(id == ad);
+    left &= ~mine;
+    if (turn % gridDim.z != blockIdx.z) continue;
+    const uint16_t *xr[TM], *ar[NR];
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      // other rows read the adapter's first row again (cached, not stored)
+      const uint32_t r = 16 * tm + l16;
+      xr[tm] = x + (uint64_t)(m0 + (((mine >> r) & 1) ? r : l0)) * K + 8 * q;
+    }
+#pragma unroll
+    for (int t = 0; t < NR; ++t)
+      ar[t] = A + ((uint64_t)ad * rank + min(16 * t + l16, rank - 1)) * K + 8 * q;
+    v4f acc[TM][NR];
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+      for (int t = 0; t < NR; ++t) acc[tm][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (uint32_t c = c0; c < c1; ++c) {
+      u32x4 xf[TM], af[NR];
+#pragma unroll
+      for (int t = 0; t < NR; ++t) af[t] = *reinterpret_cast<const u32x4*>(ar[t] + c * 32);
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) xf[tm] = *reinterpret_cast<const u32x4*>(xr[tm] + c * 32);
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+        for (int t = 0; t < NR; ++t) acc[tm][t] = mfma_bf16_32(af[t], xf[tm], acc[tm][t]);
+    }
+    // the four waves' sums, one row tile at a time
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      const uint32_t r = 16 * tm + l16;
+      if (((mine >> (16 * tm)) & 0xFFFF) == 0) continue;  // uniform over the workgroup
+#pragma unroll
+      for (int t = 0; t < NR; ++t) red[wave][t][lane] = acc[tm][t];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < (NR + 3) / 4; ++j) {
+        const uint32_t t = 4 * j + wave, k = 16 * t + 4 * q;
+        if (t < (uint32_t)NR && ((mine >> r) & 1) && k < ld) {
+          v4f s = red[0][t][lane];
+#pragma unroll
+          for (int w = 1; w < 4; ++w) s += red[w][t][lane];
+          if (k >= rank) s = v4f{0.0f, 0.0f, 0.0f, 0.0f};  // rank % 4 == 0
+          *reinterpret_cast<v4f*>(v + ((uint64_t)(m0 + r) * parts + part) * ld + k) = s;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Rows up to here go in tiles of 16, their adapters dealt over workgroups;
+// beyond, in tiles of 64 (prompts: long runs of one adapter), one workgroup
+// taking all of a tile's.
+constexpr uint32_t kShrinkSmallM = 256;
+
+template <int TM, int NR>
+hipError_t launch_shrink_cfg(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v, uint32_t M,
+                             uint32_t K, hipStream_t s) {
+  const uint32_t tiles = (M + 16 * TM - 1) / (16 * TM);
+  const uint32_t z = TM == 1 ? std::min(std::min(16u, M), l.adapters) : 1;
+  lora_shrink_kernel<TM, NR><<<dim3(tiles, l.parts, z), dim3(256), 0, s>>>(x, a, v, l.ids, M, K, l.adapters,
+                                                                          l.rank, l.ld, l.parts);
+  return hipGetLastError();
+}
+
+template <int TM>
+hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v, uint32_t M,
+                         uint32_t K, hipStream_t s) {
+  // rank tiles up to ld, so that the zeros beyond the rank are written too
+  if (l.ld <= 32) return launch_shrink_cfg<TM, 2>(x, a, l, v, M, K, s);
+  if (l.ld <= 64) return launch_shrink_cfg<TM, 4>(x, a, l, v, M, K, s);
+  return launch_shrink_cfg<TM, 8>(x, a, l, v, M, K, s);
+}
+
+// ------------------------------------------------------------------------
+// The projection's GEMM kernels with the adapters' epilogue.
+// ------------------------------------------------------------------------
+struct Gemm {
+  const uint8_t* a;
+  const float* as;
+  const uint8_t* w;
+  const float* ws;
+  uint16_t* out;
+  uint32_t M, N, K, Mp;
+};
+
+template <int TM, int TN, int NWV, int U, bool SPLIT>
+__global__ __launch_bounds__(64 * NWV) void lora_skinny_kernel(Gemm g, uint32_t base, uint32_t rem,
+                                                               float* __restrict__ part, LoraArgs l) {
+  gemm_skinny_body<TM, TN, NWV, U, false, SPLIT>(g.a, g.as, g.w, g.ws, g.out, g.M, g.N, g.K, g.Mp, base,
+                                                 rem, part, LoraEpilogue{l});
+}
+
+template <int TM, int GW>
+__global__ __launch_bounds__(512) void lora_decode_kernel(Gemm g, uint32_t base, uint32_t rem, LoraArgs l) {
+  gemm_decode_body<TM, GW, false>(g.a, g.as, g.w, g.ws, g.out, g.M, g.N, g.K, g.Mp, base, rem,
+                                  LoraEpilogue{l});
+}
+
+template <int STAGES, bool SPLIT>
+__global__ __launch_bounds__(256) void lora_tiled_kernel(Gemm g, uint32_t tiles_m, uint32_t tiles_n,
+                                                         uint32_t splits, float* __restrict__ part, LoraArgs l) {
+  uint32_t tmi, tni, split = 0;
+  if constexpr (SPLIT)
+    tile_split_coords(tiles_m, tiles_n, splits, tmi, tni, split);
+  else
+    tile_coords(tiles_m, tiles_n, tmi, tni);
+  gemm_tiled_body<128, 128, 2, 2, STAGES, false, SPLIT>(g.a, g.as, g.w, g.ws, g.out, tmi * 128, tni * 128, g.N,
+                                                        g.K, g.Mp, split, splits, part,
+                                                        DenseRows{g.M, g.M}, LoraEpilogue{l});
+}
+
+__global__ __launch_bounds__(512) void lora_pp_kernel(Gemm g, uint32_t tiles_m, uint32_t tiles_n, LoraArgs l) {
+  uint32_t tmi, tni;
+  tile_coords(tiles_m, tiles_n, tmi, tni);
+  gemm_pp_body<3, false, false>(g.a, g.as, g.w, g.ws, g.out, tmi * 256, tni * 128, g.N, g.K, g.Mp,
+                                FfnArgs{nullptr, nullptr, nullptr, nullptr, 0}, DenseRows{g.M, g.M},
+                                LoraEpilogue{l});
+}
+
+template <auto kernel, int BYTES>
+hipError_t allow_lds() {
+  static std::atomic<bool> done{false};  // idempotent: racing threads repeat it
+  if (done.load(std::memory_order_acquire)) return hipSuccess;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+  if (e == hipSuccess) done.store(true, std::memory_order_release);
+  return e;
+}
+
+template <int TM, int TN, bool SPLIT>
+hipError_t launch_skinny_cfg(const Gemm& g, uint32_t grid, uint32_t base, uint32_t rem, uint32_t splits,
+                             float* part, const LoraArgs& l, hipStream_t s) {
+  constexpr int NWV = skinny_waves(TM, TN), U = skinny_unroll(TM, TN);
+  constexpr int LDS = NWV * TN * TM * 1024;
+  const hipError_t e = allow_lds<&lora_skinny_kernel<TM, TN, NWV, U, SPLIT>, LDS>();
+  if (e != hipSuccess) return e;
+  const uint32_t row_tiles = (g.M + 16 * TM - 1) / (16 * TM);
+  lora_skinny_kernel<TM, TN, NWV, U, SPLIT>
+      <<<dim3(grid, row_tiles, splits), dim3(64 * NWV), LDS, s>>>(g, base, rem, part, l);
+  return hipGetLastError();
+}
+
+template <bool SPLIT>
+hipError_t launch_skinny(const Gemm& g, uint32_t grid, uint32_t base, uint32_t rem, uint32_t tn, uint32_t splits,
+                         float* part, const LoraArgs& l, hipStream_t s) {
+#define FP8Q_LORA_TN(TM_)                                                                    \
+  (tn <= 2   ? launch_skinny_cfg<TM_, 2, SPLIT>(g, grid, base, rem, splits, part, l, s)      \
+   : tn <= 4 ? launch_skinny_cfg<TM_, 4, SPLIT>(g, grid, base, rem, splits, part, l, s)      \
+   : tn <= 6 ? launch_skinny_cfg<TM_, 6, SPLIT>(g, grid, base, rem, splits, part, l, s)      \
+             : launch_skinny_cfg<TM_, 8, SPLIT>(g, grid, base, rem, splits, part, l, s))
+  switch ((g.M + 15) / 16) {
+    case 1: return FP8Q_LORA_TN(1);
+    case 2: return FP8Q_LORA_TN(2);
+    case 3: return FP8Q_LORA_TN(3);
+    default: return FP8Q_LORA_TN(4);
+  }
+#undef FP8Q_LORA_TN
+}
+
+template <int TM, int GW>
+hipError_t launch_decode_cfg(const Gemm& g, uint32_t grid, uint32_t base, uint32_t rem, uint32_t lds,
+                             const LoraArgs& l, hipStream_t s) {
+  const hipError_t e = allow_lds<&lora_decode_kernel<TM, GW>, kDecodeLds>();
+  if (e != hipSuccess) return e;
+  lora_decode_kernel<TM, GW><<<dim3(grid), dim3(512), lds, s>>>(g, base, rem, l);
+  return hipGetLastError();
+}
+
+template <int TM>
+hipError_t launch_decode(const Gemm& g, uint32_t gw, uint32_t grid, uint32_t base, uint32_t rem, uint32_t lds,
+                         const LoraArgs& l, hipStream_t s) {
+  if (gw == 2) return launch_decode_cfg<TM, 2>(g, grid, base, rem, lds, l, s);
+  if (gw == 4) return launch_decode_cfg<TM, 4>(g, grid, base, rem, lds, l, s);
+  if (gw == 5) return launch_decode_cfg<TM, 5>(g, grid, base, rem, lds, l, s);
+  return launch_decode_cfg<TM, 6>(g, grid, base, rem, lds, l, s);
+}
+
+template <int STAGES, bool SPLIT>
+hipError_t launch_tiled(const Gemm& g, uint32_t splits, float* part, const LoraArgs& l, hipStream_t s) {
+  using C = TileCfg<128, 128, 2, 2, STAGES, false>;
+  const hipError_t e = allow_lds<&lora_tiled_kernel<STAGES, SPLIT>, C::LDS_BYTES>();
+  if (e != hipSuccess) return e;
+  const uint32_t tiles_m = (g.M + 127) / 128, tiles_n = g.N / 128;
+  lora_tiled_kernel<STAGES, SPLIT>
+      <<<dim3(tiles_m * tiles_n * splits), dim3(C::NT), C::LDS_BYTES, s>>>(g, tiles_m, tiles_n, splits, part, l);
+  return hipGetLastError();
+}
+
+hipError_t launch_pp(const Gemm& g, const LoraArgs& l, hipStream_t s) {
+  using C = PpCfg<3, false, false>;
+  const hipError_t e = allow_lds<&lora_pp_kernel, C::LDS_BYTES>();
+  if (e != hipSuccess) return e;
+  const uint32_t tiles_m = (g.M + 255) / 256, tiles_n = g.N / 128;
+  lora_pp_kernel<<<dim3(tiles_m * tiles_n), dim3(C::NT), C::LDS_BYTES, s>>>(g, tiles_m, tiles_n, l);
+  return hipGetLastError();
+}
+
+uint32_t lora_ld(uint32_t rank) { return (rank + 31) / 32 * 32; }
+
+// Parts of K of the shrink: until about 512 workgroups (of at least 128 of K).
+uint32_t lora_parts(uint32_t M, uint32_t K) {
+  const uint32_t wgs = M <= kShrinkSmallM ? (M + 15) / 16 * std::min(16u, M) : (M + 63) / 64;
+  uint32_t p = 1;
+  while (p < kLoraMaxParts && p * wgs < 512 && 2 * p * 128 <= K) p *= 2;
+  return p;
+}
+
+}  // namespace
+
+uint64_t lora_workspace_bytes(uint32_t M, uint32_t K, uint32_t rank) {
+  return (uint64_t)M * lora_parts(M, K) * lora_ld(rank) * 4;
+}
+
+hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, void* workspace,
+                              uint32_t M, uint32_t K, uint32_t adapters, uint32_t rank, hipStream_t s) {
+  LoraArgs l{};
+  l.ids = ids;
+  l.adapters = adapters;
+  l.rank = rank;
+  l.ld = lora_ld(rank);
+  l.parts = lora_parts(M, K);
+  float* v = static_cast<float*>(workspace);
+  return M <= kShrinkSmallM ? launch_shrink<1>(x, a, l, v, M, K, s) : launch_shrink<4>(x, a, l, v, M, K, s);
+}
+
+hipError_t launch_lora_gemm(const uint8_t* a, const float* a_s_km, const uint8_t* w, const float* w_s,
+                            uint16_t* out, const void* workspace, float* part, const uint16_t* lora_b,
+                            const float* lora_scale, const int32_t* ids, uint32_t M, uint32_t N, uint32_t K,
+                            uint32_t adapters, uint32_t rank, uint32_t cus, int kernel, uint32_t splits,
+                            hipStream_t s) {
+  const Gemm g{a, a_s_km, w, w_s, out, M, N, K, m_pad16(M)};
+  const LoraArgs l{static_cast<const float*>(workspace), lora_b, lora_scale, ids, adapters, rank, lora_ld(rank),
+                   lora_parts(M, K), N};
+  if (splits >= 2) {
+    hipError_t e;
+    const uint32_t grid = skinny_split_grid(N, splits, cus);
+    const uint32_t cols = skinny_split_columns(N, splits, cus);
+    if (M <= 64 && cols <= 128)
+      e = launch_skinny<true>(g, grid, N / 4 / grid, N / 4 % grid, (cols + 15) / 16, splits, part, l, s);
+    else if ((uint64_t)((M + 127) / 128) * (N / 128) * splits <= cus)
+      e = launch_tiled<3, true>(g, splits, part, l, s);
+    else
+      e = launch_tiled<2, true>(g, splits, part, l, s);
+    return e != hipSuccess ? e : launch_splitk_reduce(part, out, M, N, splits, s);
+  }
+  if (kernel == 2) {
+    uint32_t grid = 0, base = 0, rem = 0, tn = 0, tm = 0, gw = 0, lds = 0;
+    skinny_grid(M, N, cus, grid, base, rem, tn);
+    if (decode_plan(M, K, base, rem, tm, gw, lds))
+      return tm == 1 ? launch_decode<1>(g, gw, grid, base, rem, lds, l, s)
+                     : launch_decode<2>(g, gw, grid, base, rem, lds, l, s);
+    return launch_skinny<false>(g, grid, base, rem, tn, 1, nullptr, l, s);
+  }
+  if (kernel == 1) return launch_tiled<2, false>(g, 1, nullptr, l, s);
+  return launch_pp(g, l, s);
+}
+
+}  // namespace fp8q
