@@ -94,7 +94,8 @@ struct TileCfg {
 // Rows (gemm_rows.h) says which activation rows a tile's output rows read and
 // where its rows end; Epi adds to the finished accumulators before the store
 // (NoEpilogue: nothing).  The tile is rows m0.. and columns n0.. .
-template <int BM, int BN, int WGM, int WGN, int STAGES, bool ROW, bool SPLIT, class Rows, class Epi>
+template <int BM, int BN, int WGM, int WGN, int STAGES, bool ROW, bool SPLIT, class Rows, class Epi,
+          int WAUX = 0>
 __device__ __forceinline__ void gemm_tiled_body(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t m0, uint32_t n0, uint32_t N,
@@ -148,7 +149,7 @@ __device__ __forceinline__ void gemm_tiled_body(
     for (int j = 0; j < C::DA; ++j) dma16(rA, a_off[j], kb * kGroup, base + (wave * C::DA + j) * 1024);
 #pragma unroll
     for (int j = 0; j < C::DW; ++j)
-      dma16(rW, w_off[j], kb * kGroup, base + C::A_BYTES + (wave * C::DW + j) * 1024);
+      dma16_aux<WAUX>(rW, w_off[j], kb * kGroup, base + C::A_BYTES + (wave * C::DW + j) * 1024);
 #pragma unroll
     for (int j = 0; j < C::SA; ++j) dma4(rS, s_off[j], kb * Mp * 4, base + sc_base + j * 256);
     if constexpr (!ROW) dma4(rWs, ws_off, kb * 4, base + ws_base);

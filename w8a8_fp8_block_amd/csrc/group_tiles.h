@@ -44,55 +44,74 @@ __device__ __forceinline__ uint32_t wave_scan_u32(uint32_t v, uint32_t lane) {
   return v;
 }
 
+// rows of expert e, the first of them in `first`
+__device__ __forceinline__ uint32_t group_rows(const Groups& g, uint32_t e, uint32_t& first) {
+  if (e >= g.E) return 0;
+  first = min((uint32_t)g.offsets[e], g.R);
+  const uint32_t last = min((uint32_t)g.offsets[e + 1], g.R);
+  return last > first ? last - first : 0;
+}
+
+// The row tiles of BM rows, expert by expert, seen by a wave: lane l holds
+// expert l's rows (and, beyond 64 experts, looks the later ones up again).
+template <uint32_t BM>
+struct RowTiles {
+  uint32_t lane, n = 0, first = 0, scan = 0;  // expert `lane`: rows, first row, row tiles up to it
+  uint32_t total;                             // row tiles in all
+
+  __device__ __forceinline__ RowTiles(const Groups& g, uint32_t lane_) : lane(lane_) {
+    n = group_rows(g, lane, first);
+    scan = wave_scan_u32((n + BM - 1) / BM, lane);
+    total = (uint32_t)__builtin_amdgcn_readlane((int)scan, 63);
+    for (uint32_t b = 64; b < g.E; b += 64) {
+      uint32_t f;
+      const uint32_t s = wave_scan_u32((group_rows(g, b + lane, f) + BM - 1) / BM, lane);
+      total += (uint32_t)__builtin_amdgcn_readlane((int)s, 63);
+    }
+  }
+
+  // The expert whose run of tiles (each row tile counting `each`) holds tile
+  // id < total * each: expert, its first row, end, and the tiles before it.
+  __device__ __forceinline__ void find(const Groups& g, uint32_t id, uint32_t each, uint32_t& expert,
+                                       uint32_t& row0, uint32_t& end, uint32_t& prior) {
+    uint32_t before = 0;
+    for (uint32_t b = 0;; b += 64) {
+      if (b) {
+        n = group_rows(g, b + lane, first);
+        scan = wave_scan_u32((n + BM - 1) / BM, lane);
+      }
+      const uint64_t past = __builtin_amdgcn_ballot_w64((before + scan) * each > id);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        const uint32_t rows = (uint32_t)__builtin_amdgcn_readlane((int)n, l);
+        expert = b + (uint32_t)l;
+        row0 = (uint32_t)__builtin_amdgcn_readlane((int)first, l);
+        end = row0 + rows;
+        prior = (before + (uint32_t)__builtin_amdgcn_readlane((int)scan, l) - (rows + BM - 1) / BM) * each;
+        return;
+      }
+      before += (uint32_t)__builtin_amdgcn_readlane((int)scan, 63);
+    }
+  }
+};
+
 // This workgroup's tile of BM rows (false: none left).  Tile ids go expert by
 // expert; within one, blocks of up to 8 row tiles with the column tiles outside,
 // so that neighbours share weight columns, then activation rows; each XCD takes
 // a contiguous run of ids (workgroup ids are dealt round robin to the 8 XCDs).
-// Every wave computes it from the offsets: lane l looks at expert base + l.
 template <uint32_t BM>
 __device__ __forceinline__ bool group_tile(const Groups& g, uint32_t tiles_n, uint32_t bid,
                                            uint32_t lane, GroupTile& t) {
-  auto rows = [&](uint32_t e, uint32_t& first) __attribute__((always_inline)) -> uint32_t {
-    if (e >= g.E) return 0;
-    first = min((uint32_t)g.offsets[e], g.R);
-    const uint32_t last = min((uint32_t)g.offsets[e + 1], g.R);
-    return last > first ? last - first : 0;
-  };
-  uint32_t first = 0, row_tiles = 0;
-  uint32_t n = rows(lane, first);
-  uint32_t scan = wave_scan_u32((n + BM - 1) / BM, lane);
-  row_tiles = (uint32_t)__builtin_amdgcn_readlane((int)scan, 63);
-  for (uint32_t b = 64; b < g.E; b += 64) {
-    uint32_t f;
-    const uint32_t s = wave_scan_u32((rows(b + lane, f) + BM - 1) / BM, lane);
-    row_tiles += (uint32_t)__builtin_amdgcn_readlane((int)s, 63);
-  }
-  const uint32_t total = row_tiles * tiles_n, xcd = bid & 7, slot = bid >> 3;
+  RowTiles<BM> rt(g, lane);
+  const uint32_t total = rt.total * tiles_n, xcd = bid & 7, slot = bid >> 3;
   const uint32_t q = total >> 3, r8 = total & 7;
   if (slot >= q + (xcd < r8 ? 1 : 0)) return false;
   const uint32_t id = xcd * q + min(xcd, r8) + slot;
-  // the expert whose tiles hold id
-  uint32_t before = 0;  // row tiles of earlier experts
-  for (uint32_t b = 0;; b += 64) {
-    if (b) {
-      n = rows(b + lane, first);
-      scan = wave_scan_u32((n + BM - 1) / BM, lane);
-    }
-    const uint64_t past = __builtin_amdgcn_ballot_w64((before + scan) * tiles_n > id);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const uint32_t rt = ((uint32_t)__builtin_amdgcn_readlane((int)n, l) + BM - 1) / BM;
-      const uint32_t prior = before + (uint32_t)__builtin_amdgcn_readlane((int)scan, l) - rt;
-      uint32_t tm;
-      grouped_tile(id - prior * tiles_n, rt, tiles_n, tm, t.tn);
-      t.expert = b + (uint32_t)l;
-      const uint32_t f = (uint32_t)__builtin_amdgcn_readlane((int)first, l);
-      t.end = f + (uint32_t)__builtin_amdgcn_readlane((int)n, l);
-      t.m0 = f + tm * BM;
-      return true;
-    }
-    before += (uint32_t)__builtin_amdgcn_readlane((int)scan, 63);
-  }
+  uint32_t row0, prior, tm;
+  rt.find(g, id, tiles_n, t.expert, row0, t.end, prior);
+  grouped_tile(id - prior, (t.end - row0 + BM - 1) / BM, tiles_n, tm, t.tn);
+  t.m0 = row0 + tm * BM;
+  return true;
 }
 
 // Most row tiles of bm rows that R rows in E groups can need.

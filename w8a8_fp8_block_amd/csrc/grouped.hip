@@ -19,182 +19,313 @@ struct GroupWeights {
 
 // ------------------------------------------------------------------------
 // Streaming kernel for experts of few rows.  The product is then bound by
-// reading each active expert's weights once from HBM.  A wave owns 16 output
-// columns (16 weight rows) and streams its K range through an LDS ring of its
-// own with direct loads, so there is no workgroup barrier in the loop; each
-// load instruction covers two weight rows x 512 contiguous bytes (whole cache
-// lines).  Ring buffer: 16 rows x 4 K blocks, 16-byte chunk c of a row at
-// position c ^ swz(row) within its K block, as in the tiled kernel.  The
-// activation fragments (16 * TM rows, most of them of other tokens: rows past
-// the group load as zeros, without a memory access) come from L2 into
-// registers one chunk ahead.
+// reading each active expert's weights once from HBM, so the design keeps a
+// steady stream of weight loads on every CU: one persistent workgroup of eight
+// waves per CU takes an equal, contiguous run of units (a unit: 16 * CW columns
+// of one expert's row tile over all of K) and runs them as one pipeline, the
+// loads of the next unit following the last of the current one without a gap.
 //
-// KS waves share 16 columns, each a contiguous part of K; their partial tiles
-// are added in K order through LDS at the end.
+// A stage is 16 KB of weights: KS = 8 / CW consecutive K blocks of 16 * CW
+// columns.  Wave (cw, kw) loads and multiplies its own 16 columns x K block kw
+// of every stage; the stage's activations (16 * TM rows x KS blocks), shared by
+// the waves, and each wave's scales come with it, all by direct loads into a
+// ring of ST slots with one barrier a stage.  Rows past the group and K blocks
+// past K are out-of-range loads: zeros without a memory access.  At a unit's end
+// the KS partial tiles are added in K order through LDS.
 // ------------------------------------------------------------------------
-constexpr int kStreamBlocks = 4;                             // K blocks per ring buffer
-constexpr int kStreamBuf = 16 * kStreamBlocks * 128;         // 8 KB
-// past any operand's bound (ceil16(rows) * K < 2^32, so at most 0xFFFFF800), also 16 bytes on
+constexpr int kOffsetsLds = (kMaxExperts + 1) * 4;
+template <int TM, int TN, int CW, int KS>
+struct StreamCfg {
+  static constexpr int NW = CW * KS, BN = 16 * TN * CW;
+  static constexpr int W_BYTES = NW * TN * 2048;               // weights of a stage
+  static constexpr int A_BYTES = KS * TM * 2048;               // activations of a stage
+  static constexpr int SA = (TM + 3) / 4;                      // 64-row loads of the row scales
+  static constexpr int SC_BYTES = SA * 256 + 256;              // per K block: row scales, the waves' weight scales
+  static constexpr int SLOT = W_BYTES + A_BYTES + KS * SC_BYTES;
+  // besides its weights a wave loads JOBS of its K block's 1 KB activation
+  // pieces, row scales and weight scales (dealt over the CW waves)
+  static constexpr int JOBS = (2 * TM + SA + 1 + CW - 1) / CW;
+  static constexpr int LOADS = 2 * TN + JOBS;                  // loads a wave and stage
+  static constexpr int RED = (NW - CW) * TM * TN * 1024;       // partial tiles of the waves with kw > 0
+  static constexpr int SPARE = 256;                            // where loads without a job go
+  static constexpr int ROOM = (160 * 1024 - kOffsetsLds - RED - SPARE) / SLOT, ST = ROOM < 8 ? ROOM : 8;
+  static constexpr int OFFSETS = ST * SLOT + RED + SPARE, LDS = OFFSETS + kOffsetsLds;
+  static_assert(ST >= 3 && (ST - 2) * LOADS < 63, "pipeline");
+};
+constexpr uint32_t kWholeWorkers = 4;
+// past any operand's bound (ceil16(rows) * K < 2^32, so at most 0xFFFFF800)
 constexpr uint32_t kOutOfRange = 0xFFFFFF00u;
 
-template <int TM, int WAVES, int KS>
-__global__ __launch_bounds__(64 * WAVES) void group_stream_kernel(
-    const uint8_t* __restrict__ A, const float* __restrict__ As, GroupWeights gw, Groups g,
-    uint32_t N, uint32_t K, uint32_t Mp, uint32_t tiles_n) {
-  constexpr int CW = WAVES / KS, CB = kStreamBlocks;  // column tiles a workgroup, K blocks a chunk
+// Position of a worker in its run of granules (16 * TN columns of a row tile):
+// the current unit is `width` <= CW granules from `col` on.
+struct UnitCursor {
+  uint32_t expert, m0, end, set, col, width, left;  // left: the worker's granules from col on
+  // size of the unit at col: the worker's part of this row tile in equal units
+  template <int CW>
+  __device__ __forceinline__ void size(uint32_t granules) {
+    const uint32_t seg = min(granules - col, left), n = (seg + CW - 1) / CW;
+    width = n ? (seg + n - 1) / n : 0;
+  }
+  // the next unit (left = 0: none); true if its rows differ
+  template <int BM, int CW>
+  __device__ __forceinline__ bool next(const uint32_t* offsets, uint32_t sets, uint32_t granules) {
+    col += width;
+    left -= width;
+    bool moved = false;
+    if (col == granules && left > 0) {
+      col = 0;
+      if (++set == sets) {
+        set = 0;
+        moved = true;
+        m0 += BM;
+        while (m0 >= end) {  // (granules are left: an expert with rows follows)
+          ++expert;
+          m0 = __builtin_amdgcn_readfirstlane(offsets[expert]);
+          end = __builtin_amdgcn_readfirstlane(offsets[expert + 1]);
+        }
+      }
+    }
+    size<CW>(granules);
+    return moved;
+  }
+};
+
+template <int TM, int TN, int CW, int KS>
+__global__ __launch_bounds__(64 * CW * KS) void group_stream_kernel(const uint8_t* __restrict__ A,
+                                                           const float* __restrict__ As, GroupWeights gw,
+                                                           uint32_t sets, Groups g, uint32_t N, uint32_t K,
+                                                           uint32_t Mp) {
+  using C = StreamCfg<TM, TN, CW, KS>;
+  constexpr int BM = 16 * TM, ST = C::ST;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  GroupTile t;
-  if (!group_tile<16 * TM>(g, tiles_n, blockIdx.x, lane, t)) return;
-  const uint32_t l16 = lane & 15, q = lane >> 4, G = K / kGroup;
-  const uint32_t cw = wave % CW, ks = wave / CW;
-  const uint32_t n0 = (t.tn * CW + cw) * 16;
-  const uint32_t kbeg = ks * G / KS, kend = (ks + 1) * G / KS;
-  const uint32_t which = blockIdx.y;
-  const uint8_t* W = gw.w[which] + ((uint64_t)t.expert * N + n0) * K;
-  const float* Ws = gw.ws[which] + ((uint64_t)t.expert * (N / kGroup) + n0 / kGroup) * G;
-  const GroupRows rows{g.a_rows, t.end, g.order, g.per_row};
+  const uint32_t cw = wave % CW, kw = wave / CW;
+  const uint32_t l16 = lane & 15, q = lane >> 4;
+  const uint32_t G = K / kGroup, stages = (G + KS - 1) / KS, granules = N / (16 * TN);
 
+  // this worker's granules; workers are numbered XCD by XCD
+  RowTiles<BM> rt(g, lane);
+  const uint32_t workers = gridDim.x, bid = blockIdx.x;
+  const uint32_t w = workers % 8 == 0 ? (bid & 7) * (workers / 8) + (bid >> 3) : bid;
+  // Few row tiles: each gets whole workers, so that no worker crosses from one
+  // to the next (a crossing adds a unit, and a stage takes nearly the same time
+  // however wide).  Many: equal runs.
+  const uint32_t each = sets * granules;  // granules of a row tile
+  if (rt.total == 0) return;
+  uint32_t tile, col, count;
+  if (rt.total * kWholeWorkers <= workers) {
+    tile = w * rt.total / workers;
+    const uint32_t first = (tile * workers + rt.total - 1) / rt.total;
+    const uint32_t n = ((tile + 1) * workers + rt.total - 1) / rt.total - first;
+    col = (w - first) * each / n;
+    count = (w - first + 1) * each / n - col;
+  } else {
+    const uint64_t all = (uint64_t)rt.total * each;
+    const uint64_t g0 = all * w / workers, g1 = all * (w + 1) / workers;
+    tile = (uint32_t)(g0 / each);
+    col = (uint32_t)(g0 % each);
+    count = (uint32_t)(g1 - g0);
+  }
+  if (count == 0) return;  // uniform over the workgroup
+  UnitCursor ld;
+  {
+    uint32_t row0, prior;
+    rt.find(g, tile, 1, ld.expert, row0, ld.end, prior);
+    ld.m0 = row0 + (tile - prior) * BM;
+    ld.set = col / granules;
+    ld.col = col % granules;
+    ld.left = count;
+    ld.size<CW>(granules);
+  }
+  UnitCursor cu = ld;
+  uint32_t* offs = reinterpret_cast<uint32_t*>(smem + C::OFFSETS);
+  for (uint32_t e = threadIdx.x; e <= g.E; e += 64 * C::NW) offs[e] = min((uint32_t)g.offsets[e], g.R);
+  __syncthreads();
+
+  // ---- load side ----
   const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, g.a_rows * K);
-  const __amdgpu_buffer_rsrc_t rW = make_rsrc(W, 16 * K);
-  uint32_t a_off[TM], s_idx[TM];
+  const __amdgpu_buffer_rsrc_t rS = make_rsrc(As, G * Mp * 4);
+  __amdgpu_buffer_rsrc_t rW, rWs;
+  uint32_t w_off[2 * TN], j_off[C::JOBS];  // source offsets of this lane: weights, jobs
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const uint32_t m = t.m0 + 16 * tm + l16;
-    const uint32_t r = rows.src(min(m, t.end - 1));
-    a_off[tm] = m < t.end ? r * K + 32 * q : kOutOfRange;
-    s_idx[tm] = r;
+  for (int j = 0; j < 2 * TN; ++j) {
+    const uint32_t row = 8 * j + (lane >> 3);
+    w_off[j] = row * K + ((lane & 7) ^ swz(row)) * 16;
   }
-  // source of this lane's 16 bytes in load j of a chunk: weight row 2j + lane/32,
-  // chunk position lane % 32
-  const uint32_t pos = lane & 31, blk = pos >> 3;
-  const uint32_t ring = lds_addr(smem) + wave * 2 * kStreamBuf;
-  uint32_t w_off[8];
+  auto rows_of = [&]() __attribute__((always_inline)) {
+    const GroupRows rows{g.a_rows, ld.end, g.order, g.per_row};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t row = 2 * j + (lane >> 5);
-    w_off[j] = row * K + blk * kGroup + ((pos & 7) ^ swz(row)) * 16;
-  }
-  auto issue_w = [&](uint32_t kb, uint32_t buf) __attribute__((always_inline)) {
-    const uint32_t out = kb + blk < kend ? 0 : kOutOfRange;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      dma16_at(rW, w_off[j] | out, kb * kGroup, ring + buf * kStreamBuf + j * 1024);
-  };
-  struct Frag {
-    v8i a[CB][TM];
-    float as[CB][TM], ws;  // ws: lane b holds the weight scale of block b (b < CB)
-  };
-  auto load_a = [&](Frag& f, uint32_t kb) __attribute__((always_inline)) {
-#pragma unroll
-    for (int b = 0; b < CB; ++b) {
-      const uint32_t k = min(kb + b, kend - 1);  // past the range: the weights are zeros
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) {
-        f.a[b][tm] = join(__builtin_amdgcn_raw_buffer_load_b128(rA, a_off[tm], k * kGroup, 0),
-                          __builtin_amdgcn_raw_buffer_load_b128(rA, a_off[tm] + 16, k * kGroup, 0));
-        f.as[b][tm] = As[(uint64_t)k * Mp + s_idx[tm]];
+    for (int j = 0; j < C::JOBS; ++j) {
+      const uint32_t job = cw * C::JOBS + j;
+      if (job < 2 * TM) {
+        const uint32_t r = job * 8 + (lane >> 3), m = ld.m0 + r;
+        j_off[j] = m < ld.end ? rows.src(m) * K + ((lane & 7) ^ swz(r)) * 16 : kOutOfRange;
+      } else if (job < 2 * TM + C::SA) {
+        j_off[j] = rows.src(min(ld.m0 + (job - 2 * TM) * 64 + lane, ld.end - 1)) * 4;
       }
     }
-    f.ws = Ws[min(kb + (lane & (CB - 1)), kend - 1)];
   };
-  v4f acc[TM];
+  auto weights_of = [&]() __attribute__((always_inline)) {
+    const uint32_t n0 = (ld.col + min(cw, ld.width - 1)) * 16 * TN;  // (waves past the unit load nothing)
+    rW = make_rsrc(gw.w[ld.set] + ((uint64_t)ld.expert * N + n0) * K, 16 * TN * K);
+    rWs = make_rsrc(gw.ws[ld.set] + (uint64_t)ld.expert * (N / kGroup) * G, (N / kGroup) * G * 4);
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) acc[tm] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint32_t c0 = 2 * q;
-  const uint32_t lo0 = l16 * (CB * 128) + ((c0 ^ swz(l16)) * 16);
-  const uint32_t lo1 = l16 * (CB * 128) + (((c0 + 1) ^ swz(l16)) * 16);
-  const uint8_t* my = smem + wave * 2 * kStreamBuf;
-  auto consume = [&](const Frag& f, uint32_t buf) __attribute__((always_inline)) {
-    const uint8_t* s = my + buf * kStreamBuf;
-    v8i w[CB];
+    for (int j = 0; j < C::JOBS; ++j)  // lane w: the weight scale of wave w's columns
+      if (cw * C::JOBS + j == 2 * TM + C::SA)
+        j_off[j] = lane < CW ? (ld.col + min(lane, ld.width - 1)) * 16 * TN / kGroup * G * 4 : kOutOfRange;
+  };
+  rows_of();
+  weights_of();
+  uint32_t l_kb = kw, l_slot = 0;  // l_kb: this wave's K block of the stage to load
+  const uint32_t lds0 = lds_addr(smem);
+  auto issue = [&]() __attribute__((always_inline)) {
+    const bool in = ld.left > 0 && l_kb < G;
+    const uint32_t off = in ? 0 : kOutOfRange, k = in ? l_kb : 0, w_out = cw < ld.width ? off : kOutOfRange;
+    const uint32_t slot = lds0 + l_slot * C::SLOT;
 #pragma unroll
-    for (int b = 0; b < CB; ++b) {
-      w[b] = join(*reinterpret_cast<const u32x4*>(s + lo0 + b * 128),
-                  *reinterpret_cast<const u32x4*>(s + lo1 + b * 128));
+    for (int j = 0; j < 2 * TN; ++j)
+      dma16_at_aux<kStreamOnce>(rW, w_off[j] | w_out, k * kGroup, slot + wave * TN * 2048 + j * 1024);
+    const uint32_t a_at = slot + C::W_BYTES + kw * TM * 2048;
+    const uint32_t sc_at = slot + C::W_BYTES + C::A_BYTES + kw * C::SC_BYTES;
+#pragma unroll
+    for (int j = 0; j < C::JOBS; ++j) {
+      const uint32_t job = cw * C::JOBS + j;  // uniform over the wave
+      if (job < 2 * TM)
+        dma16_at(rA, j_off[j] | off, k * kGroup, a_at + job * 1024);
+      else if (job < 2 * TM + C::SA)
+        dma4_at(rS, j_off[j], k * Mp * 4, sc_at + (job - 2 * TM) * 256);
+      else if (job == 2 * TM + C::SA)
+        dma4_at(rWs, j_off[j], k * 4, sc_at + C::SA * 256);
+      else
+        dma4_at(rWs, kOutOfRange, 0, lds0 + ST * C::SLOT + C::RED);  // no job: keeps the count of loads
     }
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) {
-      v4f p[CB];
-#pragma unroll
-      for (int b = 0; b < CB; ++b) p[b] = mfma_e4m3_128(w[b], f.a[b][tm]);
-#pragma unroll
-      for (int b = 0; b < CB; ++b)
-        acc[tm] += p[b] * (f.as[b][tm] * __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
-                                             (int)__float_as_uint(f.ws), b)));
+    l_slot = l_slot + 1 == ST ? 0 : l_slot + 1;
+    l_kb += KS;
+    if (l_kb - kw >= stages * KS && ld.left > 0) {  // uniform: the unit's last stage was loaded
+      l_kb = kw;
+      if (ld.next<BM, CW>(offs, sets, granules)) rows_of();
+      if (ld.left > 0) weights_of();
     }
   };
-  if (kbeg < kend) {
-    // Loads are issued chunk by chunk, weights then activations, in this
-    // order (the fences): at most the next chunk's 8 + 12 * TM + 1 may be
-    // outstanding when a chunk is consumed.
-    constexpr int AHEAD = 8 + CB * 3 * TM + 1;
-    Frag f0, f1;
-    auto issue = [&](Frag& f, uint32_t kb, uint32_t buf) __attribute__((always_inline)) {
-      sched_fence();
-      issue_w(kb, buf);  // past the range: zeros, no memory access
-      sched_fence();
-      load_a(f, min(kb, kend - 1));
-      sched_fence();
-    };
-    issue(f0, kbeg, 0);
-    issue(f1, kbeg + CB, 1);
-    for (uint32_t kb = kbeg; kb < kend; kb += 2 * CB) {
-      wait_vmcnt<AHEAD>();
-      consume(f0, 0);
-      wait_lgkm0();
-      issue(f0, kb + 2 * CB, 0);
-      wait_vmcnt<AHEAD>();
-      consume(f1, 1);
-      wait_lgkm0();
-      issue(f1, kb + 3 * CB, 1);
-    }
-    wait_vmcnt<0>();  // no direct load may still be writing LDS
-  }
-  if constexpr (KS > 1) {
-    wg_barrier();
-    v4f* red = reinterpret_cast<v4f*>(smem);
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) red[(wave * TM + tm) * 64 + lane] = acc[tm];
-    __syncthreads();
-    if (ks != 0) return;
+
+  // ---- compute side ----
+  v4f acc[TM][TN];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
-      for (int k = 1; k < KS; ++k) acc[tm] += red[((k * CW + cw) * TM + tm) * 64 + lane];
-  }
-  uint16_t* out = gw.out[which];
+      for (int t = 0; t < TN; ++t) acc[tm][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  };
+  clear();
+  const uint32_t c0 = 2 * q;
+  const uint32_t lo0 = l16 * 128 + ((c0 ^ swz(l16)) * 16), lo1 = l16 * 128 + (((c0 + 1) ^ swz(l16)) * 16);
+  auto frag = [&](const uint8_t* p) __attribute__((always_inline)) -> v8i {
+    return join(*reinterpret_cast<const u32x4*>(p + lo0), *reinterpret_cast<const u32x4*>(p + lo1));
+  };
+  auto epilogue = [&]() __attribute__((always_inline)) {
+    v4f* red = reinterpret_cast<v4f*>(smem + ST * C::SLOT) + lane;
+    if constexpr (KS > 1) {
+      if (kw > 0) {
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const uint32_t m = t.m0 + 16 * tm + l16;
-    if (m < t.end) *reinterpret_cast<uint2*>(out + (uint64_t)m * N + n0 + 4 * q) = pack_bf16x4(acc[tm]);
+        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+          for (int t = 0; t < TN; ++t) red[(((wave - CW) * TM + tm) * TN + t) * 64] = acc[tm][t];
+      }
+      wait_lgkm0();
+      wg_barrier();
+    }
+    if (kw == 0 && cw < cu.width) {
+      uint16_t* out = gw.out[cu.set];
+      const uint32_t n = (cu.col + cw) * 16 * TN + 4 * q;
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) {
+        const uint32_t m = cu.m0 + 16 * tm + l16;
+#pragma unroll
+        for (int t = 0; t < TN; ++t) {
+#pragma unroll
+          for (int k = 1; k < KS; ++k) acc[tm][t] += red[((((k - 1) * CW + cw) * TM + tm) * TN + t) * 64];
+          if (m < cu.end) *reinterpret_cast<uint2*>(out + (uint64_t)m * N + n + 16 * t) = pack_bf16x4(acc[tm][t]);
+        }
+      }
+    }
+    clear();
+  };
+
+#pragma unroll 1
+  for (int s = 0; s < ST - 1; ++s) issue();
+  uint32_t slot = 0;
+  while (true) {
+#pragma unroll 1
+    for (uint32_t s = 0; s < stages; ++s) {
+      wait_vmcnt<(ST - 2) * C::LOADS>();  // own part of this stage
+      wg_barrier();                       // everyone's; and the slot before is free
+      issue();
+      const uint8_t* p = smem + slot * C::SLOT;
+      const uint8_t* sc = p + C::W_BYTES + C::A_BYTES + kw * C::SC_BYTES;
+      v8i wf[TN], af[TM];
+      float as[TM];
+#pragma unroll
+      for (int t = 0; t < TN; ++t) wf[t] = frag(p + (wave * TN + t) * 2048);
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm) {
+        af[tm] = frag(p + C::W_BYTES + (kw * TM + tm) * 2048);
+        as[tm] = *reinterpret_cast<const float*>(sc + (16 * tm + l16) * 4);
+      }
+      const float ws = *reinterpret_cast<const float*>(sc + C::SA * 256 + cw * 4);
+      v4f r[TM][TN];
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+        for (int t = 0; t < TN; ++t) r[tm][t] = mfma_e4m3_128(wf[t], af[tm]);
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+        for (int t = 0; t < TN; ++t) acc[tm][t] += r[tm][t] * (as[tm] * ws);
+      wait_lgkm0();  // this stage's reads are done: the barrier frees its slot
+      slot = slot + 1 == ST ? 0 : slot + 1;
+    }
+    epilogue();
+    cu.next<BM, CW>(offs, sets, granules);
+    if (cu.left == 0) break;
   }
+  wait_vmcnt<0>();  // no direct load may still be writing LDS at exit
 }
 
-template <int TM, int WAVES, int KS>
+template <class F>
+hipError_t allow_lds(std::atomic<bool>& done, F* kernel, int bytes) {
+  if (done.load(std::memory_order_acquire)) return hipSuccess;  // idempotent: racing threads repeat it
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess) done.store(true, std::memory_order_release);
+  return e;
+}
+
+template <int TM, int TN, int CW, int KS>
 hipError_t launch_stream(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
-                         const Groups& g, uint32_t N, uint32_t K, hipStream_t s) {
-  constexpr uint32_t LDS = WAVES * 2 * kStreamBuf;
-  static_assert(LDS <= 64 * 1024 && WAVES * TM * 1024 <= (int)LDS, "ring, partial tiles");
-  const uint32_t tiles_n = N / (16 * (WAVES / KS));
-  const uint32_t grid = max_row_tiles(g.R, g.E, 16 * TM) * tiles_n;
-  group_stream_kernel<TM, WAVES, KS><<<dim3(grid, sets), dim3(64 * WAVES), LDS, s>>>(
-      a, as, gw, g, N, K, m_pad16(g.a_rows), tiles_n);
+                         const Groups& g, uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
+  using C = StreamCfg<TM, TN, CW, KS>;
+  static std::atomic<bool> done{false};
+  const hipError_t e = allow_lds(done, &group_stream_kernel<TM, TN, CW, KS>, C::LDS);
+  if (e != hipSuccess) return e;
+  const uint64_t units = (uint64_t)max_row_tiles(g.R, g.E, 16 * TM) * sets * (N / (16 * TN));
+  const uint32_t grid = (uint32_t)(units < cus ? units : cus);
+  group_stream_kernel<TM, TN, CW, KS>
+      <<<dim3(grid), dim3(64 * C::NW), C::LDS, s>>>(a, as, gw, sets, g, N, K, m_pad16(g.a_rows));
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------------
 // The dense GEMM's tiled and ping-pong kernels over the experts' rows.
 // ------------------------------------------------------------------------
-template <int BM, int BN, int WGM, int WGN, int STAGES>
+template <int BM, int BN, int WGM, int WGN, int STAGES, int WAUX>
 __global__ __launch_bounds__(64 * WGM * WGN) void group_tiled_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, GroupWeights gw, Groups g,
     uint32_t N, uint32_t K, uint32_t Mp, uint32_t tiles_n) {
   GroupTile t;
   if (!group_tile<BM>(g, tiles_n, blockIdx.x, threadIdx.x & 63, t)) return;
   const uint32_t which = blockIdx.y;
-  gemm_tiled_body<BM, BN, WGM, WGN, STAGES, false, false>(
+  gemm_tiled_body<BM, BN, WGM, WGN, STAGES, false, false, GroupRows, NoEpilogue, WAUX>(
       A, As, gw.w[which] + (uint64_t)t.expert * N * K,
       gw.ws[which] + (uint64_t)t.expert * (N / kGroup) * (K / kGroup), gw.out[which], t.m0, t.tn * BN,
       N, K, Mp, 0, 1, nullptr, GroupRows{g.a_rows, t.end, g.order, g.per_row}, NoEpilogue{});
@@ -230,23 +361,17 @@ __global__ __launch_bounds__(512) void group_gate_up_kernel(
                                GroupRows{g.a_rows, t.end, g.order, g.per_row}, NoEpilogue{});
 }
 
-template <class F>
-hipError_t allow_lds(std::atomic<bool>& done, F* kernel, int bytes) {
-  if (done.load(std::memory_order_acquire)) return hipSuccess;  // idempotent: racing threads repeat it
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.store(true, std::memory_order_release);
-  return e;
-}
-
+// WAUX: the weights' cache policy.  With one row tile an expert they are read
+// once; with several the tiles share them through L2.
+template <int WAUX>
 hipError_t launch_group_128(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                             const Groups& g, uint32_t N, uint32_t K, hipStream_t s) {
   using C = TileCfg<128, 128, 2, 2, 2, false>;
   static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_tiled_kernel<128, 128, 2, 2, 2>, C::LDS_BYTES);
+  const hipError_t e = allow_lds(done, &group_tiled_kernel<128, 128, 2, 2, 2, WAUX>, C::LDS_BYTES);
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = N / 128;
-  group_tiled_kernel<128, 128, 2, 2, 2><<<dim3(max_row_tiles(g.R, g.E, 128) * tiles_n, sets), dim3(C::NT),
+  group_tiled_kernel<128, 128, 2, 2, 2, WAUX><<<dim3(max_row_tiles(g.R, g.E, 128) * tiles_n, sets), dim3(C::NT),
                                           C::LDS_BYTES, s>>>(a, as, gw, g, N, K, m_pad16(g.a_rows), tiles_n);
   return hipGetLastError();
 }
@@ -268,20 +393,31 @@ constexpr int kGroupStream = 1, kGroupTiled = 2, kGroupPp = 3;
 
 int group_auto(uint32_t R, uint32_t E) {
   const uint32_t mean = R / (R < E ? R : E);  // rows per expert at least
-  return mean <= 16 ? kGroupStream : mean < 192 ? kGroupTiled : kGroupPp;
+  return mean < 14 ? kGroupStream : mean < 192 ? kGroupTiled : kGroupPp;
+}
+
+// One row tile holds up to this many rows an expert on average: 16-row tiles
+// (then stages of 64 columns x 2 K blocks), else 32-row ones (128 x 1).
+// Measured at E = 32, N x K = 2048 x 5120 / 5120 x 2048 (335 MB of weights), us:
+// mean 2: 45.4 / 44.7 (16 rows) against 43.1 / 44.3 (32), mean 8: 59.9 / 59.0
+// against 54.3 / 54.2; at E = 64, mean 1.5, N = 1408 and 5120 the 16-row
+// form takes 171 us for the expert FFN against 189.
+constexpr uint32_t kStreamFewRows = 4;
+
+hipError_t launch_stream_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
+                             const Groups& g, uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
+  if ((uint64_t)g.R <= (uint64_t)kStreamFewRows * g.E)
+    return launch_stream<1, 1, 4, 2>(a, as, gw, sets, g, N, K, cus, s);
+  return launch_stream<2, 1, 8, 1>(a, as, gw, sets, g, N, K, cus, s);
 }
 
 hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                       const Groups& g, uint32_t N, uint32_t K, uint32_t cus, int kernel, hipStream_t s) {
   switch (kernel) {
-    case kGroupStream: {
-      // K split until the grid holds about two workgroups per CU
-      const uint64_t wgs = (uint64_t)(g.R < g.E ? g.R : g.E) * sets * (N / 64);
-      if (wgs >= 2 * cus) return launch_stream<1, 4, 1>(a, as, gw, sets, g, N, K, s);
-      if (2 * wgs >= 2 * cus) return launch_stream<1, 4, 2>(a, as, gw, sets, g, N, K, s);
-      return launch_stream<1, 4, 4>(a, as, gw, sets, g, N, K, s);
-    }
-    case kGroupTiled: return launch_group_128(a, as, gw, sets, g, N, K, s);
+    case kGroupStream: return launch_stream_any(a, as, gw, sets, g, N, K, cus, s);
+    case kGroupTiled:
+      return g.R < 64ull * g.E ? launch_group_128<kStreamOnce>(a, as, gw, sets, g, N, K, s)
+                               : launch_group_128<0>(a, as, gw, sets, g, N, K, s);
     default: return launch_group_pp(a, as, gw, sets, g, N, K, s);
   }
 }

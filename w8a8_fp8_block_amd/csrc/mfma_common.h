@@ -45,6 +45,14 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t voff, u
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff,
                                            soff, 0, 0);
 }
+// Cache policy of data read once (streamed weights): read alone from HBM, 1 GiB
+// at 7.0 TB/s against 6.2 with the default policy.
+constexpr int kStreamOnce = 2;
+template <int AUX>
+__device__ __forceinline__ void dma16_aux(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff,
+                                           soff, 0, AUX);
+}
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff, void* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff,
                                            soff, 0, 0);
@@ -56,6 +64,12 @@ __device__ __forceinline__ void dma16_at(__amdgpu_buffer_rsrc_t r, uint32_t voff
                                          uint32_t lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(size_t)lds,
                                            16, voff, soff, 0, 0);
+}
+template <int AUX>
+__device__ __forceinline__ void dma16_at_aux(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
+                                             uint32_t lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(size_t)lds,
+                                           16, voff, soff, 0, AUX);
 }
 __device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff,
                                         uint32_t lds) {
