@@ -1309,11 +1309,21 @@ fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int
   return launched(fn, launch_combine(y, weights, pos, offsets, out_bf16, T, E, top_k, H, stream));
 }
 
+namespace {
+// Split-K of the projection with adapters: as without, but up to 64 rows only
+// where the skinny kernel's split form runs (the tiled one would take a wave's
+// adapters one after another in its first split).
+uint32_t lora_splits(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
+  const uint32_t s = splitk_auto(M, N, K, cus);
+  return M <= kSplitMinM && s >= 2 && skinny_split_columns(N, s, cus) > 128 ? 1 : s;
+}
+}  // namespace
+
 size_t fp8q_proj_lora_workspace_bytes(uint32_t M, uint32_t N, uint32_t K, uint32_t rank) {
   if (N == 0 || N % kGroup != 0 || K == 0 || K % kGroup != 0 || rank == 0 || rank > kMaxLoraRank || rank % 8 != 0)
     return 0;
   return (size_t)(align256(lora_workspace_bytes(M, K, rank)) +
-                  splitk_workspace(M, N, splitk_auto(M, N, K, current_cus())));
+                  splitk_workspace(M, N, lora_splits(M, N, K, current_cus())));
 }
 
 fp8q_status fp8q_proj_lora(const uint16_t* x_bf16, const uint8_t* w_e4m3, const float* w_scale,
@@ -1346,20 +1356,14 @@ fp8q_status fp8q_proj_lora(const uint16_t* x_bf16, const uint8_t* w_e4m3, const 
   REQUIRE_PTR(act_scale_km_scratch);
   if (M == 0) return ok();
   const uint32_t cus = current_cus();  // as the size query
-  const uint32_t splits = splitk_auto(M, N, K, cus);
+  const uint32_t splits = lora_splits(M, N, K, cus);
   const uint64_t vbytes = align256(lora_workspace_bytes(M, K, rank));
   st = check_workspace(fn, workspace, workspace_bytes, vbytes + splitk_workspace(M, N, splits));
   if (st != FP8Q_OK) return st;
   st = check_device(fn);
   if (st != FP8Q_OK) return st;
-  if ((uint64_t)M * (K / kGroup) <= kFusedKmajorMaxGroups) {
-    st = run_quant(fn, x_bf16, act_q_scratch, act_scale_scratch, act_scale_km_scratch, M, K, 0, stream);
-  } else {
-    st = run_quant(fn, x_bf16, act_q_scratch, act_scale_scratch, nullptr, M, K, 0, stream);
-    if (st == FP8Q_OK) st = launched(fn, launch_relayout(act_scale_scratch, act_scale_km_scratch, M, K, stream));
-  }
-  if (st != FP8Q_OK) return st;
-  st = launched(fn, launch_lora_shrink(x_bf16, lora_a, adapter_ids, workspace, M, K, adapters, rank, stream));
+  st = launched(fn, launch_lora_quant_shrink(x_bf16, lora_a, adapter_ids, act_q_scratch, act_scale_scratch,
+                                             act_scale_km_scratch, workspace, M, K, adapters, rank, stream));
   if (st != FP8Q_OK) return st;
   return launched(fn, launch_lora_gemm(act_q_scratch, act_scale_km_scratch, w_e4m3, w_scale, out_bf16, workspace,
                                        reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + vbytes), lora_b,

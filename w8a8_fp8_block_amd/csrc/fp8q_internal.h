@@ -189,10 +189,12 @@ hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const
 
 // ---- low-rank adapters beside the projection (lora.hip) ----
 constexpr uint32_t kMaxLoraRank = 128;
-// v = x . A^T of the rows with an adapter, into workspace (lora_workspace_bytes).
+// One pass over x: its codes and scales (both layouts, pad slots zeroed), and
+// v = x . A^T of the rows with an adapter into workspace (lora_workspace_bytes).
 uint64_t lora_workspace_bytes(uint32_t M, uint32_t K, uint32_t rank);
-hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, void* workspace,
-                              uint32_t M, uint32_t K, uint32_t adapters, uint32_t rank, hipStream_t s);
+hipError_t launch_lora_quant_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, uint8_t* x_q,
+                                    float* x_s_rm, float* x_s_km, void* workspace, uint32_t M, uint32_t K,
+                                    uint32_t adapters, uint32_t rank, hipStream_t s);
 // The block-scaled GEMM (kernel ids of launch_gemm: 1, 2 or 5; splits >= 2:
 // its split form with part [splits, M, N]) plus scale * v . B^T.
 hipError_t launch_lora_gemm(const uint8_t* a, const float* a_s_km, const uint8_t* w, const float* w_s,

@@ -453,7 +453,7 @@ __device__ __forceinline__ void gemm_pp_body(
   }
 
   epi.template add<TM, TN>([&](int tm, int tn) -> v4f& { return acc[tm][tn]; },
-                           m0 + wm * C::WM, n0 + wn * C::WN, M, lane, 0, 1, 0);
+                           m0 + wm * C::WM, n0 + wn * C::WN, M, lane, 0);
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm) {
     const uint32_t m = m0 + wm * C::WM + tm * 16 + l16;

@@ -122,8 +122,9 @@ __device__ __forceinline__ void gemm_skinny_body(
     }
   }
 
-  epi.template add<TM, TN>([&](int tm, int t) -> v4f& { return acc[t][tm]; }, m0, c0, M, lane,
-                           SPLIT ? blockIdx.z * NWV + wave : wave, SPLIT ? NWV * gridDim.z : NWV, 0);
+  epi.template add_shared<TM, TN, 64 * NWV>([&](int tm, int t) -> v4f& { return acc[t][tm]; }, smem, m0, c0, M,
+                                            lane, SPLIT ? blockIdx.z * NWV + wave : wave,
+                                            SPLIT ? NWV * gridDim.z : NWV);
 #pragma unroll
   for (int t = 0; t < TN; ++t)
 #pragma unroll
@@ -282,8 +283,9 @@ __device__ __forceinline__ void gemm_decode_body(
 #pragma unroll
       for (int j = 1; j < GW; ++j) acc[t][tm] += p[j] * (as[j][tm] * ws[j][t]);
     }
-  epi.template add<TM, NT>([&](int tm, int t) -> v4f& { return acc[t][tm]; }, 0, c0, M, lane, wave, 8, 0);
   wg_barrier();  // every wave done with the weight rows: LDS takes the partial tiles
+  epi.template add_shared<TM, NT, 512>([&](int tm, int t) -> v4f& { return acc[t][tm]; }, smem, 0, c0, M, lane,
+                                       wave, 8);
   v4f* red = reinterpret_cast<v4f*>(smem);
 #pragma unroll
   for (int t = 0; t < NT; ++t)

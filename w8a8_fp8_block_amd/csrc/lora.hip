@@ -2,8 +2,8 @@
 //   out[m] = bf16( quant(x)[m] . W^T + scale[a] * (x[m] . A[a]^T) . B[a]^T ),
 // a = ids[m], rows without an adapter the projection alone.
 //
-// Two parts: a shrink kernel forms v = x . A^T (fp32, in parts of K), and the
-// projection's own GEMM kernels run with an epilogue that adds scale * v . B^T to
+// Two parts: one pass over x quantizes it and forms v = x . A^T (fp32, in parts
+// of K), and the projection's own GEMM kernels run with an epilogue that adds scale * v . B^T to
 // their fp32 accumulators (lora.h), so that the sum is rounded once and out is
 // written once.
 #include <atomic>
@@ -16,46 +16,106 @@ namespace fp8q {
 namespace {
 
 // ------------------------------------------------------------------------
-// Shrink: v[m, r] = sum_k x[m, k] * A[a][r, k] in fp32 from bf16.  A workgroup
-// takes 16 * TM rows and one part of K, its four waves a quarter of the part
-// each; blockIdx.z picks among the rows' distinct adapters (round robin).  Per
-// adapter every row's product is formed with 16x16x32 MFMAs, NR rank tiles of
-// 16, and the rows of that adapter are stored.  Bound by reading A (decode: a
-// few rows an adapter) or x (prompts); both are read in 64-byte pieces of a row
-// by four lanes.
+// Quantize and shrink, one pass over x: the FP8 codes and scales of x (the
+// activation quantizer's steps) and v[m, r] = sum_k x[m, k] * A[a][r, k] in fp32
+// from bf16.  A workgroup takes 16 * TM rows and one part of K, its four waves
+// every fourth 128-group of it; blockIdx.z picks among the rows' distinct
+// adapters (round robin), and z = 0 quantizes as well.  A lane holds the 16-byte
+// pieces k = 32 j + 8 (l / 16), j < 4, of row l % 16 in the group: an operand of
+// the 16x16x32 MFMA as it stands, and 32 of the group's 128 values, the other
+// 96 in the lanes 16, 32 and 48 away.  Per adapter every row's product is formed
+// (NR rank tiles of 16) and the rows of that adapter are stored; adapters after
+// a workgroup's first read its rows again, from L2.  Bound by reading A (decode:
+// a few rows an adapter) or x (prompts).
 // ------------------------------------------------------------------------
+struct QuantOut {
+  uint8_t* q;    // [M,K]
+  float* rm;     // [M,K/128]
+  float* km;     // [K/128,Mp]
+};
+
+// This lane's 32 values of a 128-group -> codes, the group's scale
+__device__ __forceinline__ float quant_lane_group(const u32x4 (&x)[4], uint2 (&codes)[4]) {
+  const uint32_t mag = 0x7FFF7FFFu;
+  u16x2 mx = as_u16x2(0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = __builtin_elementwise_max(mx, as_u16x2(x[j][i] & mag));
+  uint32_t amax = max((uint32_t)mx.x, (uint32_t)mx.y);
+  amax = max(amax, (uint32_t)__shfl_xor((int)amax, 16));
+  amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32));
+  const float s = group_scale(amax);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float f[8], r[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf_lo(x[j][i]);
+      f[2 * i + 1] = bf_hi(x[j][i]);
+    }
+    quotients<8>(f, s, r);
+    codes[j] = make_uint2(encode4(r), encode4(r + 4));
+  }
+  return s;
+}
+
 template <int TM, int NR>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t* __restrict__ x,
-                                                          const uint16_t* __restrict__ A,
-                                                          float* __restrict__ v, const int32_t* ids,
-                                                          uint32_t M, uint32_t K, uint32_t adapters,
-                                                          uint32_t rank, uint32_t ld, uint32_t parts) {
+__global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, float* __restrict__ v, QuantOut out,
+    const int32_t* ids, uint32_t M, uint32_t K, uint32_t Mp, uint32_t adapters, uint32_t rank, uint32_t ld,
+    uint32_t parts) {
   __shared__ v4f red[4][NR][64];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t l16 = lane & 15, q = lane >> 4;
-  const uint32_t m0 = blockIdx.x * 16 * TM, part = blockIdx.y;
-  const uint32_t chunks = K / 32, piece = part * 4 + wave, pieces = parts * 4;
-  const uint32_t c0 = (uint32_t)((uint64_t)piece * chunks / pieces);
-  const uint32_t c1 = (uint32_t)((uint64_t)(piece + 1) * chunks / pieces);
+  const uint32_t m0 = blockIdx.x * 16 * TM, part = blockIdx.y, G = K / kGroup;
+  const uint32_t g0 = part * G / parts, g1 = (part + 1) * G / parts;
   const uint32_t row = m0 + lane;
   uint32_t id = 0xFFFFFFFFu;
   if (lane < 16 * TM && row < M) id = (uint32_t)ids[row];
   if (id >= adapters) id = 0xFFFFFFFFu;
   uint64_t left = __builtin_amdgcn_ballot_w64(id != 0xFFFFFFFFu);
+  bool quantize = blockIdx.z == 0;
+  const uint16_t* xr[TM];
+#pragma unroll
+  for (int tm = 0; tm < TM; ++tm) xr[tm] = x + (uint64_t)min(m0 + 16 * tm + l16, M - 1) * K + 8 * q;
+
+  // One group's rows, quantized.  The stores go through buffer resources, rows
+  // past M out of range, so that no branch hides their number from the waits of
+  // the loads before them.
+  const __amdgpu_buffer_rsrc_t rQ = make_rsrc(out.q, M * K), rRm = make_rsrc(out.rm, M * G * 4);
+  const __amdgpu_buffer_rsrc_t rKm = make_rsrc(out.km, G * Mp * 4);
+  constexpr uint32_t kNoStore = 0xFFFFFF00u;  // past any bound (ceil16(M) * K < 2^32)
+  auto quant = [&](uint32_t g, const u32x4 (&xf)[TM][4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      const uint32_t m = m0 + 16 * tm + l16;
+      uint2 codes[4];
+      const float s = quant_lane_group(xf[tm], codes);
+      const uint32_t to = m < M ? m * K + g * kGroup + 8 * q : kNoStore;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes[j].x, codes[j].y}, rQ, to + 32 * j, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), rRm, q == 0 && m < M ? (m * G + g) * 4 : kNoStore, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m < M ? s : 0.0f), rKm,
+                                            q == 0 && m < Mp ? (g * Mp + m) * 4 : kNoStore, 0, 0);
+    }
+  };
+  auto load_x = [&](uint32_t g, u32x4 (&xf)[TM][4]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        xf[tm][j] = *reinterpret_cast<const u32x4*>(xr[tm] + g * kGroup + 32 * j);
+  };
+
   for (uint32_t turn = 0; left; ++turn) {
-    const uint32_t l0 = (uint32_t)__builtin_ctzll(left);
-    const uint32_t ad = (uint32_t)__builtin_amdgcn_readlane((int)id, (int)l0);
+    const uint32_t ad = (uint32_t)__builtin_amdgcn_readlane((int)id, __builtin_ctzll(left));
     const uint64_t mine = __builtin_amdgcn_ballot_w64(id == ad);
     left &= ~mine;
     if (turn % gridDim.z != blockIdx.z) continue;
-    const uint16_t *xr[TM], *ar[NR];
-#pragma unroll
-    for (int tm = 0; tm < TM; ++tm) {
-      // other rows read the adapter's first row again (cached, not stored)
-      const uint32_t r = 16 * tm + l16;
-      xr[tm] = x + (uint64_t)(m0 + (((mine >> r) & 1) ? r : l0)) * K + 8 * q;
-    }
+    const uint16_t* ar[NR];
 #pragma unroll
     for (int t = 0; t < NR; ++t)
       ar[t] = A + ((uint64_t)ad * rank + min(16 * t + l16, rank - 1)) * K + 8 * q;
@@ -64,18 +124,41 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t* __rest
     for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
       for (int t = 0; t < NR; ++t) acc[tm][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (uint32_t c = c0; c < c1; ++c) {
-      u32x4 xf[TM], af[NR];
+    // x of the next group is in flight while a group is quantized; A of the
+    // group arrives (mostly from L2) under the quantization
+    auto group = [&](auto quant_c, uint32_t g, const u32x4 (&xf)[TM][4], u32x4 (&xn)[TM][4])
+        __attribute__((always_inline)) {
+      u32x4 af[NR][4];
 #pragma unroll
-      for (int t = 0; t < NR; ++t) af[t] = *reinterpret_cast<const u32x4*>(ar[t] + c * 32);
+      for (int t = 0; t < NR; ++t)
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm) xf[tm] = *reinterpret_cast<const u32x4*>(xr[tm] + c * 32);
+        for (int j = 0; j < 4; ++j) af[t][j] = *reinterpret_cast<const u32x4*>(ar[t] + g * kGroup + 32 * j);
+      load_x(min(g + 4, g1 - 1), xn);
+      sched_fence();
+      if constexpr (decltype(quant_c)::value) quant(g, xf);
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int t = 0; t < NR; ++t) acc[tm][t] = mfma_bf16_32(af[t], xf[tm], acc[tm][t]);
-    }
+        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+          for (int t = 0; t < NR; ++t) acc[tm][t] = mfma_bf16_32(af[t][j], xf[tm][j], acc[tm][t]);
+    };
+    auto groups = [&](auto quant_c) __attribute__((always_inline)) {
+      u32x4 xe[TM][4], xo[TM][4];
+      uint32_t g = g0 + wave;
+      if (g < g1) load_x(g, xe);
+      while (g < g1) {
+        group(quant_c, g, xe, xo);
+        if ((g += 4) >= g1) break;
+        group(quant_c, g, xo, xe);
+        g += 4;
+      }
+    };
+    if (quantize)
+      groups(std::true_type{});
+    else
+      groups(std::false_type{});
+    quantize = false;
     // the four waves' sums, one row tile at a time
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
@@ -98,30 +181,37 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const uint16_t* __rest
       __syncthreads();
     }
   }
+  if (quantize) {  // no adapter among the rows
+    for (uint32_t g = g0 + wave; g < g1; g += 4) {
+      u32x4 xf[TM][4];
+      load_x(g, xf);
+      quant(g, xf);
+    }
+  }
 }
 
 // Rows up to here go in tiles of 16, their adapters dealt over workgroups;
-// beyond, in tiles of 64 (prompts: long runs of one adapter), one workgroup
+// beyond, in tiles of 32 (prompts: long runs of one adapter), one workgroup
 // taking all of a tile's.
 constexpr uint32_t kShrinkSmallM = 256;
 
 template <int TM, int NR>
-hipError_t launch_shrink_cfg(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v, uint32_t M,
-                             uint32_t K, hipStream_t s) {
+hipError_t launch_shrink_cfg(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v,
+                             const QuantOut& out, uint32_t M, uint32_t K, hipStream_t s) {
   const uint32_t tiles = (M + 16 * TM - 1) / (16 * TM);
   const uint32_t z = TM == 1 ? std::min(std::min(16u, M), l.adapters) : 1;
-  lora_shrink_kernel<TM, NR><<<dim3(tiles, l.parts, z), dim3(256), 0, s>>>(x, a, v, l.ids, M, K, l.adapters,
-                                                                          l.rank, l.ld, l.parts);
+  lora_quant_shrink_kernel<TM, NR><<<dim3(tiles, l.parts, z), dim3(256), 0, s>>>(
+      x, a, v, out, l.ids, M, K, m_pad16(M), l.adapters, l.rank, l.ld, l.parts);
   return hipGetLastError();
 }
 
 template <int TM>
-hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v, uint32_t M,
-                         uint32_t K, hipStream_t s) {
+hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v,
+                         const QuantOut& out, uint32_t M, uint32_t K, hipStream_t s) {
   // rank tiles up to ld, so that the zeros beyond the rank are written too
-  if (l.ld <= 32) return launch_shrink_cfg<TM, 2>(x, a, l, v, M, K, s);
-  if (l.ld <= 64) return launch_shrink_cfg<TM, 4>(x, a, l, v, M, K, s);
-  return launch_shrink_cfg<TM, 8>(x, a, l, v, M, K, s);
+  if (l.ld <= 32) return launch_shrink_cfg<TM, 2>(x, a, l, v, out, M, K, s);
+  if (l.ld <= 64) return launch_shrink_cfg<TM, 4>(x, a, l, v, out, M, K, s);
+  return launch_shrink_cfg<TM, 8>(x, a, l, v, out, M, K, s);
 }
 
 // ------------------------------------------------------------------------
@@ -150,7 +240,7 @@ __global__ __launch_bounds__(512) void lora_decode_kernel(Gemm g, uint32_t base,
 }
 
 template <int STAGES, bool SPLIT>
-__global__ __launch_bounds__(256) void lora_tiled_kernel(Gemm g, uint32_t tiles_m, uint32_t tiles_n,
+__global__ __launch_bounds__(256, 2) void lora_tiled_kernel(Gemm g, uint32_t tiles_m, uint32_t tiles_n,
                                                          uint32_t splits, float* __restrict__ part, LoraArgs l) {
   uint32_t tmi, tni, split = 0;
   if constexpr (SPLIT)
@@ -184,7 +274,8 @@ template <int TM, int TN, bool SPLIT>
 hipError_t launch_skinny_cfg(const Gemm& g, uint32_t grid, uint32_t base, uint32_t rem, uint32_t splits,
                              float* part, const LoraArgs& l, hipStream_t s) {
   constexpr int NWV = skinny_waves(TM, TN), U = skinny_unroll(TM, TN);
-  constexpr int LDS = NWV * TN * TM * 1024;
+  // partial sums; before them, v of the rows (64 * 528 bytes at most)
+  constexpr int LDS = std::max(NWV * TN * TM * 1024, 16 * TM * (int)(kMaxLoraRank * 4 + 16));
   const hipError_t e = allow_lds<&lora_skinny_kernel<TM, TN, NWV, U, SPLIT>, LDS>();
   if (e != hipSuccess) return e;
   const uint32_t row_tiles = (g.M + 16 * TM - 1) / (16 * TM);
@@ -250,12 +341,11 @@ hipError_t launch_pp(const Gemm& g, const LoraArgs& l, hipStream_t s) {
 
 uint32_t lora_ld(uint32_t rank) { return (rank + 31) / 32 * 32; }
 
-// Parts of K of the shrink: until about 512 workgroups (of at least 128 of K).
+// Parts of K of the shrink: as many as keep the grid within 512 workgroups (two
+// a CU, one round), with at least four groups (one a wave) in each.
 uint32_t lora_parts(uint32_t M, uint32_t K) {
-  const uint32_t wgs = M <= kShrinkSmallM ? (M + 15) / 16 * std::min(16u, M) : (M + 63) / 64;
-  uint32_t p = 1;
-  while (p < kLoraMaxParts && p * wgs < 512 && 2 * p * 128 <= K) p *= 2;
-  return p;
+  const uint32_t wgs = M <= kShrinkSmallM ? (M + 15) / 16 * std::min(16u, M) : (M + 31) / 32;
+  return std::max(1u, std::min(std::min(kLoraMaxParts, 512 / wgs), K / (4 * kGroup)));
 }
 
 }  // namespace
@@ -264,8 +354,9 @@ uint64_t lora_workspace_bytes(uint32_t M, uint32_t K, uint32_t rank) {
   return (uint64_t)M * lora_parts(M, K) * lora_ld(rank) * 4;
 }
 
-hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, void* workspace,
-                              uint32_t M, uint32_t K, uint32_t adapters, uint32_t rank, hipStream_t s) {
+hipError_t launch_lora_quant_shrink(const uint16_t* x, const uint16_t* a, const int32_t* ids, uint8_t* x_q,
+                                    float* x_s_rm, float* x_s_km, void* workspace, uint32_t M, uint32_t K,
+                                    uint32_t adapters, uint32_t rank, hipStream_t s) {
   LoraArgs l{};
   l.ids = ids;
   l.adapters = adapters;
@@ -273,7 +364,8 @@ hipError_t launch_lora_shrink(const uint16_t* x, const uint16_t* a, const int32_
   l.ld = lora_ld(rank);
   l.parts = lora_parts(M, K);
   float* v = static_cast<float*>(workspace);
-  return M <= kShrinkSmallM ? launch_shrink<1>(x, a, l, v, M, K, s) : launch_shrink<4>(x, a, l, v, M, K, s);
+  const QuantOut out{x_q, x_s_rm, x_s_km};
+  return M <= kShrinkSmallM ? launch_shrink<1>(x, a, l, v, out, M, K, s) : launch_shrink<2>(x, a, l, v, out, M, K, s);
 }
 
 hipError_t launch_lora_gemm(const uint8_t* a, const float* a_s_km, const uint8_t* w, const float* w_s,
