@@ -638,9 +638,10 @@ fp8q_status fp8q_gemm_grouped(const uint8_t *a_e4m3, const float *a_scale_km,
                               uint16_t *out_bf16, uint32_t a_rows, uint32_t R,
                               uint32_t E, uint32_t top_k, uint32_t N, uint32_t K,
                               int kernel, hipStream_t stream);
-/* Kernel fp8q_gemm_grouped takes with kernel 0 for R rows in E groups (by the
- * mean rows a group).  Pure host function; 0 if E == 0. */
-int fp8q_gemm_grouped_select(uint32_t R, uint32_t E);
+/* Kernel fp8q_gemm_grouped takes with kernel 0 for R rows in E groups and N
+ * columns on the current device (by the mean rows a group and the number of
+ * tiles); 0 if E == 0 or N is not a positive multiple of 128. */
+int fp8q_gemm_grouped_select(uint32_t R, uint32_t E, uint32_t N);
 
 /* The experts' FFN, the sparse sibling of fp8q_ffn:
  *   out[t] = bf16( sum_j weights[t][j] * y[pos[t][j]] )        (fp8q_moe_combine)

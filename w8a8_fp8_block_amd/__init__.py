@@ -108,7 +108,7 @@ _SIGS = {
     "fp8q_group_rows_workspace_bytes": (_SZ, [_U, _U]),
     "fp8q_moe_combine": (_I, [_P, _P, _P, _P, _P, _U, _U, _U, _U, _P]),
     "fp8q_gemm_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _U, _U, _U, _U, _U, _U, _I, _P]),
-    "fp8q_gemm_grouped_select": (_I, [_U, _U]),
+    "fp8q_gemm_grouped_select": (_I, [_U, _U, _U]),
     "fp8q_moe_ffn": (_I, [_P] * 13 + [_SZ, _U, _U, _U, _U, _U, _I, _P]),
     "fp8q_moe_ffn_select": (_I, [_U, _U, _U]),
     "fp8q_proj_lora": (_I, [_P] * 12 + [_SZ, _U, _U, _U, _U, _U, _P]),
@@ -474,10 +474,10 @@ def fp8q_moe_combine(y, weights, pos, offsets, out, stream=None):
     _check(lib().fp8q_moe_combine(_ptr(y), _ptr(weights), p, f, _ptr(out), T, E, k, H, _stream(stream)))
 
 
-def fp8q_gemm_grouped_select(R: int, E: int) -> int:
-    """Kernel fp8q_gemm_grouped runs with kernel=0 for R rows in E groups:
-    1 weight streaming, 2 128x128 tiles, 3 256x128 tiles."""
-    return int(lib().fp8q_gemm_grouped_select(R, E))
+def fp8q_gemm_grouped_select(R: int, E: int, N: int) -> int:
+    """Kernel fp8q_gemm_grouped runs with kernel=0 for R rows in E groups and N
+    columns: 1 weight streaming, 2 128x128 tiles, 3 256x128 tiles."""
+    return int(lib().fp8q_gemm_grouped_select(R, E, N))
 
 
 def fp8q_gemm_grouped(a, a_scale_km, w, w_scale, offsets, out, order=None, top_k: int = 1,

@@ -1201,7 +1201,9 @@ fp8q_status fp8q_moe_combine(const uint16_t* y_bf16, const float* weights, const
   return launched(fn, launch_combine(y_bf16, weights, pos, offsets, out_bf16, T, E, top_k, H, stream));
 }
 
-int fp8q_gemm_grouped_select(uint32_t R, uint32_t E) { return E == 0 ? 0 : group_gemm_auto(R, E); }
+int fp8q_gemm_grouped_select(uint32_t R, uint32_t E, uint32_t N) {
+  return E == 0 || N == 0 || N % kGroup != 0 ? 0 : group_gemm_auto(R, E, N, current_cus());
+}
 
 fp8q_status fp8q_gemm_grouped(const uint8_t* a_e4m3, const float* a_scale_km, const uint8_t* w_e4m3,
                               const float* w_scale, const int32_t* offsets, const int32_t* order,
@@ -1229,7 +1231,7 @@ fp8q_status fp8q_gemm_grouped(const uint8_t* a_e4m3, const float* a_scale_km, co
   uint32_t cus = 0;
   st = check_device(fn, &cus);
   if (st != FP8Q_OK) return st;
-  if (kernel == 0) kernel = group_gemm_auto(R, E);
+  if (kernel == 0) kernel = group_gemm_auto(R, E, N, cus);
   return launched(fn, launch_gemm_grouped(a_e4m3, a_scale_km, w_e4m3, w_scale, out_bf16, offsets, order,
                                           top_k, a_rows, R, E, N, K, cus, kernel, stream));
 }
@@ -1289,7 +1291,6 @@ fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int
   uint8_t *xq = ws + w.xq, *hq = ws + w.hq;
   float *xs = reinterpret_cast<float*>(ws + w.xs), *hs = reinterpret_cast<float*>(ws + w.hs);
   uint16_t* y = reinterpret_cast<uint16_t*>(ws + w.y);
-  const int kernel = group_gemm_auto(R, E);
   // x is quantized once a token, whatever the number of its experts
   st = run_quant(fn, x_bf16, xq, nullptr, xs, T, H, 0, stream);
   if (st != FP8Q_OK) return st;
@@ -1299,12 +1300,13 @@ fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int
   } else {
     uint16_t *g = reinterpret_cast<uint16_t*>(ws + w.g), *u = reinterpret_cast<uint16_t*>(ws + w.u);
     st = launched(fn, launch_group_gate_and_up(xq, xs, w_gate, w_gate_scale, w_up, w_up_scale, g, u, offsets,
-                                               order, top_k, T, R, E, H, I, cus, kernel, stream));
+                                               order, top_k, T, R, E, H, I, cus,
+                                               group_gemm_auto(R, E, 2 * I, cus), stream));
     if (st == FP8Q_OK) st = launched(fn, launch_silu_mul_quant(g, u, hq, hs, R, I, stream));
   }
   if (st != FP8Q_OK) return st;
   st = launched(fn, launch_gemm_grouped(hq, hs, w_down, w_down_scale, y, offsets, nullptr, 1, R, R, E, H, I, cus,
-                                        kernel, stream));
+                                        group_gemm_auto(R, E, H, cus), stream));
   if (st != FP8Q_OK) return st;
   return launched(fn, launch_combine(y, weights, pos, offsets, out_bf16, T, E, top_k, H, stream));
 }

@@ -391,24 +391,41 @@ hipError_t launch_group_pp(const uint8_t* a, const float* as, const GroupWeights
 // Kernel ids of the grouped product
 constexpr int kGroupStream = 1, kGroupTiled = 2, kGroupPp = 3;
 
-int group_auto(uint32_t R, uint32_t E) {
-  const uint32_t mean = R / (R < E ? R : E);  // rows per expert at least
-  return mean < 14 ? kGroupStream : mean < 192 ? kGroupTiled : kGroupPp;
+// By the mean rows an expert: streaming below kTiledMinRows (and below
+// kFewTilesMaxRows where 128-column tiles would not give every CU one), 128 x 128
+// tiles below kPpMinRows, else 256 x 128.  E = 32, N x K = 2048 x 5120, us,
+// streaming / 128 x 128: mean 12: 54.8 / 57.6, 16: 61.6 / 59.3, 32: 85 / 65;
+// E = 8, mean 16 (128 tiles): 21.4 / 39.9.
+constexpr uint32_t kTiledMinRows = 14, kFewTilesMaxRows = 64, kPpMinRows = 192;
+
+int group_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus) {
+  const uint32_t groups = R < E ? R : E;
+  if (groups == 0) return kGroupStream;
+  const uint32_t mean = R / groups;
+  const bool few = (uint64_t)groups * (N / 128) < cus;
+  if (mean < (few ? kFewTilesMaxRows : kTiledMinRows)) return kGroupStream;
+  return mean < kPpMinRows ? kGroupTiled : kGroupPp;
 }
 
-// One row tile holds up to this many rows an expert on average: 16-row tiles
-// (then stages of 64 columns x 2 K blocks), else 32-row ones (128 x 1).
-// Measured at E = 32, N x K = 2048 x 5120 / 5120 x 2048 (335 MB of weights), us:
-// mean 2: 45.4 / 44.7 (16 rows) against 43.1 / 44.3 (32), mean 8: 59.9 / 59.0
-// against 54.3 / 54.2; at E = 64, mean 1.5, N = 1408 and 5120 the 16-row
-// form takes 171 us for the expert FFN against 189.
-constexpr uint32_t kStreamFewRows = 4;
+// The streaming form.  Rows a tile: 16 up to a mean of kStreamFewRows rows an
+// expert, else 32.  A stage is 16 KB of weights: 128 columns x 1 K block where
+// every worker has at least kWideGranules granules, 64 x 2 from kMidGranules on,
+// else 32 x 4 (narrower stages would leave waves without columns).  us at
+// 64 x 2 / 128 x 1 / 32 x 4: E = 32, N x K = 2048 x 5120 (16 granules a worker),
+// mean 8: 60.7 / 54.3 / -; E = 8 (4 granules), mean 2: 14.8 / 14.9 / 15.3;
+// E = 4 (2 granules), mean 2: 11.4 / 11.4 / 8.7; one expert, N x K = 5120 x
+// 17408, 16 rows: 32.7 / 53.3 / 23.5.
+constexpr uint32_t kStreamFewRows = 4, kWideGranules = 6, kMidGranules = 3;
 
 hipError_t launch_stream_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                              const Groups& g, uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
+  const uint64_t per_worker = (uint64_t)(g.R < g.E ? g.R : g.E) * sets * (N / 16) / cus;
   if ((uint64_t)g.R <= (uint64_t)kStreamFewRows * g.E)
-    return launch_stream<1, 1, 4, 2>(a, as, gw, sets, g, N, K, cus, s);
-  return launch_stream<2, 1, 8, 1>(a, as, gw, sets, g, N, K, cus, s);
+    return per_worker >= kMidGranules ? launch_stream<1, 1, 4, 2>(a, as, gw, sets, g, N, K, cus, s)
+                                      : launch_stream<1, 1, 2, 4>(a, as, gw, sets, g, N, K, cus, s);
+  if (per_worker >= kWideGranules) return launch_stream<2, 1, 8, 1>(a, as, gw, sets, g, N, K, cus, s);
+  return per_worker >= kMidGranules ? launch_stream<2, 1, 4, 2>(a, as, gw, sets, g, N, K, cus, s)
+                                    : launch_stream<2, 1, 2, 4>(a, as, gw, sets, g, N, K, cus, s);
 }
 
 hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
@@ -429,7 +446,7 @@ Groups make_groups(const int32_t* offsets, const int32_t* order, uint32_t E, uin
 
 }  // namespace
 
-int group_gemm_auto(uint32_t R, uint32_t E) { return group_auto(R, E); }
+int group_gemm_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus) { return group_auto(R, E, N, cus); }
 
 hipError_t launch_gemm_grouped(const uint8_t* a, const float* a_s_km, const uint8_t* w,
                                const float* w_s, uint16_t* out, const int32_t* offsets,
