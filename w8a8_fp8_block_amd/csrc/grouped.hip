@@ -90,7 +90,31 @@ struct UnitCursor {
   }
 };
 
-template <int TM, int TN, int CW, int KS>
+// e4m3 codes -> f16, exactly: 8 of a lane's 32 codes of a K block (step s of 4)
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v8h codes_f16(const v8i& c, int s) {
+  v8h h;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const v2h a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * s + i], 1.0f, false);
+    const v2h b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * s + i], 1.0f, true);
+    h[4 * i] = a[0];
+    h[4 * i + 1] = a[1];
+    h[4 * i + 2] = b[0];
+    h[4 * i + 3] = b[1];
+  }
+  return h;
+}
+
+// F16: the products of a K block by f16 MFMAs on the widened codes.  The FP8
+// MFMA's 128-deep sums are off by 1.4e-5 of their RMS (its products are summed
+// to about 16 bits; the same for the 32-deep form), the f16 one's by 1e-8.
+// Where the result is rounded to bf16 and quantized again, as gate and up are,
+// that moves values across rounding boundaries: with few rows the expert FFN's
+// output was up to 6.6e-3 from its 64-bit value, against 1.7e-3 with f16.  The
+// conversions and the slower MFMA hide under the weight stream.
+template <int TM, int TN, int CW, int KS, bool F16>
 __global__ __launch_bounds__(64 * CW * KS) void group_stream_kernel(const uint8_t* __restrict__ A,
                                                            const float* __restrict__ As, GroupWeights gw,
                                                            uint32_t sets, Groups g, uint32_t N, uint32_t K,
@@ -277,7 +301,17 @@ __global__ __launch_bounds__(64 * CW * KS) void group_stream_kernel(const uint8_
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
-        for (int t = 0; t < TN; ++t) r[tm][t] = mfma_e4m3_128(wf[t], af[tm]);
+        for (int t = 0; t < TN; ++t) {
+          if constexpr (F16) {
+            r[tm][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              r[tm][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(wf[t], i), codes_f16(af[tm], i), r[tm][t],
+                                                                0, 0, 0);
+          } else {
+            r[tm][t] = mfma_e4m3_128(wf[t], af[tm]);
+          }
+        }
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
@@ -301,16 +335,16 @@ hipError_t allow_lds(std::atomic<bool>& done, F* kernel, int bytes) {
   return e;
 }
 
-template <int TM, int TN, int CW, int KS>
+template <int TM, int TN, int CW, int KS, bool F16>
 hipError_t launch_stream(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                          const Groups& g, uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
   using C = StreamCfg<TM, TN, CW, KS>;
   static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_stream_kernel<TM, TN, CW, KS>, C::LDS);
+  const hipError_t e = allow_lds(done, &group_stream_kernel<TM, TN, CW, KS, F16>, C::LDS);
   if (e != hipSuccess) return e;
   const uint64_t units = (uint64_t)max_row_tiles(g.R, g.E, 16 * TM) * sets * (N / (16 * TN));
   const uint32_t grid = (uint32_t)(units < cus ? units : cus);
-  group_stream_kernel<TM, TN, CW, KS>
+  group_stream_kernel<TM, TN, CW, KS, F16>
       <<<dim3(grid), dim3(64 * C::NW), C::LDS, s>>>(a, as, gw, sets, g, N, K, m_pad16(g.a_rows));
   return hipGetLastError();
 }
@@ -417,21 +451,24 @@ int group_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus) {
 // 17408, 16 rows: 32.7 / 53.3 / 23.5.
 constexpr uint32_t kStreamFewRows = 4, kWideGranules = 6, kMidGranules = 3;
 
+template <bool F16>
 hipError_t launch_stream_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                              const Groups& g, uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
   const uint64_t per_worker = (uint64_t)(g.R < g.E ? g.R : g.E) * sets * (N / 16) / cus;
   if ((uint64_t)g.R <= (uint64_t)kStreamFewRows * g.E)
-    return per_worker >= kMidGranules ? launch_stream<1, 1, 4, 2>(a, as, gw, sets, g, N, K, cus, s)
-                                      : launch_stream<1, 1, 2, 4>(a, as, gw, sets, g, N, K, cus, s);
-  if (per_worker >= kWideGranules) return launch_stream<2, 1, 8, 1>(a, as, gw, sets, g, N, K, cus, s);
-  return per_worker >= kMidGranules ? launch_stream<2, 1, 4, 2>(a, as, gw, sets, g, N, K, cus, s)
-                                    : launch_stream<2, 1, 2, 4>(a, as, gw, sets, g, N, K, cus, s);
+    return per_worker >= kMidGranules ? launch_stream<1, 1, 4, 2, F16>(a, as, gw, sets, g, N, K, cus, s)
+                                      : launch_stream<1, 1, 2, 4, F16>(a, as, gw, sets, g, N, K, cus, s);
+  if (per_worker >= kWideGranules) return launch_stream<2, 1, 8, 1, F16>(a, as, gw, sets, g, N, K, cus, s);
+  return per_worker >= kMidGranules ? launch_stream<2, 1, 4, 2, F16>(a, as, gw, sets, g, N, K, cus, s)
+                                    : launch_stream<2, 1, 2, 4, F16>(a, as, gw, sets, g, N, K, cus, s);
 }
 
 hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                       const Groups& g, uint32_t N, uint32_t K, uint32_t cus, int kernel, hipStream_t s) {
   switch (kernel) {
-    case kGroupStream: return launch_stream_any(a, as, gw, sets, g, N, K, cus, s);
+    case kGroupStream:  // (two sets: gate and up)
+      return sets == 2 ? launch_stream_any<true>(a, as, gw, sets, g, N, K, cus, s)
+                       : launch_stream_any<false>(a, as, gw, sets, g, N, K, cus, s);
     case kGroupTiled:
       return g.R < 64ull * g.E ? launch_group_128<kStreamOnce>(a, as, gw, sets, g, N, K, s)
                                : launch_group_128<0>(a, as, gw, sets, g, N, K, s);
