@@ -40,7 +40,7 @@ import os
 # library asks for "libamdhip64.so.7"; loading torch's runtime first lets the
 # dynamic linker satisfy ours with the same object (matching soname), so one
 # HIP runtime serves both.  The other order would load a second runtime.
-import torch  # noqa: F401  (device memory and streams)
+import torch  # (device memory and streams)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp8q.so")
@@ -153,7 +153,6 @@ def _check(st: int):
 
 
 def _ptr(t) -> int:
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError("expected a torch.Tensor")
     if not t.is_cuda:
@@ -176,12 +175,13 @@ def _stream(stream=None) -> int:
     where the build has it: ~0.4 us against ~2.7 us for building a Stream
     object, per call, on the host)."""
     global _raw_stream
-    import torch
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is None:
         q = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _raw_stream = ((lambda: q(torch.cuda.current_device())) if q is not None
+        dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        torch.cuda.current_device()  # initialises torch's device state
+        _raw_stream = ((lambda: q(dev())) if q is not None
                        else (lambda: torch.cuda.current_stream().cuda_stream))
     return _raw_stream()
 
@@ -403,23 +403,17 @@ def fp8q_ffn(x, w_gate, w_gate_scale, w_up, w_up_scale, w_down, w_down_scale, ou
                          _stream(stream)))
 
 
-def _int32(t, what):
-    import torch
-    if t.dtype != torch.int32:
-        raise TypeError(f"{what} must be int32, got {t.dtype}")
+def _of(t, dtype, n, what) -> int:
+    """Pointer of a tensor of `dtype` with n elements."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.numel() != n:
+        raise ValueError(f"{what} has {t.numel()} elements, {n} needed")
     return _ptr(t)
 
 
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
-
-
-def _grouping(order, pos, offsets, R, E):
-    """Pointers of a grouping of R slots into E groups (each may be None)."""
-    for t, n, what in ((order, R, "order"), (pos, R, "pos"), (offsets, E + 1, "offsets")):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{what} has {t.numel()} elements, {n} needed")
-    return [0 if t is None else _int32(t, w) for t, w in ((order, "order"), (pos, "pos"), (offsets, "offsets"))]
 
 
 def fp8q_moe_route_workspace_bytes(T: int, E: int, top_k: int) -> int:
@@ -433,19 +427,20 @@ def fp8q_moe_route(logits, ids, weights, order, pos, offsets, workspace, renorma
     float32, order and pos [T*top_k] int32, offsets [E+1] int32; workspace: a
     device tensor of fp8q_moe_route_workspace_bytes(T, E, top_k) bytes, or
     None when that is 0."""
-    import torch
     T, E = _dims(logits, 2)
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    k = _dims(ids, 2)[1]
+    bf16 = logits.dtype is torch.bfloat16
+    if not bf16 and logits.dtype is not torch.float32:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    T2, k = _dims(ids, 2)
-    if T2 != T or _dims(weights, 2) != (T, k):
-        raise ValueError("logits, ids and weights disagree in shape")
-    if weights.dtype != torch.float32:
-        raise TypeError(f"weights must be float32, got {weights.dtype}")
-    o, p, f = _grouping(order, pos, offsets, T * k, E)
-    _check(lib().fp8q_moe_route(_ptr(logits), int(logits.dtype == torch.bfloat16), _int32(ids, "ids"),
-                               _ptr(weights), o, p, f, _optr(workspace), _nbytes(workspace), T, E, k,
-                               int(bool(renormalize)), _stream(stream)))
+    if ids.shape != weights.shape:
+        raise ValueError("ids and weights disagree in shape")
+    R, i32 = T * k, torch.int32
+    st = lib().fp8q_moe_route(_ptr(logits), bf16, _of(ids, i32, R, "ids"), _of(weights, torch.float32, R, "weights"),
+                              _of(order, i32, R, "order"), _of(pos, i32, R, "pos"),
+                              _of(offsets, i32, E + 1, "offsets"), _optr(workspace), _nbytes(workspace), T, E, k,
+                              bool(renormalize), _stream(stream))
+    if st:
+        _check(st)
 
 
 def fp8q_group_rows_workspace_bytes(n: int, groups: int) -> int:
@@ -456,9 +451,9 @@ def fp8q_group_rows(ids, order, pos, offsets, workspace, stream=None):
     """The grouping of given ids (any shape, int32) into offsets.numel() - 1
     groups; ids outside them come last.  workspace: a device tensor of
     fp8q_group_rows_workspace_bytes(n, groups) bytes, or None when that is 0."""
-    n, groups = ids.numel(), offsets.numel() - 1
-    o, p, f = _grouping(order, pos, offsets, n, groups)
-    _check(lib().fp8q_group_rows(_int32(ids, "ids"), o, p, f, _optr(workspace), _nbytes(workspace), n,
+    n, groups, i32 = ids.numel(), offsets.numel() - 1, torch.int32
+    _check(lib().fp8q_group_rows(_of(ids, i32, n, "ids"), _of(order, i32, n, "order"), _of(pos, i32, n, "pos"),
+                                _of(offsets, i32, groups + 1, "offsets"), _optr(workspace), _nbytes(workspace), n,
                                 groups, _stream(stream)))
 
 
@@ -470,8 +465,9 @@ def fp8q_moe_combine(y, weights, pos, offsets, out, stream=None):
     if R != T * k or _dims(out, 2) != (T, H):
         raise ValueError("y, weights and out disagree in shape")
     E = offsets.numel() - 1
-    _, p, f = _grouping(None, pos, offsets, R, E)
-    _check(lib().fp8q_moe_combine(_ptr(y), _ptr(weights), p, f, _ptr(out), T, E, k, H, _stream(stream)))
+    _check(lib().fp8q_moe_combine(_ptr(y), _of(weights, torch.float32, R, "weights"),
+                                 _of(pos, torch.int32, R, "pos"), _of(offsets, torch.int32, E + 1, "offsets"),
+                                 _ptr(out), T, E, k, H, _stream(stream)))
 
 
 def fp8q_gemm_grouped_select(R: int, E: int, N: int) -> int:
@@ -493,8 +489,9 @@ def fp8q_gemm_grouped(a, a_scale_km, w, w_scale, offsets, out, order=None, top_k
         raise ValueError("a, w and out disagree in shape")
     if _dims(w_scale, 3) != (E, N // 128, K // 128) or _dims(a_scale_km, 2) != (K // 128, (rows + 15) // 16 * 16):
         raise ValueError("a scale tensor's shape does not match")
-    o, _, f = _grouping(order, None, offsets, R, E)
-    _check(lib().fp8q_gemm_grouped(_ptr(a), _ptr(a_scale_km), _ptr(w), _ptr(w_scale), f, o, _ptr(out), rows,
+    _check(lib().fp8q_gemm_grouped(_ptr(a), _ptr(a_scale_km), _ptr(w), _ptr(w_scale),
+                                  _of(offsets, torch.int32, E + 1, "offsets"),
+                                  0 if order is None else _of(order, torch.int32, R, "order"), _ptr(out), rows,
                                   R, E, top_k, N, K, kernel, _stream(stream)))
 
 
@@ -522,8 +519,9 @@ def fp8q_moe_ffn(x, weights, order, pos, offsets, w_gate, w_gate_scale, w_up, w_
     if not (_dims(w_gate_scale, 3) == _dims(w_up_scale, 3) == (E, I // 128, H // 128)
             and _dims(w_down_scale, 3) == (E, H // 128, I // 128)):
         raise ValueError("a scale tensor's shape does not match")
-    o, p, f = _grouping(order, pos, offsets, T * k, E)
-    _check(lib().fp8q_moe_ffn(_ptr(x), _ptr(weights), o, p, f, _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up),
+    R, i32 = T * k, torch.int32
+    _check(lib().fp8q_moe_ffn(_ptr(x), _of(weights, torch.float32, R, "weights"), _of(order, i32, R, "order"),
+                             _of(pos, i32, R, "pos"), _of(offsets, i32, E + 1, "offsets"), _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up),
                              _ptr(w_up_scale), _ptr(w_down), _ptr(w_down_scale), _ptr(out), _optr(workspace),
                              _nbytes(workspace), T, E, k, H, I, variant, _stream(stream)))
 
@@ -539,18 +537,14 @@ def fp8q_proj_lora(x, w, w_scale, lora_a, lora_b, lora_scale, adapter_ids, out, 
     (outside 0..n-1: none).  lora_a [n,rank,K], lora_b [n,N,rank] bf16,
     lora_scale [n] float32, adapter_ids [M] int32; workspace: a device byte
     tensor of fp8q_proj_lora_workspace_bytes(M, N, K, rank)."""
-    import torch
     M, K = _dims(x, 2)
     N, K2 = _dims(w, 2)
     n, R, K3 = _dims(lora_a, 3)
     if K2 != K or K3 != K or _dims(lora_b, 3) != (n, N, R) or _dims(out, 2) != (M, N):
         raise ValueError("x, w, the adapters and out disagree in shape")
-    if lora_scale.numel() != n or adapter_ids.numel() != M:
-        raise ValueError("lora_scale or adapter_ids has the wrong length")
-    if lora_scale.dtype != torch.float32:
-        raise TypeError(f"lora_scale must be float32, got {lora_scale.dtype}")
-    _check(lib().fp8q_proj_lora(_ptr(x), _ptr(w), _ptr(w_scale), _ptr(lora_a), _ptr(lora_b), _ptr(lora_scale),
-                               _int32(adapter_ids, "adapter_ids"), _ptr(out), _ptr(act_q), _ptr(act_scale),
+    _check(lib().fp8q_proj_lora(_ptr(x), _ptr(w), _ptr(w_scale), _ptr(lora_a), _ptr(lora_b),
+                               _of(lora_scale, torch.float32, n, "lora_scale"),
+                               _of(adapter_ids, torch.int32, M, "adapter_ids"), _ptr(out), _ptr(act_q), _ptr(act_scale),
                                _ptr(act_scale_km), _optr(workspace), _nbytes(workspace), M, N, K, n, R,
                                _stream(stream)))
 

@@ -37,11 +37,25 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return max(a, b);
 }
 
-__device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+// sum over the wave, uniform: as the maximum, within 16-lane rows by DPP, the
+// rows in order
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
 }
+__device__ __forceinline__ float lane_f32(float v, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), lane));
+}
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  v += dpp_f32<0x141>(v);
+  v += dpp_f32<0x140>(v);
+  return (lane_f32(v, 0) + lane_f32(v, 16)) + (lane_f32(v, 32) + lane_f32(v, 48));
+}
+
+// e^x, x <= 0 (2 ulp; below e^-87 the result may be flushed to zero)
+__device__ __forceinline__ float exp_neg(float x) { return exp_f32(fmaxf(x, -110.0f)); }
 
 // Finite logits as unsigned keys in the same order, all above kNoKey; -inf and
 // NaN are kNoKey (never chosen), +inf counts as the largest finite value.
@@ -94,9 +108,12 @@ __device__ __forceinline__ void scan_groups(uint32_t* total, uint32_t* wave_tot,
   __syncthreads();
 }
 
-// This wave's slots [s0, s1): place = the stored rank + its wave's and its
-// group's first place (group e's in base[e], which for a block of many also
-// holds the blocks before).
+// A wave's slots are few enough to stay in LDS (group and rank) up to this
+// many; beyond, ids and pos hold them.
+constexpr uint32_t kLdsSlots = 128;
+
+// This wave's slots [s0, s1) of a lone workgroup: place = the stored rank + its
+// wave's and its group's first place.
 __device__ __forceinline__ void place_slots(const int32_t* ids, int32_t* order, int32_t* pos,
                                             const uint32_t* cnt, const uint32_t* base, uint32_t s0,
                                             uint32_t s1, uint32_t groups) {
@@ -126,27 +143,38 @@ template <int NV>
 __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   extern __shared__ uint32_t lds[];
   const uint32_t EB = a.E + 1;
-  uint32_t *cnt = lds, *total = lds + kWaves * EB, *wave_tot = total + EB;
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint32_t i = threadIdx.x; i < kWaves * EB; i += kThreads) cnt[i] = 0;
-  __syncthreads();
-  uint32_t* mine = cnt + wave * EB;
+  uint32_t *cnt = lds, *total = lds + kWaves * EB, *wave_tot = total + EB, *slots = wave_tot + kWaves;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint64_t first = ((uint64_t)blockIdx.x * kWaves + wave) * a.per_wave;
   const uint32_t t0 = (uint32_t)min(first, (uint64_t)a.T);
   const uint32_t t1 = (uint32_t)min(first + a.per_wave, (uint64_t)a.T);
+  float raw[NV];  // the next token's logits
+  auto load = [&](uint32_t t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t e = 64 * i + lane;
+      const uint64_t at = (uint64_t)t * a.E + min(e, a.E - 1);
+      const float l = a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16)
+                             : static_cast<const float*>(a.logits)[at];
+      raw[i] = e < a.E ? l : -INFINITY;
+    }
+  };
+  if (t0 < t1) load(t0);
+  for (uint32_t i = threadIdx.x; i < kWaves * EB; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  uint32_t* mine = cnt + wave * EB;
+  slots += wave * kLdsSlots;
+  const bool in_lds = a.per_wave * a.k <= kLdsSlots;
   for (uint32_t t = t0; t < t1; ++t) {
     uint32_t key[NV];
     float l[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const uint32_t e = 64 * i + lane;
-      const uint64_t at = (uint64_t)t * a.E + e;
-      l[i] = -INFINITY;
-      if (e < a.E)
-        l[i] = clean_logit(a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[at] << 16)
-                                  : static_cast<const float*>(a.logits)[at]);
+      l[i] = clean_logit(raw[i]);
       key[i] = logit_key(l[i]);
     }
+    load(min(t + 1, t1 - 1));
     uint32_t my_key = kNoKey, my_id = 0xFFFFFFFFu, top = kNoKey;  // lane j: the j-th choice
     for (uint32_t j = 0; j < a.k; ++j) {
       uint32_t best = key[0];
@@ -170,12 +198,12 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       }
     }
     const float lmax = top == kNoKey ? 0.0f : key_logit(top);
-    const float ex = my_key == kNoKey ? 0.0f : expf(key_logit(my_key) - lmax);
+    const float ex = my_key == kNoKey ? 0.0f : exp_neg(key_logit(my_key) - lmax);
     float sum = ex;
     if (!a.renorm) {
       sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) sum += l[i] == -INFINITY ? 0.0f : expf(l[i] - lmax);
+      for (int i = 0; i < NV; ++i) sum += l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - lmax);
     }
     sum = wave_sum_f32(sum);
     // ranks within the wave: a token's experts differ, so every counter has
@@ -187,7 +215,11 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
       a.ids[s] = (int32_t)my_id;
       a.weights[s] = my_key == kNoKey ? 0.0f : ex / sum;
       const uint32_t e = none ? a.E : my_id, c = mine[e];
-      a.pos[s] = (int32_t)(none ? c + (uint32_t)__builtin_popcountll(nones & ((1ull << lane) - 1)) : c);
+      const uint32_t rank = none ? c + (uint32_t)__builtin_popcountll(nones & ((1ull << lane) - 1)) : c;
+      if (in_lds)
+        slots[(t - t0) * a.k + lane] = rank << 16 | e;  // rank < kLdsSlots
+      else
+        a.pos[s] = (int32_t)rank;
       if (!none) mine[e] = c + 1;
     }
     if (lane == 0 && nones) mine[a.E] += (uint32_t)__builtin_popcountll(nones);
@@ -197,11 +229,23 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a) {
   if (a.lone) {
     scan_groups(total, wave_tot, EB);
     for (uint32_t e = threadIdx.x; e < EB; e += kThreads) a.offsets[e] = (int32_t)total[e];
-    place_slots(a.ids, a.order, a.pos, mine, total, t0 * a.k, t1 * a.k, a.E);
   } else {
-    for (uint32_t s = t0 * a.k + lane; s < t1 * a.k; s += 64)
-      a.pos[s] += (int32_t)mine[min((uint32_t)a.ids[s], a.E)];
     for (uint32_t e = threadIdx.x; e < EB; e += kThreads) a.hist[blockIdx.x * EB + e] = total[e];
+  }
+  // places (a lone workgroup) or ranks within the block
+  for (uint32_t i = lane; i < (t1 - t0) * a.k; i += 64) {
+    const uint32_t s = t0 * a.k + i;
+    uint32_t rank, e;
+    if (in_lds) {
+      rank = slots[i] >> 16;
+      e = slots[i] & 0xFFFF;
+    } else {
+      rank = (uint32_t)a.pos[s];
+      e = min((uint32_t)a.ids[s], a.E);
+    }
+    rank += mine[e] + (a.lone ? total[e] : 0);
+    a.pos[s] = (int32_t)rank;
+    if (a.lone) a.order[rank] = (int32_t)s;
   }
 }
 
@@ -259,16 +303,23 @@ __global__ __launch_bounds__(kThreads) void place_kernel(const int32_t* ids, int
   extern __shared__ uint32_t lds[];
   const uint32_t EB = groups + 1, nb = gridDim.x, b = blockIdx.x;
   uint32_t *total = lds, *before = lds + EB, *wave_tot = before + EB, *zero = wave_tot + kWaves;
+  constexpr uint32_t kAhead = 16;
   const uint32_t parts = kThreads / EB;  // >= 1: groups < kThreads
   const uint32_t e = threadIdx.x % EB, part = threadIdx.x / EB;
   uint32_t *pt = zero + EB, *pb = pt + kThreads;  // partial sums per thread
   if (part < parts) {
     uint32_t st = 0, sb = 0;
-#pragma unroll 4
-    for (uint32_t r = part; r < nb; r += parts) {
-      const uint32_t c = hist[r * EB + e];
-      st += c;
-      sb += r < b ? c : 0;
+    // all of a thread's counts in flight at once (kMaxBlocks of them at most)
+    for (uint32_t r0 = part; r0 < nb; r0 += kAhead * parts) {
+      uint32_t c[kAhead];
+#pragma unroll
+      for (uint32_t i = 0; i < kAhead; ++i) c[i] = hist[min(r0 + i * parts, nb - 1) * EB + e];
+#pragma unroll
+      for (uint32_t i = 0; i < kAhead; ++i) {
+        const uint32_t r = r0 + i * parts;
+        st += r < nb ? c[i] : 0;
+        sb += r < b ? c[i] : 0;
+      }
     }
     pt[threadIdx.x] = st;
     pb[threadIdx.x] = sb;
@@ -333,6 +384,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
 }
 
 uint32_t count_lds(uint32_t groups) { return (kWaves * (groups + 1) + (groups + 1) + kWaves) * 4; }
+uint32_t route_lds(uint32_t groups) { return count_lds(groups) + kWaves * kLdsSlots * 4; }
 uint32_t place_lds(uint32_t groups) { return (3 * (groups + 1) + kWaves + 2 * kThreads) * 4; }
 
 // tokens (slots) a wave and workgroups for n of them
@@ -377,7 +429,7 @@ hipError_t launch_route(const void* logits, bool bf16, int32_t* ids, float* weig
   RouteArgs a{logits, ids, order, pos, offsets, weights, static_cast<uint32_t*>(workspace), T, E,
               top_k, per_wave, bf16, renorm, blocks == 1};
   const dim3 grid(blocks), block(kThreads);
-  const uint32_t lds = count_lds(E);
+  const uint32_t lds = route_lds(E);
   if (E <= 64) route_kernel<1><<<grid, block, lds, s>>>(a);
   else if (E <= 128) route_kernel<2><<<grid, block, lds, s>>>(a);
   else if (E <= 256) route_kernel<4><<<grid, block, lds, s>>>(a);
