@@ -4,8 +4,7 @@
 // with P the 128-deep e4m3 dot products of the dense GEMM (gemm.hip).
 #include <atomic>
 
-#include "gemm_pp.h"
-#include "group_tiles.h"
+#include "group_pp.h"
 
 namespace fp8q {
 namespace {
@@ -422,6 +421,18 @@ hipError_t launch_group_pp(const uint8_t* a, const float* as, const GroupWeights
   return hipGetLastError();
 }
 
+hipError_t launch_group_persist(const uint8_t* a, const float* as, const GroupWeights& gw, const Groups& g,
+                                uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
+  static std::atomic<bool> done{false};
+  const hipError_t e = allow_lds(done, &group_persist_kernel, PersistCfg::LDS);
+  if (e != hipSuccess) return e;
+  const uint32_t tiles_n = (N + 255) / 256;
+  const uint64_t most = (uint64_t)max_row_tiles(g.R, g.E, 128) * tiles_n;
+  group_persist_kernel<<<dim3((uint32_t)(most < cus ? most : cus)), dim3(512), PersistCfg::LDS, s>>>(
+      a, as, gw.w[0], gw.ws[0], gw.out[0], g, N, K, m_pad16(g.a_rows), tiles_n);
+  return hipGetLastError();
+}
+
 // Kernel ids of the grouped product
 constexpr int kGroupStream = 1, kGroupTiled = 2, kGroupPp = 3;
 
@@ -472,7 +483,10 @@ hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw,
     case kGroupTiled:
       return g.R < 64ull * g.E ? launch_group_128<kStreamOnce>(a, as, gw, sets, g, N, K, s)
                                : launch_group_128<0>(a, as, gw, sets, g, N, K, s);
-    default: return launch_group_pp(a, as, gw, sets, g, N, K, s);
+    default:
+      if (sets == 1 && g.E <= kPersistMaxExperts && K >= kPersistMinBlocks * kGroup)
+        return launch_group_persist(a, as, gw, g, N, K, cus, s);
+      return launch_group_pp(a, as, gw, sets, g, N, K, s);
   }
 }
 
