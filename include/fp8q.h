@@ -627,8 +627,9 @@ fp8q_status fp8q_moe_combine(const uint16_t *y_bf16, const float *weights,
  *   w_e4m3       [E,N,K], w_scale [E,N/128,K/128]
  *   out_bf16     [R,N]: rows of no expert (p >= offsets[E]) are left as they are
  *   kernel       0 automatic (fp8q_gemm_grouped_select), 1 weight streaming,
- *                2 128x128 tiles, 3 256x128 tiles; 2 and 3 give the same
- *                results, 1 may differ in the order of the fp32 sums
+ *                2 128x128 tiles, 3 persistent workgroups over 128x256 tiles (2
+ *                runs in its place for E > 256 or K < 512); 2 and 3 give the
+ *                same results, 1 may differ in the order of the fp32 sums
  * N % 128 == 0, K % 128 == 0, 1 <= E <= FP8Q_MAX_EXPERTS; element counts of a,
  * out and one expert's weights below 2^32 (the whole of w may be larger).
  * Plans that are not groupings give unspecified rows, in bounds. */
@@ -655,8 +656,7 @@ int fp8q_gemm_grouped_select(uint32_t R, uint32_t E, uint32_t N);
  *   out_bf16 [T,H]
  *   workspace of fp8q_moe_ffn_workspace_bytes(...) bytes, 16-byte aligned
  *   variant  0 automatic, 1 fused gate/up kernel, 2 separate gate and up;
- *            0 takes 1 from a mean of fp8q_moe_ffn's own threshold of rows an
- *            expert (fp8q_moe_ffn_select)
+ *            0 takes 1 from a mean of 32 rows an expert (fp8q_moe_ffn_select)
  * H % 128 == 0, I % 128 == 0.  x is quantized once a token.  Limits as
  * fp8q_gemm_grouped (with R = T*top_k rows of H and of I). */
 fp8q_status fp8q_moe_ffn(const uint16_t *x_bf16, const float *weights,

@@ -472,7 +472,7 @@ def fp8q_moe_combine(y, weights, pos, offsets, out, stream=None):
 
 def fp8q_gemm_grouped_select(R: int, E: int, N: int) -> int:
     """Kernel fp8q_gemm_grouped runs with kernel=0 for R rows in E groups and N
-    columns: 1 weight streaming, 2 128x128 tiles, 3 256x128 tiles."""
+    columns: 1 weight streaming, 2 128x128 tiles, 3 persistent 128x256 tiles."""
     return int(lib().fp8q_gemm_grouped_select(R, E, N))
 
 

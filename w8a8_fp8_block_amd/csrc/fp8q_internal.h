@@ -164,7 +164,7 @@ hipError_t launch_combine(const uint16_t* y, const float* weights, const int32_t
 // Sorted rows p of expert e (offsets[e] <= p < offsets[e + 1]) read activation
 // row order[p] / per_row (order NULL: row p) of a_rows; weights w [E, N, K]
 // with block scales [E, N/128, K/128]; out [R, N].  Kernel ids: 1 weight
-// streaming, 2 128 x 128 tiles, 3 ping-pong 256 x 128 tiles; group_gemm_auto
+// streaming, 2 128 x 128 tiles, 3 persistent ping-pong 128 x 256 tiles; group_gemm_auto
 // picks by the mean rows an expert and the number of tiles.
 int group_gemm_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus);
 hipError_t launch_gemm_grouped(const uint8_t* a, const float* a_s_km, const uint8_t* w,

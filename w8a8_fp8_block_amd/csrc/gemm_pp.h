@@ -178,7 +178,7 @@ __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* 
   }
 }
 
-template <int STAGES, bool ROW, bool FFN, class Rows, class Epi>
+template <int STAGES, bool ROW, bool FFN, class Rows, class Epi, int WAUX = 0>
 __device__ __forceinline__ void gemm_pp_body(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t m0, uint32_t n0, uint32_t N,
@@ -251,8 +251,10 @@ __device__ __forceinline__ void gemm_pp_body(
     unroll_seq(
         [&](auto jc) {
           constexpr int J = decltype(jc)::value;
-          if constexpr (FFN)
-            dma16(J < 4 ? rA : rW2, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
+          if constexpr (FFN && J >= 4)
+            dma16_aux<WAUX>(rW2, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
+          else if constexpr (FFN)
+            dma16(rA, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
           else
             dma16(g0_act ? rA : rW, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
         },
@@ -263,7 +265,10 @@ __device__ __forceinline__ void gemm_pp_body(
     unroll_seq(
         [&](auto jc) {
           constexpr int J = decltype(jc)::value;
-          dma16(FFN ? rW : rA, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
+          if constexpr (FFN)
+            dma16_aux<WAUX>(rW, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
+          else
+            dma16(rA, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
         },
         std::make_integer_sequence<int, CH1>{});
     dma4(rS, s_off, kb * Mp * 4, base + my_sc);

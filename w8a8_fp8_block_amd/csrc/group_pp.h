@@ -36,6 +36,8 @@ struct PersistCfg {
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
+// WAUX: the weights' cache policy.
+template <int WAUX>
 __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __restrict__ A,
                                                             const float* __restrict__ As,
                                                             const uint8_t* __restrict__ W,
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
             if constexpr (grp == 0 && J < 4)
               dma16_at(rA, c_off[J], kb * kGroup, lds + chunk(J) * 1024);
             else
-              dma16_at(rW, c_off[J], kb * kGroup, lds + chunk(J) * 1024);
+              dma16_at_aux<WAUX>(rW, c_off[J], kb * kGroup, lds + chunk(J) * 1024);
           },
           std::make_integer_sequence<int, CH>{});
       if constexpr (grp == 1) {

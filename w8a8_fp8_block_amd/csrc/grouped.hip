@@ -349,7 +349,8 @@ hipError_t launch_stream(const uint8_t* a, const float* as, const GroupWeights& 
 }
 
 // ------------------------------------------------------------------------
-// The dense GEMM's tiled and ping-pong kernels over the experts' rows.
+// The dense GEMM's tiled kernel over the experts' rows: for shapes the persistent
+// kernel does not take (K < 512, more than 256 experts), and gate and up at once.
 // ------------------------------------------------------------------------
 template <int BM, int BN, int WGM, int WGN, int STAGES, int WAUX>
 __global__ __launch_bounds__(64 * WGM * WGN) void group_tiled_kernel(
@@ -364,23 +365,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void group_tiled_kernel(
       N, K, Mp, 0, 1, nullptr, GroupRows{g.a_rows, t.end, g.order, g.per_row}, NoEpilogue{});
 }
 
-__global__ __launch_bounds__(512) void group_pp_kernel(const uint8_t* __restrict__ A,
-                                                       const float* __restrict__ As, GroupWeights gw,
-                                                       Groups g, uint32_t N, uint32_t K, uint32_t Mp,
-                                                       uint32_t tiles_n) {
-  using C = PpCfg<3, false, false>;
-  GroupTile t;
-  if (!group_tile<C::BM>(g, tiles_n, blockIdx.x, threadIdx.x & 63, t)) return;
-  const uint32_t which = blockIdx.y;
-  gemm_pp_body<3, false, false>(A, As, gw.w[which] + (uint64_t)t.expert * N * K,
-                                gw.ws[which] + (uint64_t)t.expert * (N / kGroup) * (K / kGroup),
-                                gw.out[which], t.m0, t.tn * C::BN, N, K, Mp,
-                                FfnArgs{nullptr, nullptr, nullptr, nullptr, 0},
-                                GroupRows{g.a_rows, t.end, g.order, g.per_row}, NoEpilogue{});
-}
-
 // Fused gate/up of the experts' FFN: the ping-pong kernel's FFN mode, 128
 // sorted rows by 128 intermediate columns, writing the quantized intermediate.
+template <int WAUX>
 __global__ __launch_bounds__(512) void group_gate_up_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, GroupWeights gw, Groups g,
     uint8_t* __restrict__ hq, float* __restrict__ hs, uint32_t I, uint32_t H, uint32_t Mp,
@@ -389,9 +376,10 @@ __global__ __launch_bounds__(512) void group_gate_up_kernel(
   GroupTile t;
   if (!group_tile<C::BM>(g, tiles_n, blockIdx.x, threadIdx.x & 63, t)) return;
   const uint64_t wo = (uint64_t)t.expert * I * H, so = (uint64_t)t.expert * (I / kGroup) * (H / kGroup);
-  gemm_pp_body<3, false, true>(A, As, gw.w[0] + wo, gw.ws[0] + so, nullptr, t.m0, t.tn * kGroup, I, H,
-                               Mp, FfnArgs{gw.w[1] + wo, gw.ws[1] + so, hq, hs, Mp_h},
-                               GroupRows{g.a_rows, t.end, g.order, g.per_row}, NoEpilogue{});
+  gemm_pp_body<3, false, true, GroupRows, NoEpilogue, WAUX>(
+      A, As, gw.w[0] + wo, gw.ws[0] + so, nullptr, t.m0, t.tn * kGroup, I, H, Mp,
+      FfnArgs{gw.w[1] + wo, gw.ws[1] + so, hq, hs, Mp_h}, GroupRows{g.a_rows, t.end, g.order, g.per_row},
+      NoEpilogue{});
 }
 
 // WAUX: the weights' cache policy.  With one row tile an expert they are read
@@ -409,47 +397,40 @@ hipError_t launch_group_128(const uint8_t* a, const float* as, const GroupWeight
   return hipGetLastError();
 }
 
-hipError_t launch_group_pp(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
-                           const Groups& g, uint32_t N, uint32_t K, hipStream_t s) {
-  using C = PpCfg<3, false, false>;
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_pp_kernel, C::LDS_BYTES);
-  if (e != hipSuccess) return e;
-  const uint32_t tiles_n = N / C::BN;
-  group_pp_kernel<<<dim3(max_row_tiles(g.R, g.E, C::BM) * tiles_n, sets), dim3(C::NT), C::LDS_BYTES, s>>>(
-      a, as, gw, g, N, K, m_pad16(g.a_rows), tiles_n);
-  return hipGetLastError();
-}
-
+template <int WAUX>
 hipError_t launch_group_persist(const uint8_t* a, const float* as, const GroupWeights& gw, const Groups& g,
                                 uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
   static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_persist_kernel, PersistCfg::LDS);
+  const hipError_t e = allow_lds(done, &group_persist_kernel<WAUX>, PersistCfg::LDS);
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = (N + 255) / 256;
   const uint64_t most = (uint64_t)max_row_tiles(g.R, g.E, 128) * tiles_n;
-  group_persist_kernel<<<dim3((uint32_t)(most < cus ? most : cus)), dim3(512), PersistCfg::LDS, s>>>(
+  group_persist_kernel<WAUX><<<dim3((uint32_t)(most < cus ? most : cus)), dim3(512), PersistCfg::LDS, s>>>(
       a, as, gw.w[0], gw.ws[0], gw.out[0], g, N, K, m_pad16(g.a_rows), tiles_n);
   return hipGetLastError();
 }
 
+// Weights bypass the caches below this mean of rows an expert.
+constexpr uint32_t kReadOnceRows = 64;
 // Kernel ids of the grouped product
-constexpr int kGroupStream = 1, kGroupTiled = 2, kGroupPp = 3;
+constexpr int kGroupStream = 1, kGroupPp = 3;  // 2: 128 x 128 tiles
 
-// By the mean rows an expert: streaming below kTiledMinRows (and below
-// kFewTilesMaxRows where 128-column tiles would not give every CU one), 128 x 128
-// tiles below kPpMinRows, else 256 x 128.  E = 32, N x K = 2048 x 5120, us,
-// streaming / 128 x 128: mean 12: 54.8 / 57.6, 16: 61.6 / 59.3, 32: 85 / 65;
-// E = 8, mean 16 (128 tiles): 21.4 / 39.9.
-constexpr uint32_t kTiledMinRows = 14, kFewTilesMaxRows = 64, kPpMinRows = 192;
+// By the mean rows an expert: streaming below kTileMinRows, and below
+// kFewTilesMaxRows where 128-column tiles would not give every CU one; else the
+// persistent 128 x 256 kernel.  E = 32, N x K = 2048 x 5120 / 5120 x 2048, us,
+// streaming against the persistent kernel: mean 10: 61.8 / 55.0 against 60.3 /
+// 61.5, 14: 66.3 / 58.1 against 60.0 / 61.7, 24: 70.1 / 73.1 against 62.0 / 66.9;
+// against 128 x 128 tiles from mean 14 on it is 1-15% faster at K = 2048 and
+// within 5% at K = 5120 up to mean 48, and 5-20% faster beyond at both.  E = 8,
+// mean 16, N = 2048 (128 tiles), streaming against 128 x 128: 21.4 / 39.9.
+constexpr uint32_t kTileMinRows = 14, kFewTilesMaxRows = 64;
 
 int group_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus) {
   const uint32_t groups = R < E ? R : E;
   if (groups == 0) return kGroupStream;
   const uint32_t mean = R / groups;
   const bool few = (uint64_t)groups * (N / 128) < cus;
-  if (mean < (few ? kFewTilesMaxRows : kTiledMinRows)) return kGroupStream;
-  return mean < kPpMinRows ? kGroupTiled : kGroupPp;
+  return mean < (few ? kFewTilesMaxRows : kTileMinRows) ? kGroupStream : kGroupPp;
 }
 
 // The streaming form.  Rows a tile: 16 up to a mean of kStreamFewRows rows an
@@ -476,18 +457,21 @@ hipError_t launch_stream_any(const uint8_t* a, const float* as, const GroupWeigh
 
 hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                       const Groups& g, uint32_t N, uint32_t K, uint32_t cus, int kernel, hipStream_t s) {
+  // mostly one row tile an expert: its weights are read once
+  const bool once = g.R < (uint64_t)kReadOnceRows * g.E;
   switch (kernel) {
     case kGroupStream:  // (two sets: gate and up)
       return sets == 2 ? launch_stream_any<true>(a, as, gw, sets, g, N, K, cus, s)
                        : launch_stream_any<false>(a, as, gw, sets, g, N, K, cus, s);
-    case kGroupTiled:
-      return g.R < 64ull * g.E ? launch_group_128<kStreamOnce>(a, as, gw, sets, g, N, K, s)
-                               : launch_group_128<0>(a, as, gw, sets, g, N, K, s);
-    default:
+    case kGroupPp:
       if (sets == 1 && g.E <= kPersistMaxExperts && K >= kPersistMinBlocks * kGroup)
-        return launch_group_persist(a, as, gw, g, N, K, cus, s);
-      return launch_group_pp(a, as, gw, sets, g, N, K, s);
+        return once ? launch_group_persist<kStreamOnce>(a, as, gw, g, N, K, cus, s)
+                    : launch_group_persist<0>(a, as, gw, g, N, K, cus, s);
+      break;
+    default: break;
   }
+  return once ? launch_group_128<kStreamOnce>(a, as, gw, sets, g, N, K, s)
+              : launch_group_128<0>(a, as, gw, sets, g, N, K, s);
 }
 
 Groups make_groups(const int32_t* offsets, const int32_t* order, uint32_t E, uint32_t R,
@@ -518,21 +502,30 @@ hipError_t launch_group_gate_and_up(const uint8_t* x, const float* x_s_km, const
                     make_groups(offsets, order, E, R, per_row, a_rows), I, H, cus, kernel, s);
 }
 
+namespace {
+template <int WAUX>
+hipError_t launch_gate_up(const uint8_t* x, const float* x_s_km, const GroupWeights& gw, uint8_t* hq,
+                          float* hs_km, const Groups& g, uint32_t H, uint32_t I, hipStream_t s) {
+  using C = PpCfg<3, false, true>;
+  static std::atomic<bool> done{false};
+  const hipError_t e = allow_lds(done, &group_gate_up_kernel<WAUX>, C::LDS_BYTES);
+  if (e != hipSuccess) return e;
+  const uint32_t tiles_n = I / kGroup;
+  group_gate_up_kernel<WAUX><<<dim3(max_row_tiles(g.R, g.E, C::BM) * tiles_n), dim3(C::NT), C::LDS_BYTES, s>>>(
+      x, x_s_km, gw, g, hq, hs_km, I, H, m_pad16(g.a_rows), m_pad16(g.R), tiles_n);
+  return hipGetLastError();
+}
+}  // namespace
+
 hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const uint8_t* w_gate,
                                     const float* ws_gate, const uint8_t* w_up, const float* ws_up,
                                     uint8_t* hq, float* hs_km, const int32_t* offsets,
                                     const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
                                     uint32_t E, uint32_t H, uint32_t I, hipStream_t s) {
-  using C = PpCfg<3, false, true>;
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_gate_up_kernel, C::LDS_BYTES);
-  if (e != hipSuccess) return e;
-  const uint32_t tiles_n = I / kGroup;
-  group_gate_up_kernel<<<dim3(max_row_tiles(R, E, C::BM) * tiles_n), dim3(C::NT), C::LDS_BYTES, s>>>(
-      x, x_s_km, GroupWeights{{w_gate, w_up}, {ws_gate, ws_up}, {nullptr, nullptr}},
-      make_groups(offsets, order, E, R, per_row, a_rows), hq, hs_km, I, H, m_pad16(a_rows), m_pad16(R),
-      tiles_n);
-  return hipGetLastError();
+  const GroupWeights gw{{w_gate, w_up}, {ws_gate, ws_up}, {nullptr, nullptr}};
+  const Groups g = make_groups(offsets, order, E, R, per_row, a_rows);
+  return R < (uint64_t)kReadOnceRows * E ? launch_gate_up<kStreamOnce>(x, x_s_km, gw, hq, hs_km, g, H, I, s)
+                                         : launch_gate_up<0>(x, x_s_km, gw, hq, hs_km, g, H, I, s);
 }
 
 }  // namespace fp8q
