@@ -20,10 +20,11 @@ namespace {
 // activation quantizer's steps) and v[m, r] = sum_k x[m, k] * A[a][r, k] in fp32
 // from bf16.  A workgroup takes 16 * TM rows and one part of K, its four waves
 // every fourth 128-group of it; blockIdx.z picks among the rows' distinct
-// adapters (round robin), and z = 0 quantizes as well.  A lane holds the 16-byte
-// pieces k = 32 j + 8 (l / 16), j < 4, of row l % 16 in the group: an operand of
-// the 16x16x32 MFMA as it stands, and 32 of the group's 128 values, the other
-// 96 in the lanes 16, 32 and 48 away.  Per adapter every row's product is formed
+// adapters (round robin), and z = 0 quantizes as well.  A lane holds values k =
+// 64 h + 16 (l / 16) .. + 15, h < 2, of row l % 16 in the group, the other 96 in
+// the lanes 16, 32 and 48 away: its codes are two 16-byte stores, and its
+// 16-byte pieces are operands of the 16x16x32 MFMA as they stand (in an order of
+// k that A's pieces share).  Per adapter every row's product is formed
 // (NR rank tiles of 16) and the rows of that adapter are stored; adapters after
 // a workgroup's first read its rows again, from L2.  Bound by reading A (decode:
 // a few rows an adapter) or x (prompts).
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
   bool quantize = blockIdx.z == 0;
   const uint16_t* xr[TM];
 #pragma unroll
-  for (int tm = 0; tm < TM; ++tm) xr[tm] = x + (uint64_t)min(m0 + 16 * tm + l16, M - 1) * K + 8 * q;
+  for (int tm = 0; tm < TM; ++tm) xr[tm] = x + (uint64_t)min(m0 + 16 * tm + l16, M - 1) * K + 16 * q;
 
   // One group's rows, quantized.  The stores go through buffer resources, rows
   // past M out of range, so that no branch hides their number from the waits of
@@ -93,10 +94,10 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
       const uint32_t m = m0 + 16 * tm + l16;
       uint2 codes[4];
       const float s = quant_lane_group(xf[tm], codes);
-      const uint32_t to = m < M ? m * K + g * kGroup + 8 * q : kNoStore;
+      const uint32_t to = m < M ? m * K + g * kGroup + 16 * q : kNoStore;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes[j].x, codes[j].y}, rQ, to + 32 * j, 0, 0);
+      for (int j = 0; j < 2; ++j)
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{codes[2 * j].x, codes[2 * j].y, codes[2 * j + 1].x, codes[2 * j + 1].y}, rQ, to + 64 * j, 0, 0);
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), rRm, q == 0 && m < M ? (m * G + g) * 4 : kNoStore, 0, 0);
       __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(m < M ? s : 0.0f), rKm,
                                             q == 0 && m < Mp ? (g * Mp + m) * 4 : kNoStore, 0, 0);
@@ -107,7 +108,7 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
     for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        xf[tm][j] = *reinterpret_cast<const u32x4*>(xr[tm] + g * kGroup + 32 * j);
+        xf[tm][j] = *reinterpret_cast<const u32x4*>(xr[tm] + g * kGroup + 64 * (j >> 1) + 8 * (j & 1));
   };
 
   for (uint32_t turn = 0; left; ++turn) {
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
     const uint16_t* ar[NR];
 #pragma unroll
     for (int t = 0; t < NR; ++t)
-      ar[t] = A + ((uint64_t)ad * rank + min(16 * t + l16, rank - 1)) * K + 8 * q;
+      ar[t] = A + ((uint64_t)ad * rank + min(16 * t + l16, rank - 1)) * K + 16 * q;
     v4f acc[TM][NR];
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm)
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
 #pragma unroll
       for (int t = 0; t < NR; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) af[t][j] = *reinterpret_cast<const u32x4*>(ar[t] + g * kGroup + 32 * j);
+        for (int j = 0; j < 4; ++j) af[t][j] = *reinterpret_cast<const u32x4*>(ar[t] + g * kGroup + 64 * (j >> 1) + 8 * (j & 1));
       load_x(min(g + 4, g1 - 1), xn);
       sched_fence();
       if constexpr (decltype(quant_c)::value) quant(g, xf);
