@@ -106,7 +106,9 @@ def test_grouped_select():
     assert sel(8, 0, 256) == 0 and sel(8, 4, 0) == 0 and sel(8, 4, 200) == 0
     assert sel(8, 128, 2048) == 1               # one row an expert: streaming
     assert sel(32 * 13, 32, 2048) == 1 and sel(32 * 14, 32, 2048) == 3
-    assert sel(8 * 63, 8, 2048) == 1 and sel(8 * 64, 8, 2048) == 3   # few tiles: streaming further
+    assert sel(8 * 63, 8, 2048) == 1 and sel(8 * 64, 8, 2048) == 2   # few tiles: streaming further
+    assert sel(8 * 500, 8, 2048) == 2 and sel(4 * 500, 4, 5120) == 2  # 1.5 rounds of 128x256 tiles at most
+    assert sel(8 * 500, 8, 5120) == 3 and sel(64 * 572, 64, 2048) == 3
     assert sel(0, 8, 2048) == 1
 
 

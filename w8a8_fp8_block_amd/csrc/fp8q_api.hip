@@ -563,9 +563,10 @@ fp8q_status check_workspace(const char* fn, const void* workspace, size_t have, 
 
 // fp8q_moe_ffn's automatic choice: the fused gate/up kernel (128-row tiles) from
 // this mean of rows an expert.  us, fused / separate: E = 32, H = 5120, I = 2048:
-// mean 10: 191 / 171, 20: 209 / 209, 32: 219 / 224, 80: 269 / 288, 128: 304 /
-// 327; E = 64, H = 2560, I = 512: mean 32: 89 / 92; E = 8, H = 2048, I = 1024
-// (64 tiles): 37 / 36.
+// mean 10: 179 / 171, 20: 196 / 205, 32: 206 / 230, 80: 271 / 287, 128: 305 /
+// 331; E = 64, H = 2560, I = 512: 32: 101 / 93, 128: 127 / 136; E = 8, H = 2048,
+// I = 1024 (64 tiles): 32: 38 / 36, 128: 41 / 40.  The separate form also needs
+// R * I * 4 bytes more workspace.
 constexpr uint32_t kMoeFusedMinRows = 32;
 
 int moe_ffn_auto(uint32_t T, uint32_t E, uint32_t top_k) {

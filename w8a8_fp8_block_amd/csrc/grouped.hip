@@ -2,6 +2,7 @@
 //   out[p, n] = bf16( sum_kb a_s[kb][r] * w_s[e][n/128][kb] * P(r, e, n, kb) ),
 //   r = order[p] / per_row (or p), e: offsets[e] <= p < offsets[e + 1],
 // with P the 128-deep e4m3 dot products of the dense GEMM (gemm.hip).
+#include <algorithm>
 #include <atomic>
 
 #include "group_pp.h"
@@ -349,8 +350,9 @@ hipError_t launch_stream(const uint8_t* a, const float* as, const GroupWeights& 
 }
 
 // ------------------------------------------------------------------------
-// The dense GEMM's tiled kernel over the experts' rows: for shapes the persistent
-// kernel does not take (K < 512, more than 256 experts), and gate and up at once.
+// The dense GEMM's tiled kernel over the experts' rows: for few tiles, for shapes
+// the persistent kernel does not take (K < 512, more than 256 experts), and for
+// gate and up at once.
 // ------------------------------------------------------------------------
 template <int BM, int BN, int WGM, int WGN, int STAGES, int WAUX>
 __global__ __launch_bounds__(64 * WGM * WGN) void group_tiled_kernel(
@@ -413,24 +415,35 @@ hipError_t launch_group_persist(const uint8_t* a, const float* as, const GroupWe
 // Weights bypass the caches below this mean of rows an expert.
 constexpr uint32_t kReadOnceRows = 64;
 // Kernel ids of the grouped product
-constexpr int kGroupStream = 1, kGroupPp = 3;  // 2: 128 x 128 tiles
+constexpr int kGroupStream = 1, kGroupTiled = 2, kGroupPp = 3;
 
-// By the mean rows an expert: streaming below kTileMinRows, and below
-// kFewTilesMaxRows where 128-column tiles would not give every CU one; else the
-// persistent 128 x 256 kernel.  E = 32, N x K = 2048 x 5120 / 5120 x 2048, us,
-// streaming against the persistent kernel: mean 10: 61.8 / 55.0 against 60.3 /
-// 61.5, 14: 66.3 / 58.1 against 60.0 / 61.7, 24: 70.1 / 73.1 against 62.0 / 66.9;
-// against 128 x 128 tiles from mean 14 on it is 1-15% faster at K = 2048 and
-// within 5% at K = 5120 up to mean 48, and 5-20% faster beyond at both.  E = 8,
-// mean 16, N = 2048 (128 tiles), streaming against 128 x 128: 21.4 / 39.9.
-constexpr uint32_t kTileMinRows = 14, kFewTilesMaxRows = 64;
+// By the mean rows an expert and the tiles (us).
+//  Streaming below kTileMinRows; and below kFewTilesMaxRows where 128-column tiles
+//  would not give every CU one.  Against the persistent kernel at E = 32, N x K =
+//  2048 x 5120 and 5120 x 2048, mean 12: 54.3 / 54.3 against 62.3 / 63.3, 16: 71.2
+//  / 60.7 against 62.0 / 66.0, 24: 70.5 / 72.9 against 63.9 / 66.5.  Against 128 x
+//  128 tiles at E = 8, N x K = 2048 x 2048, mean 32: 13.5 / 18.1, 56: 17.4 / 18.6,
+//  72: 21.8 / 15.5.
+//  128 x 128 tiles where they number at most a CU's one each, or, with
+//  kTallRows or more rows an expert, where 128 x 256 tiles would take at most one
+//  and a half rounds: against the persistent kernel at E = 8, N = K = 2048, mean
+//  72: 15.5 / 20.6, 200: 17.2 / 22.9, 500: 34.9 / 40.2; E = 64, N x K = 512 x
+//  2560, mean 24: 24.1 / 31.9; E = 4, N x K = 5120 x 2048, mean 500: 34.2 / 43.0.
+//  Elsewhere the persistent kernel: against 128 x 128 tiles at E = 40, N x K =
+//  5120 x 1408, mean 16: 59.1 / 67.3, 48: 70.3 / 80.1, 80: 77.0 / 89.9; E = 32,
+//  N x K = 2048 x 5120, mean 24: 63.9 / 61.8, 80: 104.3 / 111.6.
+constexpr uint32_t kTileMinRows = 14, kFewTilesMaxRows = 64, kTallRows = 192;
 
 int group_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus) {
   const uint32_t groups = R < E ? R : E;
   if (groups == 0) return kGroupStream;
   const uint32_t mean = R / groups;
   const bool few = (uint64_t)groups * (N / 128) < cus;
-  return mean < (few ? kFewTilesMaxRows : kTileMinRows) ? kGroupStream : kGroupPp;
+  if (mean < (few ? kFewTilesMaxRows : kTileMinRows)) return kGroupStream;
+  // row tiles: half a tile an expert more than its rows fill
+  const uint64_t rt = std::max<uint64_t>(groups, ((uint64_t)R + 64ull * groups) / 128);
+  if (rt * (N / 128) <= cus || (mean >= kTallRows && 2 * rt * ((N + 255) / 256) <= 3ull * cus)) return kGroupTiled;
+  return kGroupPp;
 }
 
 // The streaming form.  Rows a tile: 16 up to a mean of kStreamFewRows rows an
