@@ -629,8 +629,8 @@ __global__ __launch_bounds__(64 * NWV) void gemm_skinny_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t M, uint32_t N, uint32_t K,
     uint32_t Mp, uint32_t units_base, uint32_t units_rem, float* __restrict__ part = nullptr) {
-  gemm_skinny_body<TM, TN, NWV, U, ROW, SPLIT>(A, As, W, Ws, out, M, N, K, Mp, units_base, units_rem,
-                                               part, NoEpilogue{});
+  const NoEpilogue epi{};
+#include "gemm_skinny_body.h"
 }
 
 template <int TM, int GW, bool ROW>
