@@ -130,11 +130,11 @@ def test_ffn_refusals():
         assert need > 0 and ffn(variant=variant, nb=need - 1) == SHAPE and "workspace" in _err()
     assert ffn(T=0) == 0
     # the automatic variant's workspace is that variant's
-    for T in (4, 5000):
-        v = fp8q.fp8q_moe_ffn_select(T, 8, 2)
-        assert v == (2 if T == 4 else 1)
-        assert fp8q.fp8q_moe_ffn_workspace_bytes(T, 8, 2, 256, 128) == \
-            fp8q.fp8q_moe_ffn_workspace_bytes(T, 8, 2, 256, 128, v)
+    for T, I, want in ((4, 2048, 2), (5000, 2048, 1), (5000, 128, 2)):
+        v = fp8q.fp8q_moe_ffn_select(T, 8, 2, I)
+        assert v == want
+        assert fp8q.fp8q_moe_ffn_workspace_bytes(T, 8, 2, 256, I) == \
+            fp8q.fp8q_moe_ffn_workspace_bytes(T, 8, 2, 256, I, v)
 
 
 def test_lora_refusals():

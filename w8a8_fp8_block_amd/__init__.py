@@ -110,7 +110,7 @@ _SIGS = {
     "fp8q_gemm_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _U, _U, _U, _U, _U, _U, _I, _P]),
     "fp8q_gemm_grouped_select": (_I, [_U, _U, _U]),
     "fp8q_moe_ffn": (_I, [_P] * 13 + [_SZ, _U, _U, _U, _U, _U, _I, _P]),
-    "fp8q_moe_ffn_select": (_I, [_U, _U, _U]),
+    "fp8q_moe_ffn_select": (_I, [_U, _U, _U, _U]),
     "fp8q_proj_lora": (_I, [_P] * 12 + [_SZ, _U, _U, _U, _U, _U, _P]),
     "fp8q_proj_lora_workspace_bytes": (_SZ, [_U, _U, _U, _U]),
     "fp8q_moe_ffn_workspace_bytes": (_SZ, [_U, _U, _U, _U, _U, _I]),
@@ -495,9 +495,9 @@ def fp8q_gemm_grouped(a, a_scale_km, w, w_scale, offsets, out, order=None, top_k
                                   R, E, top_k, N, K, kernel, _stream(stream)))
 
 
-def fp8q_moe_ffn_select(T: int, E: int, top_k: int) -> int:
+def fp8q_moe_ffn_select(T: int, E: int, top_k: int, I: int) -> int:
     """Variant fp8q_moe_ffn runs with variant=0: 1 fused gate/up, 2 separate."""
-    return int(lib().fp8q_moe_ffn_select(T, E, top_k))
+    return int(lib().fp8q_moe_ffn_select(T, E, top_k, I))
 
 
 def fp8q_moe_ffn_workspace_bytes(T: int, E: int, top_k: int, H: int, I: int, variant: int = 0) -> int:

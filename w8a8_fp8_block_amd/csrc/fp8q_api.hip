@@ -561,16 +561,20 @@ fp8q_status check_workspace(const char* fn, const void* workspace, size_t have, 
   return FP8Q_OK;
 }
 
-// fp8q_moe_ffn's automatic choice: the fused gate/up kernel (128-row tiles) from
-// this mean of rows an expert.  us, fused / separate: E = 32, H = 5120, I = 2048:
-// mean 10: 179 / 171, 20: 196 / 205, 32: 206 / 230, 80: 271 / 287, 128: 305 /
-// 331; E = 64, H = 2560, I = 512: 32: 101 / 93, 128: 127 / 136; E = 8, H = 2048,
-// I = 1024 (64 tiles): 32: 38 / 36, 128: 41 / 40.  The separate form also needs
-// R * I * 4 bytes more workspace.
-constexpr uint32_t kMoeFusedMinRows = 32;
+// fp8q_moe_ffn's automatic choice: the fused gate/up kernel from a mean of
+// kMoeFusedMinRows rows an expert, where its tiles of 128 rows x 128 intermediate
+// columns (counting half a row tile an expert beyond its rows) make two rounds
+// of the CUs or more.  us, fused / separate: E = 32, H = 5120, I = 2048: mean 10:
+// 172 / 173, 20: 190 / 207, 32: 201 / 227, 80: 262 / 285, 128: 297 / 328; E = 64,
+// H = 2560, I = 512 (256 tiles at mean 32): 20: 78 / 75, 32: 100 / 92, 80: 113 /
+// 106, 128: 132 / 134; E = 8, H = 2048, I = 1024 (64 tiles): 32: 39 / 36, 128: 42 /
+// 40.  The separate form also needs R * I * 4 bytes more workspace.
+constexpr uint32_t kMoeFusedMinRows = 16;
 
-int moe_ffn_auto(uint32_t T, uint32_t E, uint32_t top_k) {
-  return (uint64_t)T * top_k >= (uint64_t)kMoeFusedMinRows * E ? 1 : 2;
+int moe_ffn_auto(uint32_t T, uint32_t E, uint32_t top_k, uint32_t I, uint32_t cus) {
+  const uint64_t R = (uint64_t)T * top_k, groups = std::min<uint64_t>(R, E);
+  const uint64_t row_tiles = std::max<uint64_t>(groups, (R + 64 * groups) / 128);
+  return R >= kMoeFusedMinRows * groups && row_tiles * (I / kGroup) >= 2ull * cus ? 1 : 2;
 }
 
 // Workspace of fp8q_moe_ffn: regions in this order, each on a 256-byte boundary.
@@ -1240,8 +1244,8 @@ fp8q_status fp8q_gemm_grouped(const uint8_t* a_e4m3, const float* a_scale_km, co
                                           top_k, a_rows, R, E, N, K, cus, kernel, stream));
 }
 
-int fp8q_moe_ffn_select(uint32_t T, uint32_t E, uint32_t top_k) {
-  return E == 0 || E > kMaxExperts || top_k == 0 || top_k > kMaxTopK ? -1 : moe_ffn_auto(T, E, top_k);
+int fp8q_moe_ffn_select(uint32_t T, uint32_t E, uint32_t top_k, uint32_t I) {
+  return E == 0 || E > kMaxExperts || top_k == 0 || top_k > kMaxTopK ? -1 : moe_ffn_auto(T, E, top_k, I, current_cus());
 }
 
 size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k, uint32_t H, uint32_t I,
@@ -1249,7 +1253,7 @@ size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k, uint
   if (variant < 0 || variant > 2 || H == 0 || H % kGroup != 0 || I == 0 || I % kGroup != 0 || E == 0 ||
       E > kMaxExperts || top_k == 0 || top_k > kMaxTopK)
     return 0;
-  if (variant == 0) variant = moe_ffn_auto(T, E, top_k);
+  if (variant == 0) variant = moe_ffn_auto(T, E, top_k, I, current_cus());
   return (size_t)moe_workspace(T, top_k, H, I, variant).total;
 }
 
@@ -1284,7 +1288,7 @@ fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int
   REQUIRE_PTR(w_down_scale);
   REQUIRE_PTR(out_bf16);
   if (T == 0) return ok();
-  if (variant == 0) variant = moe_ffn_auto(T, E, top_k);
+  if (variant == 0) variant = moe_ffn_auto(T, E, top_k, I, current_cus());
   const MoeWorkspace w = moe_workspace(T, top_k, H, I, variant);
   st = check_workspace(fn, workspace, workspace_bytes, w.total);
   if (st != FP8Q_OK) return st;
@@ -1300,7 +1304,7 @@ fp8q_status fp8q_moe_ffn(const uint16_t* x_bf16, const float* weights, const int
   if (st != FP8Q_OK) return st;
   if (variant == 1) {
     st = launched(fn, launch_group_ffn_gate_up(xq, xs, w_gate, w_gate_scale, w_up, w_up_scale, hq, hs, offsets,
-                                               order, top_k, T, R, E, H, I, stream));
+                                               order, top_k, T, R, E, H, I, cus, stream));
   } else {
     uint16_t *g = reinterpret_cast<uint16_t*>(ws + w.g), *u = reinterpret_cast<uint16_t*>(ws + w.u);
     st = launched(fn, launch_group_gate_and_up(xq, xs, w_gate, w_gate_scale, w_up, w_up_scale, g, u, offsets,

@@ -185,7 +185,7 @@ hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const
                                     const float* ws_gate, const uint8_t* w_up, const float* ws_up,
                                     uint8_t* hq, float* hs_km, const int32_t* offsets,
                                     const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
-                                    uint32_t E, uint32_t H, uint32_t I, hipStream_t s);
+                                    uint32_t E, uint32_t H, uint32_t I, uint32_t cus, hipStream_t s);
 
 // ---- low-rank adapters beside the projection (lora.hip) ----
 constexpr uint32_t kMaxLoraRank = 128;

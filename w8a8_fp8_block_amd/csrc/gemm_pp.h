@@ -71,42 +71,33 @@ struct FfnArgs {
   uint32_t Mp_h;  // row stride of hs
 };
 
-// FFN-mode epilogue, after the main loop (all direct loads of this wave
-// complete).  Gate wave gw (group 0) and up wave gw (group 1, wave gw + 4)
-// hold the same 64x64 output positions in the same registers; they split
-// the rows: the gate wave finishes rows tm = 0, 1 of its band, the up wave
-// rows tm = 2, 3.
-//   1. each wave rounds its accumulators to bf16 (the projections' output
-//      format) and parks the half its partner finishes in LDS;
-//   2. each wave forms h = bf16(silu(g) * u) for its rows (silu_mul_f32, the
-//      same code as the standalone intermediate kernel) and the maximum |h|
-//      of each row over its 64 columns (integer max of bf16 magnitudes:
-//      within a lane, then across the 4 lanes of a row);
-//   3. the two waves of a group covering columns 0-63 and 64-127 of the
-//      128-column group combine their row maxima through LDS; scale =
-//      amax/448 and the codes of h / scale follow the activation quantizer's
-//      exact steps (quotients, encode4).  Codes of rows < M are stored; the
-//      wave on columns 0-63 stores the K-major scales of its rows < M and
-//      zeros for pad rows M .. pad_end-1.
-// Every wave passes the same three workgroup barriers, each after its own LDS
-// writes have completed (s_barrier alone does not wait for them).
+// FFN-mode epilogue.  Gate wave gw (group 0) and up wave gw (group 1, wave gw +
+// 4) hold the same 64x64 output positions in the same registers; they split the
+// rows: the gate wave finishes rows tm = 0, 1 of its band, the up wave rows tm =
+// 2, 3.
+//   1. ffn_park: each wave rounds its accumulators to bf16 (the projections'
+//      output format) and parks the half its partner finishes in LDS (32 KB);
+//   2. ffn_h: each wave forms h = bf16(silu(g) * u) for its rows (silu_mul_f32,
+//      the same code as the standalone intermediate kernel) and the maximum |h|
+//      of each row over its 64 columns (integer max of bf16 magnitudes: within a
+//      lane, then across the 4 lanes of a row), left in LDS (512 bytes);
+//   3. ffn_codes: the two waves of a group covering columns 0-63 and 64-127 of
+//      the 128-column group combine their row maxima; scale = amax/448 and the
+//      codes of h / scale follow the activation quantizer's exact steps
+//      (quotients, encode4).  Codes of rows < M are stored; the wave on columns
+//      0-63 stores the K-major scales of its rows < M and zeros for pad rows M
+//      .. pad_end-1.
+// A workgroup barrier between the steps, each after the LDS writes before it
+// have completed (s_barrier alone does not wait for them).
+constexpr uint32_t kFfnPark = 32 * 1024, kFfnMax = 8 * 2 * 16 * 2;
+
 template <int TM, int TN>
-__device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* smem,
-                                             const FfnArgs& ffn, uint32_t wave, uint32_t lane,
-                                             uint32_t mrow0, uint32_t ncol0, uint32_t nb,
-                                             uint32_t M, uint32_t N, uint32_t pad_end) {
+__device__ __forceinline__ void ffn_park(const v4f (&acc)[TM][TN], uint8_t* smem, uint32_t wave, uint32_t lane) {
   static_assert(TM == 4 && TN == 4, "64x64 wave tile");
-  uint32_t* park = reinterpret_cast<uint32_t*>(smem);                // [8][4][64][4] u32: 32 KB
-  uint32_t* rmax = reinterpret_cast<uint32_t*>(smem + 32 * 1024);    // [8][2][16] u32
-  const uint32_t l16 = lane & 15, q4 = lane >> 4;
+  uint32_t* park = reinterpret_cast<uint32_t*>(smem);  // [8][4][64][4] u32
   const bool up = wave >= 4;
-  auto lds_barrier = [] {
-    wait_lgkm0();
-    wg_barrier();
-  };
-  lds_barrier();  // every wave is done with the operand ring
-  // 1. park the partner's half: tiles of rows tm = 0, 1 (up waves) or 2, 3
-  //    (gate waves), two 16x16 tiles per 16-byte slot
+  // the tiles of rows tm = 0, 1 (up waves) or 2, 3 (gate waves), two 16x16
+  // tiles per 16-byte slot
 #pragma unroll
   for (int t2 = 0; t2 < 4; ++t2) {
     const int t = 2 * t2;  // tile index within the half
@@ -115,11 +106,15 @@ __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* 
                        : pack_bf16x4(acc[2 + (t + 1) / TN][(t + 1) % TN]);
     *reinterpret_cast<uint4*>(park + ((wave * 4 + t2) * 64 + lane) * 4) = make_uint4(a.x, a.y, b.x, b.y);
   }
-  lds_barrier();
-  // 2. h for this wave's rows
-  const uint32_t partner = wave ^ 4;
-  uint32_t hb[2][TN][2];  // h as packed bf16 pairs: rows i = 0, 1 of this wave's half
-  uint32_t amax[2];
+}
+
+// hb: h as packed bf16 pairs, rows i = 0, 1 of this wave's half
+template <int TM, int TN>
+__device__ __forceinline__ void ffn_h(const v4f (&acc)[TM][TN], const uint8_t* smem, uint16_t* rmax, uint32_t wave,
+                                      uint32_t lane, uint32_t (&hb)[2][TN][2], uint32_t (&amax)[2]) {
+  const uint32_t* park = reinterpret_cast<const uint32_t*>(smem);
+  const uint32_t l16 = lane & 15, q4 = lane >> 4, partner = wave ^ 4;
+  const bool up = wave >= 4;
 #pragma unroll
   for (int t2 = 0; t2 < 4; ++t2) {
     const uint4 pp = *reinterpret_cast<const uint4*>(park + ((partner * 4 + t2) * 64 + lane) * 4);
@@ -149,14 +144,21 @@ __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* 
     mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
     mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
     amax[i] = mx;
-    if (q4 == 0) rmax[(wave * 2 + i) * 16 + l16] = mx;
+    if (q4 == 0) rmax[(wave * 2 + i) * 16 + l16] = (uint16_t)mx;
   }
-  lds_barrier();
-  // 3. scales and codes
+}
+
+template <int TN>
+__device__ __forceinline__ void ffn_codes(const uint32_t (&hb)[2][TN][2], const uint32_t (&amax)[2],
+                                          const uint16_t* rmax, const FfnArgs& ffn, uint32_t wave, uint32_t lane,
+                                          uint32_t mrow0, uint32_t ncol0, uint32_t nb, uint32_t M, uint32_t N,
+                                          uint32_t pad_end) {
+  const uint32_t l16 = lane & 15, q4 = lane >> 4;
   const uint32_t mate = wave ^ 1;  // the other 64 columns of the 128-column group
+  const bool up = wave >= 4;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint32_t a = max(amax[i], rmax[(mate * 2 + i) * 16 + l16]);
+    const uint32_t a = max(amax[i], (uint32_t)rmax[(mate * 2 + i) * 16 + l16]);
     const float sc = group_scale(a);
     float x[16], q[16];
 #pragma unroll
@@ -178,7 +180,28 @@ __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* 
   }
 }
 
-template <int STAGES, bool ROW, bool FFN, class Rows, class Epi, int WAUX = 0>
+// The whole of it after the main loop (all direct loads of this wave complete):
+// every wave passes the same three workgroup barriers.
+template <int TM, int TN>
+__device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* smem,
+                                             const FfnArgs& ffn, uint32_t wave, uint32_t lane,
+                                             uint32_t mrow0, uint32_t ncol0, uint32_t nb,
+                                             uint32_t M, uint32_t N, uint32_t pad_end) {
+  uint16_t* rmax = reinterpret_cast<uint16_t*>(smem + kFfnPark);
+  auto lds_barrier = [] {
+    wait_lgkm0();
+    wg_barrier();
+  };
+  lds_barrier();  // every wave is done with the operand ring
+  ffn_park<TM, TN>(acc, smem, wave, lane);
+  lds_barrier();
+  uint32_t hb[2][TN][2], amax[2];
+  ffn_h<TM, TN>(acc, smem, rmax, wave, lane, hb, amax);
+  lds_barrier();
+  ffn_codes<TN>(hb, amax, rmax, ffn, wave, lane, mrow0, ncol0, nb, M, N, pad_end);
+}
+
+template <int STAGES, bool ROW, bool FFN, class Rows, class Epi>
 __device__ __forceinline__ void gemm_pp_body(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t m0, uint32_t n0, uint32_t N,
@@ -251,10 +274,8 @@ __device__ __forceinline__ void gemm_pp_body(
     unroll_seq(
         [&](auto jc) {
           constexpr int J = decltype(jc)::value;
-          if constexpr (FFN && J >= 4)
-            dma16_aux<WAUX>(rW2, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
-          else if constexpr (FFN)
-            dma16(rA, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
+          if constexpr (FFN)
+            dma16(J < 4 ? rA : rW2, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
           else
             dma16(g0_act ? rA : rW, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
         },
@@ -265,10 +286,7 @@ __device__ __forceinline__ void gemm_pp_body(
     unroll_seq(
         [&](auto jc) {
           constexpr int J = decltype(jc)::value;
-          if constexpr (FFN)
-            dma16_aux<WAUX>(rW, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
-          else
-            dma16(rA, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
+          dma16(FFN ? rW : rA, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
         },
         std::make_integer_sequence<int, CH1>{});
     dma4(rS, s_off, kb * Mp * 4, base + my_sc);

@@ -1,5 +1,5 @@
 // The ping-pong GEMM over experts' rows as one persistent pipeline: the grouped
-// product's kernel for many rows an expert.
+// product's and the fused gate/up projection's kernel for many rows an expert.
 #pragma once
 
 #include "gemm_pp.h"
@@ -23,6 +23,16 @@ namespace {
 // its first block is loaded.  They come a tile ahead, by direct loads into a
 // small LDS table of two sets, so that no wave waits for them; K must hold at
 // least kPersistMinBlocks blocks for them to have arrived.
+//
+// Bound by the matrix pipe at many rows: 36608 rows of 64 experts, N = 2048, K =
+// 5120: 465 us, 1.65 PFLOP/s (1.83 with the partial tiles' rows), the pipe busy
+// 43.6% of the cycles at the clock the power limit allows (the dense kernel,
+// without partial tiles: 1.9-2.1, 55%); one launch of 256-row tiles took 511 us
+// there and 310 us for the FFN's down product (18304 rows, 32 experts, N = 5120, K =
+// 2048), this kernel 260.  The fused gate/up projection of those rows (H = 5120, I =
+// 2048): 515 us with a workgroup a tile, 470 us as part of the pipeline.  Near its
+// lower limit of rows it is bound by the weights' stream (70 us for 288 MB at a
+// mean of 51 rows: 3.1 rounds of tiles over the CUs cost the fourth round's time).
 // ------------------------------------------------------------------------
 constexpr uint32_t kPersistMinBlocks = 4;
 constexpr uint32_t kPersistMaxExperts = 256;  // the experts' tables in LDS
@@ -32,18 +42,20 @@ struct PersistCfg {
   static constexpr int ROWS = C::LDS_BYTES;              // [2][128] sorted rows' order entries
   static constexpr int OFFS = ROWS + 2 * 128 * 4;        // [E + 1] first rows
   static constexpr int TILES = OFFS + (kPersistMaxExperts + 1) * 4;  // [E + 1] row tiles before
-  static constexpr int LDS = TILES + (kPersistMaxExperts + 1) * 4;
+  static constexpr int RMAX = TILES + (kPersistMaxExperts + 1) * 4;  // FFN: row maxima
+  static constexpr int LDS = RMAX + (int)kFfnMax;
   static_assert(LDS <= 160 * 1024, "LDS budget");
 };
 
-// WAUX: the weights' cache policy.
-template <int WAUX>
-__global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __restrict__ A,
-                                                            const float* __restrict__ As,
-                                                            const uint8_t* __restrict__ W,
-                                                            const float* __restrict__ Ws,
-                                                            uint16_t* __restrict__ out, Groups g, uint32_t N,
-                                                            uint32_t K, uint32_t Mp, uint32_t tiles_n) {
+// WAUX: the weights' cache policy.  FFN: the experts' fused gate/up projection; W
+// and Ws are gate's, ffn holds up's and the quantized intermediate [R,N], a tile's
+// 256 columns are gate's and up's same 128, and out is unused.
+template <int WAUX, bool FFN>
+__device__ __forceinline__ void group_persist_body(const uint8_t* __restrict__ A, const float* __restrict__ As,
+                                                   const uint8_t* __restrict__ W, const float* __restrict__ Ws,
+                                                   uint16_t* __restrict__ out, const FfnArgs& ffn,
+                                                   const Groups& g, uint32_t N, uint32_t K, uint32_t Mp,
+                                                   uint32_t tiles_n) {
   using C = PersistCfg::C;
   constexpr int STAGES = 3, TM = C::TM, TN = C::TN, NP = C::NP;
   constexpr int CH0 = C::CH0, CH1 = C::CH1, LW0 = C::LW0, LW1 = C::LW1;
@@ -97,7 +109,7 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
       t.m0 = __builtin_amdgcn_readfirstlane(offs[x]) + tm * 128;
       // (an empty expert's tables repeat the next one's first row)
       t.end = __builtin_amdgcn_readfirstlane(offs[x + 1]);
-      t.n0 = tn * 256;
+      t.n0 = tn * (FFN ? 128 : 256);
       return;
     }
   };
@@ -116,7 +128,7 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
     uint32_t c_off[CH];  // weights: from the tile's first column; activations: from A
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      const uint32_t row = (grp ? 4 * gw + j : 128 / 8 + 4 * gw + (j & 3)) * 8 + (lane >> 3);
+      const uint32_t row = (grp || FFN ? 4 * gw + (j & 3) : 128 / 8 + 4 * gw + (j & 3)) * 8 + (lane >> 3);
       c_off[j] = row * K + ((lane & 7) ^ swz(row)) * 16;
     }
     const uint32_t my_sc = C::A_BYTES + C::W_BYTES + wave * C::SCW_BYTES;
@@ -124,7 +136,7 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
     const uint32_t lds0 = lds_addr(smem);
     const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, g.a_rows * K), rS = make_rsrc(As, G * Mp * 4);
     const __amdgpu_buffer_rsrc_t rO = make_rsrc(g.order ? g.order : g.offsets, g.order ? g.R * 4 : 4);
-    __amdgpu_buffer_rsrc_t rW, rWs;
+    __amdgpu_buffer_rsrc_t rW, rWs, rWs2;  // FFN: gate's (group 1) or up's (group 0) weights; gate's, up's scales
     uint32_t s_off = 0, ws_off = 0;
 
     // ---- load cursor: tile, block, and the set of the row table it uses ----
@@ -156,9 +168,10 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
         s_off = src(min(r, lt.end - 1 - lt.m0)) * 4;
         ws_off = lt.n0 / kGroup * G * 4;
         rWs = make_rsrc(Ws + (uint64_t)lt.expert * (N / kGroup) * G, (N / kGroup) * G * 4);
+        if constexpr (FFN) rWs2 = make_rsrc(ffn.ws_up + (uint64_t)lt.expert * (N / kGroup) * G, (N / kGroup) * G * 4);
       }
       // columns past N (N / 128 odd): out of range, zeros
-      rW = make_rsrc(W + ((uint64_t)lt.expert * N + lt.n0) * K, (N - lt.n0) * K);
+      rW = make_rsrc((FFN && grp == 0 ? ffn.w_up : W) + ((uint64_t)lt.expert * N + lt.n0) * K, (N - lt.n0) * K);
     };
     // the next block, or the first of the next tile
     Tile nt;  // the tile after lt
@@ -191,7 +204,10 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
       if constexpr (grp == 1) {
         dma4_at(rS, s_off, kb * Mp * 4, lds + my_sc);
         dma4_at(rS, s_off, kb * Mp * 4, lds + p_sc);  // (the partner: the same rows)
-        dma4_at(rWs, 0, ws_off + G * 4 + kb * 4, lds + my_sc + 256);
+        if constexpr (FFN)
+          dma4_at(rWs2, 0, ws_off + kb * 4, lds + my_sc + 256);
+        else
+          dma4_at(rWs, 0, ws_off + G * 4 + kb * 4, lds + my_sc + 256);
         dma4_at(rWs, 0, ws_off + kb * 4, lds + p_sc + 256);
       }
       // with a tile's first block: the row table of the tile after it (waves 0
@@ -260,12 +276,15 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
       sc_tail = sc[TM - 1];
     };
     Tile ct = lt;  // compute cursor
-    auto epilogue = [&]() __attribute__((always_inline)) {
+    auto promote_rest = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int j = NP - kPromoteDist; j < NP; ++j) acc[j / TN][j % TN] += p[j & 3] * sc_tail;
       sc_tail = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    auto epilogue = [&]() __attribute__((always_inline)) {
+      promote_rest();
       if (ct.n0 + wn * C::WN < N) {
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm) {
@@ -320,6 +339,43 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
       else
         half(std::integral_constant<int, 2>{});
     };
+    // FFN: a tile's last block, in slot sl, with its epilogue.  The slot's refill
+    // waits until the epilogue has used it: both groups have read the block
+    // after half 0, the waves exchange gate and up through it, and after the
+    // second exchange barrier it is free again.  At the next block's waits as many
+    // loads are in flight as without (and this tile's stores, which are older).
+    auto last_ffn = [&](uint32_t sl) __attribute__((always_inline)) {
+      uint8_t* slot = smem + sl * C::STAGE_BYTES;
+      uint16_t* rmax = reinterpret_cast<uint16_t*>(smem + PersistCfg::RMAX);
+      if constexpr (grp == 0) {
+        compute_block();
+        wait_vmcnt<LW0>();
+        wg_barrier();
+      } else {
+        dispatch(sl, read_block);
+        wait_lgkm0();
+        wait_vmcnt<LW1>();  // own part of the next block
+        wg_barrier();
+        compute_block();
+      }
+      promote_rest();
+      ffn_park<TM, TN>(acc, slot, wave, lane);
+      wait_lgkm0();
+      wg_barrier();
+      uint32_t hb[2][TN][2], amax[2];
+      ffn_h<TM, TN>(acc, slot, rmax, wave, lane, hb, amax);
+      wait_lgkm0();
+      wg_barrier();
+      ffn_codes<TN>(hb, amax, rmax, ffn, wave, lane, ct.m0 + wm * C::WM, ct.n0 + (gw & 1) * C::WN, ct.n0 / kGroup,
+                    ct.end, N, ct.end);
+      issue(sl);
+      if constexpr (grp == 0) {
+        dispatch(sl == 2 ? 0 : sl + 1, read_block);
+        wait_lgkm0();
+      }
+      wg_barrier();
+      clear();
+    };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
     using S2 = std::integral_constant<int, 2>;
@@ -373,10 +429,14 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
         step(S1{});
         ++i;
       }
-      dispatch(i % 3, half0);
-      if constexpr (grp == 0) epilogue();
-      dispatch(i % 3, half1);
-      if constexpr (grp == 1) epilogue();
+      if constexpr (FFN) {
+        last_ffn(i % 3);
+      } else {
+        dispatch(i % 3, half0);
+        if constexpr (grp == 0) epilogue();
+        dispatch(i % 3, half1);
+        if constexpr (grp == 1) epilogue();
+      }
       ++i;
       if (ct.id + workers >= all) break;
       locate(ct.id + workers, ct);
@@ -387,6 +447,27 @@ __global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __res
     body(std::integral_constant<uint32_t, 1>{});
   else
     body(std::integral_constant<uint32_t, 0>{});
+}
+
+template <int WAUX>
+__global__ __launch_bounds__(512) void group_persist_kernel(const uint8_t* __restrict__ A,
+                                                            const float* __restrict__ As,
+                                                            const uint8_t* __restrict__ W,
+                                                            const float* __restrict__ Ws,
+                                                            uint16_t* __restrict__ out, Groups g, uint32_t N,
+                                                            uint32_t K, uint32_t Mp, uint32_t tiles_n) {
+  group_persist_body<WAUX, false>(A, As, W, Ws, out, FfnArgs{nullptr, nullptr, nullptr, nullptr, 0}, g, N, K, Mp,
+                                  tiles_n);
+}
+
+template <int WAUX>
+__global__ __launch_bounds__(512) void group_persist_ffn_kernel(const uint8_t* __restrict__ A,
+                                                                const float* __restrict__ As,
+                                                                const uint8_t* __restrict__ w_gate,
+                                                                const float* __restrict__ ws_gate, FfnArgs ffn,
+                                                                Groups g, uint32_t I, uint32_t H, uint32_t Mp,
+                                                                uint32_t tiles_n) {
+  group_persist_body<WAUX, true>(A, As, w_gate, ws_gate, nullptr, ffn, g, I, H, Mp, tiles_n);
 }
 
 }  // namespace

@@ -367,9 +367,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void group_tiled_kernel(
       N, K, Mp, 0, 1, nullptr, GroupRows{g.a_rows, t.end, g.order, g.per_row}, NoEpilogue{});
 }
 
-// Fused gate/up of the experts' FFN: the ping-pong kernel's FFN mode, 128
-// sorted rows by 128 intermediate columns, writing the quantized intermediate.
-template <int WAUX>
+// Fused gate/up of the experts' FFN for shapes the persistent kernel does not take:
+// the ping-pong kernel's FFN mode, 128 sorted rows by 128 intermediate columns,
+// writing the quantized intermediate.
 __global__ __launch_bounds__(512) void group_gate_up_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, GroupWeights gw, Groups g,
     uint8_t* __restrict__ hq, float* __restrict__ hs, uint32_t I, uint32_t H, uint32_t Mp,
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(512) void group_gate_up_kernel(
   GroupTile t;
   if (!group_tile<C::BM>(g, tiles_n, blockIdx.x, threadIdx.x & 63, t)) return;
   const uint64_t wo = (uint64_t)t.expert * I * H, so = (uint64_t)t.expert * (I / kGroup) * (H / kGroup);
-  gemm_pp_body<3, false, true, GroupRows, NoEpilogue, WAUX>(
+  gemm_pp_body<3, false, true>(
       A, As, gw.w[0] + wo, gw.ws[0] + so, nullptr, t.m0, t.tn * kGroup, I, H, Mp,
       FfnArgs{gw.w[1] + wo, gw.ws[1] + so, hq, hs, Mp_h}, GroupRows{g.a_rows, t.end, g.order, g.per_row},
       NoEpilogue{});
@@ -516,16 +516,28 @@ hipError_t launch_group_gate_and_up(const uint8_t* x, const float* x_s_km, const
 }
 
 namespace {
-template <int WAUX>
-hipError_t launch_gate_up(const uint8_t* x, const float* x_s_km, const GroupWeights& gw, uint8_t* hq,
-                          float* hs_km, const Groups& g, uint32_t H, uint32_t I, hipStream_t s) {
+hipError_t launch_gate_up(const uint8_t* x, const float* x_s_km, const GroupWeights& gw, const FfnArgs& f,
+                          const Groups& g, uint32_t H, uint32_t I, hipStream_t s) {
   using C = PpCfg<3, false, true>;
   static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_gate_up_kernel<WAUX>, C::LDS_BYTES);
+  const hipError_t e = allow_lds(done, &group_gate_up_kernel, C::LDS_BYTES);
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = I / kGroup;
-  group_gate_up_kernel<WAUX><<<dim3(max_row_tiles(g.R, g.E, C::BM) * tiles_n), dim3(C::NT), C::LDS_BYTES, s>>>(
-      x, x_s_km, gw, g, hq, hs_km, I, H, m_pad16(g.a_rows), m_pad16(g.R), tiles_n);
+  group_gate_up_kernel<<<dim3(max_row_tiles(g.R, g.E, C::BM) * tiles_n), dim3(C::NT), C::LDS_BYTES, s>>>(
+      x, x_s_km, gw, g, f.hq, f.hs, I, H, m_pad16(g.a_rows), f.Mp_h, tiles_n);
+  return hipGetLastError();
+}
+
+template <int WAUX>
+hipError_t launch_persist_ffn(const uint8_t* x, const float* x_s_km, const GroupWeights& gw, const FfnArgs& f,
+                              const Groups& g, uint32_t H, uint32_t I, uint32_t cus, hipStream_t s) {
+  static std::atomic<bool> done{false};
+  const hipError_t e = allow_lds(done, &group_persist_ffn_kernel<WAUX>, PersistCfg::LDS);
+  if (e != hipSuccess) return e;
+  const uint32_t tiles_n = I / kGroup;
+  const uint64_t most = (uint64_t)max_row_tiles(g.R, g.E, 128) * tiles_n;
+  group_persist_ffn_kernel<WAUX><<<dim3((uint32_t)(most < cus ? most : cus)), dim3(512), PersistCfg::LDS, s>>>(
+      x, x_s_km, gw.w[0], gw.ws[0], f, g, I, H, m_pad16(g.a_rows), tiles_n);
   return hipGetLastError();
 }
 }  // namespace
@@ -534,11 +546,13 @@ hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const
                                     const float* ws_gate, const uint8_t* w_up, const float* ws_up,
                                     uint8_t* hq, float* hs_km, const int32_t* offsets,
                                     const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
-                                    uint32_t E, uint32_t H, uint32_t I, hipStream_t s) {
+                                    uint32_t E, uint32_t H, uint32_t I, uint32_t cus, hipStream_t s) {
   const GroupWeights gw{{w_gate, w_up}, {ws_gate, ws_up}, {nullptr, nullptr}};
   const Groups g = make_groups(offsets, order, E, R, per_row, a_rows);
-  return R < (uint64_t)kReadOnceRows * E ? launch_gate_up<kStreamOnce>(x, x_s_km, gw, hq, hs_km, g, H, I, s)
-                                         : launch_gate_up<0>(x, x_s_km, gw, hq, hs_km, g, H, I, s);
+  const FfnArgs f{w_up, ws_up, hq, hs_km, m_pad16(R)};
+  if (E > kPersistMaxExperts || H < kPersistMinBlocks * kGroup) return launch_gate_up(x, x_s_km, gw, f, g, H, I, s);
+  return R < (uint64_t)kReadOnceRows * E ? launch_persist_ffn<kStreamOnce>(x, x_s_km, gw, f, g, H, I, cus, s)
+                                         : launch_persist_ffn<0>(x, x_s_km, gw, f, g, H, I, cus, s);
 }
 
 }  // namespace fp8q
