@@ -235,6 +235,47 @@ def test_gemm_grouped_routed(orc, E, T, top_k, N, K):
     assert np.array_equal(outs[2], outs[3])
 
 
+@pytest.mark.parametrize("K", [512, 640, 768, 896])
+@pytest.mark.parametrize("gather", [True, False])
+def test_gemm_grouped_many_tiles(orc, K, gather):
+    """More tiles than CUs: the persistent kernels' workgroups run several, whose
+    first blocks fall on every slot of the ring (K / 128 = 4 .. 7)."""
+    sizes, N, top_k = [130, 0, 257, 1, 128, 700, 60, 500], 3840, 4
+    a, a_s, wq, ws, order, offsets, ref = _grouped_case(orc, sizes, N, K, top_k, gather, 0, K)
+    ad, kmd, wqd, wsd = dev(a), dev(orc.scale_to_kmajor(a_s)), dev(wq), dev(ws)
+    for kernel in (1, 2, 3):
+        log(f"gemm_grouped many tiles K={K} gather={gather} kernel={kernel}")
+        out = Guarded((len(order), N), torch.int16)
+        fp8q.fp8q_gemm_grouped(ad, kmd, wqd, wsd, dev(offsets), out.t, order=dev(order) if gather else None,
+                               top_k=top_k if gather else 1, kernel=kernel)
+        torch.cuda.synchronize()
+        out.check_canary()
+        assert_tol(bf16_bits_to_f64(host(out.t)), ref, f"many tiles K {K} kernel {kernel}")
+
+
+def test_gemm_grouped_weights_past_32_bits(orc):
+    """180 experts of 5120 x 5120: 4.7e9 codes; rows in the first and last experts."""
+    E, N, K = 180, 5120, 5120
+    rng = np.random.default_rng(4)
+    used = (0, 1, 163, 164, 179)
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(E, N // 128, K // 128, device="cuda")
+    hosts = {e: orc.quant_weight_block(rng.normal(0, 0.02, (N, K)).astype(np.float32)) for e in used}
+    for e, (q, s) in hosts.items():
+        w[e], ws[e] = dev(q), dev(s)
+    ids = np.repeat(np.array(used, np.int32), 3)
+    _, _, offsets = _group_ref(ids, E)
+    a, a_s = orc.quant_act(_acts(orc, len(ids), K, rng))
+    ref = np.concatenate([orc.gemm_ref(a[3 * i:3 * i + 3], a_s[3 * i:3 * i + 3], *hosts[e]) for i, e in enumerate(used)])
+    for kernel in (1, 2, 3):
+        log(f"gemm_grouped weights past 32 bits kernel={kernel}")
+        out = Guarded((len(ids), N), torch.int16)
+        fp8q.fp8q_gemm_grouped(dev(a), dev(orc.scale_to_kmajor(a_s)), w, ws, dev(offsets), out.t, kernel=kernel)
+        torch.cuda.synchronize()
+        out.check_canary()
+        assert_tol(bf16_bits_to_f64(host(out.t)), ref, f"past 32 bits kernel {kernel}")
+
+
 # --------------------------------------------------------------- weighted sum
 @pytest.mark.parametrize("T,k,H", [(1, 1, 8), (5, 3, 136), (33, 8, 5120), (2, 32, 2056)])
 def test_combine(T, k, H):
@@ -310,7 +351,8 @@ def _ffn_gpu(x, w, order, pos, offsets, wg, wu, wd, variant, stream=None):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 3, 1, 128, 128), (2, 8, 3, 512, 384), (16, 24, 4, 1024, 640),
-                                       (70, 5, 2, 640, 256), (300, 4, 3, 512, 512)])
+                                       (70, 5, 2, 640, 256), (300, 4, 3, 512, 512),
+                                       (500, 3, 2, 512, 4096), (450, 3, 2, 768, 4096)])
 @pytest.mark.parametrize("holes", [False, True])
 def test_ffn_against_the_definition(orc, T, E, k, H, I, holes):
     """Against the 64-bit definition: bf16 roundings of each expert's output and

@@ -124,6 +124,42 @@ def test_more_adapters_than_rows(orc):
         _run(orc, M, 256, 384, n, 8, "each", n)
 
 
+@pytest.mark.parametrize("M,N", [(1024, 5120), (1100, 4096)])
+@pytest.mark.parametrize("kind", ["each", "runs"])
+def test_prompts(orc, M, N, kind):
+    """The ping-pong kernel's tiles, the last one partial."""
+    log(f"lora M={M} N={N} {kind}")
+    assert fp8q.fp8q_gemm_select(M, N, 384) == 5
+    _run(orc, M, N, 384, 4, 40, kind, M)
+
+
+def test_stacks_past_32_bits(orc):
+    """2000 adapters of 17408 x 128 B: 4.5e9 numbers; rows of the first and last."""
+    M, N, K, n, R = 6, 17408, 128, 2000, 128
+    log("lora stacks past 32 bits")
+    rng = np.random.default_rng(8)
+    x = synth.f32_to_bf16_bits(rng.normal(0, 1, (M, K)).astype(np.float32))
+    wq, ws = orc.quant_weight_block(rng.normal(0, 0.02, (N, K)).astype(np.float32))
+    ids = np.array([0, 1999, 1930, -1, 1, 1928], np.int32)
+    A = torch.zeros(n, R, K, dtype=torch.int16, device="cuda")
+    B = torch.zeros(n, N, R, dtype=torch.int16, device="cuda")
+    s = (0.5 + rng.random(n)).astype(np.float32)
+    a, a_s = orc.quant_act(x)
+    ref = orc.gemm_ref(a, a_s, wq, ws)
+    for m, i in enumerate(ids):
+        if i >= 0:
+            Ai = synth.f32_to_bf16_bits((rng.normal(0, 1, (R, K)) / np.sqrt(K)).astype(np.float32))
+            Bi = synth.f32_to_bf16_bits(rng.normal(0, 0.05, (N, R)).astype(np.float32))
+            A[int(i)], B[int(i)] = dev(Ai), dev(Bi)
+            ref[m] += float(s[i]) * (bf16_bits_to_f64(Bi) @ (bf16_bits_to_f64(Ai) @ bf16_bits_to_f64(x[m])))
+    out = Guarded((M, N), torch.int16)
+    work = torch.empty(fp8q.fp8q_proj_lora_workspace_bytes(M, N, K, R), dtype=torch.uint8, device="cuda")
+    fp8q.fp8q_proj_lora(dev(x), dev(wq), dev(ws), A, B, dev(s), dev(ids), out.t, *fp8q.alloc_proj_scratch(M, K), work)
+    torch.cuda.synchronize()
+    out.check_canary()
+    assert_tol(bf16_bits_to_f64(host(out.t)), ref, "lora stacks past 32 bits")
+
+
 def test_without_adapters_is_the_projection(orc):
     """Rows without an adapter get fp8q_proj's bits where it takes the same kernel."""
     M, N, K = 20, 512, 640
