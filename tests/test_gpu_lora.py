@@ -124,6 +124,33 @@ def test_more_adapters_than_rows(orc):
         _run(orc, M, 256, 384, n, 8, "each", n)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 256, 384), (16, 5120, 512), (40, 512, 640), (100, 1024, 8192), (200, 384, 512),
+                                   (1024, 5120, 384)])
+@pytest.mark.parametrize("where", ["a", "b", "scale"])
+def test_adapters_do_not_reach_other_rows(orc, M, N, K, where):
+    """Infinities and NaN in one adapter leave the rows of the others, and those
+    without one, bit for bit as they were."""
+    log(f"lora M={M} N={N} K={K} non-finite {where}")
+    args, want = _run(orc, M, N, K, 3, 16, "outside" if M < 1000 else "runs", M + K)
+    x, wq, ws, A, B, s, ids, out = args[:8]
+    who = host(ids)
+    ids.copy_(torch.from_numpy(np.where(np.arange(M) % 3 == 0, 1, who).astype(np.int32)))
+    fp8q.fp8q_proj_lora(*args)
+    torch.cuda.synchronize()
+    clean, others = host(out).copy(), host(ids) != 1
+    if where == "a":
+        A[1, :, ::7], A[1, :, 3] = 0x7F80, 0x7FC0
+    elif where == "b":
+        B[1, ::3], B[1, 1::3] = 0x7F80, 0x7FC0
+    else:
+        s[1] = float("nan")
+    fp8q.fp8q_proj_lora(*args)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(out)[others], clean[others])
+    if others.sum() < M:
+        assert not np.array_equal(host(out), clean)
+
+
 @pytest.mark.parametrize("M,N", [(1024, 5120), (1100, 4096)])
 @pytest.mark.parametrize("kind", ["each", "runs"])
 def test_prompts(orc, M, N, kind):

@@ -47,10 +47,14 @@ __device__ __forceinline__ void split_bf16(const v4f& v, float s, uint2& hi, uin
 // out[m, n] += scale[a] * sum_r v[m, r] * B[a][n, r] for the rows m of adapter
 // a, on the GEMM's accumulator layout (lane l: row l % 16 of its 16-row tile,
 // columns 4 * (l / 16) .. +3).  A wave walks the distinct adapters of its rows
-// (up to 64, a row a lane); for each, one pass over the rank in MFMA steps of 32
-// with the other rows' v zeroed.  The scaled v enters the bf16 product as the
-// sum of two bf16 numbers, so that the delta keeps about 16 bits of v, and the
-// accumulator is rounded once, with the base.
+// (up to 64, a row a lane); for each, one pass over the rank in MFMA steps of 32,
+// whose result only that adapter's rows take: the others keep their accumulators
+// (a zero v would not do: an adapter's infinities would reach them).  The scaled
+// v enters the bf16 product as the sum of two bf16 numbers, so that the delta
+// keeps about 16 bits of v, and the accumulator is rounded once, with the base.
+// Bound by reading B at decode (25 rows of 22 adapters, N = 17408, rank 64: 49 MB in
+// 13 us beside the base's 26); at prompts 15-25 us of the GEMM's 400 (M = 4576, N
+// = 5120, K = 17408, rank 32).
 struct LoraEpilogue {
   LoraArgs a;
 
@@ -106,6 +110,18 @@ struct LoraEpilogue {
     }
   }
 
+  // acc += b . (hi + lo) for the lanes of rows that are `own`
+  template <int TN, class Acc>
+  __device__ __forceinline__ void accumulate(Acc&& acc, int tm, const u32x4 (&b)[TN], const u32x4& hi,
+                                             const u32x4& lo, bool own) const {
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      const v4f sum = mfma_bf16_32(b[t], hi, mfma_bf16_32(b[t], lo, acc(tm, t)));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc(tm, t)[i] = own ? sum[i] : acc(tm, t)[i];
+    }
+  }
+
   // Many rows (prompts: one or two adapters a wave): the wave takes its own
   // rows' adapters one after another, v read where it is used.
   template <int TM, int TN, class Acc>
@@ -146,11 +162,7 @@ struct LoraEpilogue {
         split_bf16(v[0][0], s, h0, r0);
         split_bf16(v[0][1], s, h1, r1);
         const u32x4 hi = {h0.x, h0.y, h1.x, h1.y}, lo = {r0.x, r0.y, r1.x, r1.y};
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          acc(tm, t) = mfma_bf16_32(b[t], lo, acc(tm, t));
-          acc(tm, t) = mfma_bf16_32(b[t], hi, acc(tm, t));
-        }
+        accumulate<TN>(acc, tm, b, hi, lo, (it.mine >> (16 * tm + l16)) & 1);
       }
     }
   }
@@ -204,17 +216,14 @@ struct LoraEpilogue {
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm) {
         if (((mine >> (16 * tm)) & 0xFFFF) == 0) continue;  // uniform
+        const bool own = (mine >> (16 * tm + l16)) & 1;
         u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-        if ((mine >> (16 * tm + l16)) & 1) {
+        if (own) {
           const uint8_t* at = smem + (16 * tm + l16) * pitch + 2 * k;
           hi = *reinterpret_cast<const u32x4*>(at);
           lo = *reinterpret_cast<const u32x4*>(at + 2 * a.ld);
         }
-#pragma unroll
-        for (int t = 0; t < TN; ++t) {
-          acc(tm, t) = mfma_bf16_32(b[t], lo, acc(tm, t));
-          acc(tm, t) = mfma_bf16_32(b[t], hi, acc(tm, t));
-        }
+        accumulate<TN>(acc, tm, b, hi, lo, own);
       }
     };
     while (more) {
