@@ -638,7 +638,8 @@ __global__ __launch_bounds__(512) void gemm_decode_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t M, uint32_t N, uint32_t K,
     uint32_t Mp, uint32_t units_base, uint32_t units_rem) {
-  gemm_decode_body<TM, GW, ROW>(A, As, W, Ws, out, M, N, K, Mp, units_base, units_rem, NoEpilogue{});
+  const NoEpilogue epi{};
+#include "gemm_decode_body.h"
 }
 
 template <int TM, int GW, bool ROW>
