@@ -73,7 +73,7 @@ BF16_PEAK_TFLOPS = 2500.0  # MI355X dense bf16 MFMA, TFLOP/s
 # the HBM-bytes summary under profiles/).
 # Valid only for the kernel source they were taken with: reported as null
 # once the ping-pong kernel's source changes (gemm_source_hash).
-GEMM_TRAFFIC = {"bytes": 1.2195e+09 + 4.7055e+07, "gemm_source_sha256": "0a510050a0b1e2be"}
+GEMM_TRAFFIC = {"bytes": 1.2195e+09 + 4.7055e+07, "gemm_source_sha256": "997b2d9515942153"}
 
 
 def gemm_source_hash():

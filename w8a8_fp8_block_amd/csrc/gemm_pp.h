@@ -475,8 +475,8 @@ __device__ __forceinline__ void gemm_pp_body(
     }
   }
 
-  epi.template add<TM, TN>([&](int tm, int tn) -> v4f& { return acc[tm][tn]; },
-                           m0 + wm * C::WM, n0 + wn * C::WN, M, lane, 0);
+  epi.template add<TM, TN, C::NT, C::BM>([&](int tm, int tn) -> v4f& { return acc[tm][tn]; }, smem, m0,
+                                         wm * C::WM, n0 + wn * C::WN, M, lane, 0);
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm) {
     const uint32_t m = m0 + wm * C::WM + tm * 16 + l16;

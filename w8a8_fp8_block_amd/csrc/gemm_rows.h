@@ -22,12 +22,14 @@ struct DenseRows {
   __device__ __forceinline__ uint32_t pad_end(uint32_t Mp) const { return Mp; }
 };
 
-// Adds nothing to the accumulators.  An epilogue adds to a wave's TM x TN tiles
-// of 16 x 16 (rows m0.., columns n0..): `add` in the tiled kernels, wave by wave;
-// `add_shared` in the decode-width ones, by the whole workgroup with its LDS.
+// Adds nothing to the accumulators.  An epilogue adds to a wave's TM x TN tiles of
+// 16 x 16, called by the whole workgroup with its LDS: `add` in the tiled kernels,
+// where the wave's rows are band.. of the workgroup's BM, `add_shared` in the
+// decode-width ones, where the waves hold the same rows and columns.
 struct NoEpilogue {
-  template <int TM, int TN, class Acc>
-  __device__ __forceinline__ void add(Acc&&, uint32_t, uint32_t, uint32_t, uint32_t, uint32_t) const {}
+  template <int TM, int TN, int NT, int BM, class Acc>
+  __device__ __forceinline__ void add(Acc&&, uint8_t*, uint32_t, uint32_t, uint32_t, uint32_t, uint32_t,
+                                      uint32_t) const {}
   template <int TM, int TN, int NT, class Acc>
   __device__ __forceinline__ void add_shared(Acc&&, uint8_t*, uint32_t, uint32_t, uint32_t, uint32_t, uint32_t,
                                              uint32_t) const {}

@@ -122,118 +122,113 @@ struct LoraEpilogue {
     }
   }
 
-  // Many rows (prompts: one or two adapters a wave): the wave takes its own
-  // rows' adapters one after another, v read where it is used.
-  template <int TM, int TN, class Acc>
-  __device__ __forceinline__ void add(Acc&& acc, uint32_t m0, uint32_t n0, uint32_t M, uint32_t lane,
-                                      uint32_t split) const {
-    if (split != 0) return;  // split-K: the first part adds
-    const uint32_t l16 = lane & 15, q = lane >> 4;
-    Items it = items<TM>(m0, M, lane, 0, 1);
-    while (it.next()) {
-      const uint32_t k = 32 * it.step + 8 * q;
-      const float s = a.scale[it.ad];
-      u32x4 b[TN];
-      load_b<TN>(b, it.ad, k, n0, l16);
-      zero_past_rank<TN>(b, k);
+  // v of `rows` rows from m0 on, summed over its parts, scaled and split, into LDS
+  // by the workgroup's NT threads: rows of pitch() bytes, the high halves of ld
+  // values, then the low ones.  (Rows without an adapter: unused values.)
+  __device__ __forceinline__ uint32_t pitch() const { return a.ld * 4 + 16; }
+  template <int NT>
+  __device__ __forceinline__ void stage(uint8_t* smem, uint32_t m0, uint32_t rows) const {
+    const uint32_t quads = a.ld / 4;
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < rows * quads; i += NT) {
+      const uint32_t r = i / quads, c = i % quads;
+      const float* from = a.v + (uint64_t)(m0 + r) * a.parts * a.ld + 4 * c;
+      v4f v[kLoraMaxParts];
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm) {
-        if (((it.mine >> (16 * tm)) & 0xFFFF) == 0) continue;  // uniform
-        v4f v[kLoraMaxParts][2];
-        if ((it.mine >> (16 * tm + l16)) & 1) {
-          const float* from = a.v + (uint64_t)(m0 + 16 * tm + l16) * a.parts * a.ld + k;
+      for (uint32_t p = 0; p < kLoraMaxParts; ++p)  // (the last part again past the end: not added)
+        v[p] = *reinterpret_cast<const v4f*>(from + min(p, a.parts - 1) * a.ld);
+      const float s = a.scale[min((uint32_t)a.ids[m0 + r], a.adapters - 1)];
 #pragma unroll
-          for (uint32_t p = 0; p < kLoraMaxParts; ++p) {  // (the last part again past the end: not added)
-            v[p][0] = *reinterpret_cast<const v4f*>(from + min(p, a.parts - 1) * a.ld);
-            v[p][1] = *reinterpret_cast<const v4f*>(from + min(p, a.parts - 1) * a.ld + 4);
-          }
-        } else {
-#pragma unroll
-          for (uint32_t p = 0; p < kLoraMaxParts; ++p) v[p][0] = v[p][1] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-#pragma unroll
-        for (uint32_t p = 1; p < kLoraMaxParts; ++p) {
-          if (p < a.parts) {
-            v[0][0] += v[p][0];
-            v[0][1] += v[p][1];
-          }
-        }
-        uint2 h0, h1, r0, r1;
-        split_bf16(v[0][0], s, h0, r0);
-        split_bf16(v[0][1], s, h1, r1);
-        const u32x4 hi = {h0.x, h0.y, h1.x, h1.y}, lo = {r0.x, r0.y, r1.x, r1.y};
-        accumulate<TN>(acc, tm, b, hi, lo, (it.mine >> (16 * tm + l16)) & 1);
-      }
+      for (uint32_t p = 1; p < kLoraMaxParts; ++p)
+        if (p < a.parts) v[0] += v[p];
+      uint2 hi, lo;
+      split_bf16(v[0], s, hi, lo);
+      *reinterpret_cast<uint2*>(smem + r * pitch() + 8 * c) = hi;
+      *reinterpret_cast<uint2*>(smem + r * pitch() + 2 * a.ld + 8 * c) = lo;
     }
   }
 
-  // Few rows (decode: up to an adapter a row): the workgroup's NT threads sum,
-  // scale and split v of its rows into LDS once; then its waves share the items,
-  // each with the B fragments of the next one in flight.  Called by the whole
-  // workgroup; LDS must be free before and is free after.  At most
-  // 64 * (128 * 4 + 16) bytes of it are used.
+  // One item's B fragments and what it applies to
+  template <int TN>
+  struct Fetched {
+    u32x4 b[TN];
+    uint32_t k;
+    uint64_t mine;
+  };
+  // The next item's loads; after the last one, loads all the same (of any adapter,
+  // in bounds), so that no branch hides them from the waits.
+  template <int TN>
+  __device__ __forceinline__ bool fetch(Items& it, Fetched<TN>& f, uint32_t n0, uint32_t l16, uint32_t q) const {
+    const bool more = it.next();
+    f.k = 32 * it.step + 8 * q;
+    f.mine = it.mine;
+    load_b<TN>(f.b, it.ad, f.k, n0, l16);
+    sched_fence();
+    return more;
+  }
+  // f applied to the wave's rows, whose v starts at `v` in LDS
+  template <int TM, int TN, class Acc>
+  __device__ __forceinline__ void apply(Acc&& acc, Fetched<TN>& f, const uint8_t* v, uint32_t l16) const {
+    zero_past_rank<TN>(f.b, f.k);
+#pragma unroll
+    for (int tm = 0; tm < TM; ++tm) {
+      if (((f.mine >> (16 * tm)) & 0xFFFF) == 0) continue;  // uniform
+      const bool own = (f.mine >> (16 * tm + l16)) & 1;
+      u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
+      if (own) {
+        const uint8_t* at = v + (16 * tm + l16) * pitch() + 2 * f.k;
+        hi = *reinterpret_cast<const u32x4*>(at);
+        lo = *reinterpret_cast<const u32x4*>(at + 2 * a.ld);
+      }
+      accumulate<TN>(acc, tm, f.b, hi, lo, own);
+    }
+  }
+  // All items from the one in f0 on, each with the next one's B in flight
+  template <int TM, int TN, class Acc>
+  __device__ __forceinline__ void apply_all(Acc&& acc, Items& it, Fetched<TN>& f0, bool more, const uint8_t* v,
+                                            uint32_t n0, uint32_t l16, uint32_t q) const {
+    Fetched<TN> f1;
+    while (more) {
+      more = fetch<TN>(it, f1, n0, l16, q);
+      apply<TM, TN>(acc, f0, v, l16);
+      const bool again = fetch<TN>(it, f0, n0, l16, q);
+      if (!more) break;
+      apply<TM, TN>(acc, f1, v, l16);
+      more = again;
+    }
+  }
+
+  // Tiled kernels: the workgroup stages v of its BM rows, where the operand ring
+  // was (BM * (128 * 4 + 16) bytes at most); then each wave takes the adapters of
+  // its own rows, band .. band + 16 * TM.
+  template <int TM, int TN, int NT, int BM, class Acc>
+  __device__ __forceinline__ void add(Acc&& acc, uint8_t* smem, uint32_t m0, uint32_t band, uint32_t n0, uint32_t M,
+                                      uint32_t lane, uint32_t split) const {
+    if (split != 0) return;  // split-K: the first part adds
+    const uint32_t l16 = lane & 15, q = lane >> 4;
+    Items it = items<TM>(m0 + band, M, lane, 0, 1);
+    Fetched<TN> f;
+    const bool more = fetch<TN>(it, f, n0, l16, q);
+    __syncthreads();  // every wave is done with the ring
+    stage<NT>(smem, m0, min((uint32_t)BM, M - m0));
+    __syncthreads();
+    apply_all<TM, TN>(acc, it, f, more, smem + band * pitch(), n0, l16, q);
+  }
+
+  // Decode widths (up to an adapter a row): the waves hold the same rows and
+  // share the items.  LDS must be free before and is free after; at most 64 *
+  // (128 * 4 + 16) bytes of it are used.
   template <int TM, int TN, int NT, class Acc>
   __device__ __forceinline__ void add_shared(Acc&& acc, uint8_t* smem, uint32_t m0, uint32_t n0, uint32_t M,
                                              uint32_t lane, uint32_t first, uint32_t stride) const {
     const uint32_t l16 = lane & 15, q = lane >> 4;
     Items it = items<TM>(m0, M, lane, first, stride);
     if (it.left == 0) return;  // uniform over the workgroup
-    u32x4 b0[TN], b1[TN];
-    uint32_t k0 = 0, k1 = 0;
-    uint64_t mine0 = 0, mine1 = 0;
-    // the next item's loads; after the last one, loads all the same (of any
-    // adapter, in bounds), so that no branch hides them from the waits
-    auto load = [&](u32x4 (&b)[TN], uint32_t& k, uint64_t& mine) __attribute__((always_inline)) -> bool {
-      const bool more = it.next();
-      k = 32 * it.step + 8 * q;
-      mine = it.mine;
-      load_b<TN>(b, it.ad, k, n0, l16);
-      sched_fence();
-      return more;
-    };
-    bool more = load(b0, k0, mine0);
-    // rows of `pitch` bytes: the high halves of ld values, then the low ones
-    const uint32_t pitch = a.ld * 4 + 16, quads = a.ld / 4, rows = min(16u * TM, M - m0);
-    for (uint32_t i = threadIdx.x; i < rows * quads; i += NT) {
-      const uint32_t r = i / quads, c = i % quads, id = lora_id(a, m0 + r);
-      if (id == 0xFFFFFFFFu) continue;
-      const float* from = a.v + (uint64_t)(m0 + r) * a.parts * a.ld + 4 * c;
-      v4f v[kLoraMaxParts];
-#pragma unroll
-      for (uint32_t p = 0; p < kLoraMaxParts; ++p)
-        v[p] = *reinterpret_cast<const v4f*>(from + min(p, a.parts - 1) * a.ld);
-#pragma unroll
-      for (uint32_t p = 1; p < kLoraMaxParts; ++p)
-        if (p < a.parts) v[0] += v[p];
-      uint2 hi, lo;
-      split_bf16(v[0], a.scale[id], hi, lo);
-      *reinterpret_cast<uint2*>(smem + r * pitch + 8 * c) = hi;
-      *reinterpret_cast<uint2*>(smem + r * pitch + 2 * a.ld + 8 * c) = lo;
-    }
+    Fetched<TN> f;
+    const bool more = fetch<TN>(it, f, n0, l16, q);
+    stage<NT>(smem, m0, min(16u * TM, M - m0));
     __syncthreads();
-    auto apply = [&](u32x4 (&b)[TN], uint32_t k, uint64_t mine) __attribute__((always_inline)) {
-      zero_past_rank<TN>(b, k);
-#pragma unroll
-      for (int tm = 0; tm < TM; ++tm) {
-        if (((mine >> (16 * tm)) & 0xFFFF) == 0) continue;  // uniform
-        const bool own = (mine >> (16 * tm + l16)) & 1;
-        u32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
-        if (own) {
-          const uint8_t* at = smem + (16 * tm + l16) * pitch + 2 * k;
-          hi = *reinterpret_cast<const u32x4*>(at);
-          lo = *reinterpret_cast<const u32x4*>(at + 2 * a.ld);
-        }
-        accumulate<TN>(acc, tm, b, hi, lo, own);
-      }
-    };
-    while (more) {
-      more = load(b1, k1, mine1);
-      apply(b0, k0, mine0);
-      const bool again = load(b0, k0, mine0);
-      if (!more) break;
-      apply(b1, k1, mine1);
-      more = again;
-    }
+    apply_all<TM, TN>(acc, it, f, more, smem, n0, l16, q);
     __syncthreads();
   }
 };

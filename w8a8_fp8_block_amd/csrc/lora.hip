@@ -19,8 +19,8 @@ namespace {
 // Quantize and shrink, one pass over x: the FP8 codes and scales of x (the
 // activation quantizer's steps) and v[m, r] = sum_k x[m, k] * A[a][r, k] in fp32
 // from bf16.  A workgroup takes 16 * TM rows and one part of K, its four waves
-// every fourth 128-group of it; blockIdx.z picks among the rows' distinct
-// adapters (round robin), and z = 0 quantizes as well.  A lane holds values k =
+// every fourth 128-group of it; blockIdx.z picks the rank tiles (`chunks` of NR)
+// and among the rows' distinct adapters (round robin); z = 0 quantizes as well.  A lane holds values k =
 // 64 h + 16 (l / 16) .. + 15, h < 2, of row l % 16 in the group, the other 96 in
 // the lanes 16, 32 and 48 away: its codes are two 16-byte stores, and its
 // 16-byte pieces are operands of the 16x16x32 MFMA as they stand (in an order of
@@ -69,7 +69,7 @@ template <int TM, int NR>
 __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ A, float* __restrict__ v, QuantOut out,
     const int32_t* ids, uint32_t M, uint32_t K, uint32_t Mp, uint32_t adapters, uint32_t rank, uint32_t ld,
-    uint32_t parts) {
+    uint32_t parts, uint32_t chunks) {
   __shared__ v4f red[4][NR][64];
   const uint32_t lane = threadIdx.x & 63;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -81,6 +81,7 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
   if (lane < 16 * TM && row < M) id = (uint32_t)ids[row];
   if (id >= adapters) id = 0xFFFFFFFFu;
   uint64_t left = __builtin_amdgcn_ballot_w64(id != 0xFFFFFFFFu);
+  const uint32_t turns = gridDim.z / chunks, t0 = blockIdx.z % chunks * NR;  // this workgroup's rank tiles
   bool quantize = blockIdx.z == 0;
   const uint16_t* xr[TM];
 #pragma unroll
@@ -119,11 +120,11 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
     const uint32_t ad = (uint32_t)__builtin_amdgcn_readlane((int)id, __builtin_ctzll(left));
     const uint64_t mine = __builtin_amdgcn_ballot_w64(id == ad);
     left &= ~mine;
-    if (turn % gridDim.z != blockIdx.z) continue;
+    if (turn % turns != blockIdx.z / chunks) continue;
     const uint16_t* ar[NR];
 #pragma unroll
     for (int t = 0; t < NR; ++t)
-      ar[t] = A + ((uint64_t)ad * rank + min(16 * t + l16, rank - 1)) * K + 16 * q;
+      ar[t] = A + ((uint64_t)ad * rank + min(16 * (t0 + t) + l16, rank - 1)) * K + 16 * q;
     v4f acc[TM][NR];
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm)
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < (NR + 3) / 4; ++j) {
-        const uint32_t t = 4 * j + wave, k = 16 * t + 4 * q;
+        const uint32_t t = 4 * j + wave, k = 16 * (t0 + t) + 4 * q;
         if (t < (uint32_t)NR && ((mine >> r) & 1) && k < ld) {
           v4f s = red[0][t][lane];
 #pragma unroll
@@ -195,28 +196,28 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
   }
 }
 
-// Rows up to here go in tiles of 16, their adapters dealt over workgroups;
-// beyond, in tiles of 32 (prompts: long runs of one adapter), one workgroup
-// taking all of a tile's.
+// Rows up to here go in tiles of 16, 32 ranks a workgroup, their adapters dealt over
+// workgroups; beyond, in tiles of 32.
 constexpr uint32_t kShrinkSmallM = 256;
 
 template <int TM, int NR>
 hipError_t launch_shrink_cfg(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v,
                              const QuantOut& out, uint32_t M, uint32_t K, hipStream_t s) {
-  const uint32_t tiles = (M + 16 * TM - 1) / (16 * TM);
-  const uint32_t z = TM == 1 ? std::min(std::min(16u, M), l.adapters) : 1;
-  lora_quant_shrink_kernel<TM, NR><<<dim3(tiles, l.parts, z), dim3(256), 0, s>>>(
-      x, a, v, out, l.ids, M, K, m_pad16(M), l.adapters, l.rank, l.ld, l.parts);
+  // rank tiles up to ld, so that the zeros beyond the rank are written too
+  const uint32_t tiles = (M + 16 * TM - 1) / (16 * TM), chunks = (l.ld / 16 + NR - 1) / NR;
+  // one workgroup an adapter for few rows; for more, as many as leave no CU idle
+  const uint32_t most = TM == 1 ? 16u : std::max(1u, std::min(8u, 512 / (tiles * l.parts * chunks)));
+  const uint32_t z = std::min(std::min(most, M), l.adapters);
+  lora_quant_shrink_kernel<TM, NR><<<dim3(tiles, l.parts, z * chunks), dim3(256), 0, s>>>(
+      x, a, v, out, l.ids, M, K, m_pad16(M), l.adapters, l.rank, l.ld, l.parts, chunks);
   return hipGetLastError();
 }
 
-template <int TM>
 hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v,
                          const QuantOut& out, uint32_t M, uint32_t K, hipStream_t s) {
-  // rank tiles up to ld, so that the zeros beyond the rank are written too
-  if (l.ld <= 32) return launch_shrink_cfg<TM, 2>(x, a, l, v, out, M, K, s);
-  if (l.ld <= 64) return launch_shrink_cfg<TM, 4>(x, a, l, v, out, M, K, s);
-  return launch_shrink_cfg<TM, 8>(x, a, l, v, out, M, K, s);
+  if (M <= kShrinkSmallM) return launch_shrink_cfg<1, 2>(x, a, l, v, out, M, K, s);
+  return l.ld <= 32 ? launch_shrink_cfg<2, 2>(x, a, l, v, out, M, K, s)
+                    : launch_shrink_cfg<2, 4>(x, a, l, v, out, M, K, s);
 }
 
 // ------------------------------------------------------------------------
@@ -327,6 +328,7 @@ hipError_t launch_decode(const Gemm& g, uint32_t gw, uint32_t grid, uint32_t bas
 template <int STAGES, bool SPLIT>
 hipError_t launch_tiled(const Gemm& g, uint32_t splits, float* part, const LoraArgs& l, hipStream_t s) {
   using C = TileCfg<128, 128, 2, 2, STAGES, false>;
+  static_assert(128 * (kMaxLoraRank * 4 + 16) <= C::LDS_BYTES, "the rows' v in the operand ring");
   const hipError_t e = allow_lds<&lora_tiled_kernel<STAGES, SPLIT>, C::LDS_BYTES>();
   if (e != hipSuccess) return e;
   const uint32_t tiles_m = (g.M + 127) / 128, tiles_n = g.N / 128;
@@ -337,6 +339,7 @@ hipError_t launch_tiled(const Gemm& g, uint32_t splits, float* part, const LoraA
 
 hipError_t launch_pp(const Gemm& g, const LoraArgs& l, hipStream_t s) {
   using C = PpCfg<3, false, false>;
+  static_assert(C::BM * (kMaxLoraRank * 4 + 16) <= C::LDS_BYTES, "the rows' v in the operand ring");
   const hipError_t e = allow_lds<&lora_pp_kernel, C::LDS_BYTES>();
   if (e != hipSuccess) return e;
   const uint32_t tiles_m = (g.M + 255) / 256, tiles_n = g.N / 128;
@@ -370,7 +373,7 @@ hipError_t launch_lora_quant_shrink(const uint16_t* x, const uint16_t* a, const 
   l.parts = lora_parts(M, K);
   float* v = static_cast<float*>(workspace);
   const QuantOut out{x_q, x_s_rm, x_s_km};
-  return M <= kShrinkSmallM ? launch_shrink<1>(x, a, l, v, out, M, K, s) : launch_shrink<2>(x, a, l, v, out, M, K, s);
+  return launch_shrink(x, a, l, v, out, M, K, s);
 }
 
 hipError_t launch_lora_gemm(const uint8_t* a, const float* a_s_km, const uint8_t* w, const float* w_s,
