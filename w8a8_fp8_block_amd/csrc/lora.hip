@@ -28,7 +28,7 @@ namespace {
 // (NR rank tiles of 16) and the rows of that adapter are stored; adapters after
 // a workgroup's first read its rows again, from L2.  Bound by reading A (decode:
 // a few rows an adapter) or x (prompts): 25 rows of 22 adapters, rank 64, K = 5120:
-// 9.5 us for 14 MB of A, two launches' latencies; M = 1168, rank 24: 16 us; M =
+// 7.7 us for 14 MB of A, a launch and two latencies; M = 1168, rank 24: 16 us; M =
 // 4576, K = 17408, rank 32: 97 us for 240 MB of x and codes, 2.5 TB/s.  There 70 us remain
 // without the quantization and 75 without A: the reads of 32 rows 34 KB apart; more
 // workgroups a CU (registers spill) and 64 rows a workgroup were slower.
@@ -196,8 +196,11 @@ __global__ __launch_bounds__(256) void lora_quant_shrink_kernel(
   }
 }
 
-// Rows up to here go in tiles of 16, 32 ranks a workgroup, their adapters dealt over
-// workgroups; beyond, in tiles of 32.
+// Rows up to here go in tiles of 16, their adapters dealt over workgroups; beyond, in
+// tiles of 32.  32 ranks a workgroup: with all 128 in one, M = 3, K = 16128 took 31.9
+// us instead of 11.1, and M = 258, K = 1792, rank 96, 48 requests 49.6 instead of
+// 11.6 (there 64 ranks: 10.2; at M = 3270, K = 5760, rank 128 32 or 64 ranks: 63.5 /
+// 61.7).
 constexpr uint32_t kShrinkSmallM = 256;
 
 template <int TM, int NR>
@@ -216,8 +219,7 @@ hipError_t launch_shrink_cfg(const uint16_t* x, const uint16_t* a, const LoraArg
 hipError_t launch_shrink(const uint16_t* x, const uint16_t* a, const LoraArgs& l, float* v,
                          const QuantOut& out, uint32_t M, uint32_t K, hipStream_t s) {
   if (M <= kShrinkSmallM) return launch_shrink_cfg<1, 2>(x, a, l, v, out, M, K, s);
-  return l.ld <= 32 ? launch_shrink_cfg<2, 2>(x, a, l, v, out, M, K, s)
-                    : launch_shrink_cfg<2, 4>(x, a, l, v, out, M, K, s);
+  return launch_shrink_cfg<2, 2>(x, a, l, v, out, M, K, s);
 }
 
 // ------------------------------------------------------------------------
