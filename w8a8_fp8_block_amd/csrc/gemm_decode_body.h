@@ -92,6 +92,7 @@
 #pragma unroll
       for (int j = 1; j < GW; ++j) acc[t][tm] += p[j] * (as[j][tm] * ws[j][t]);
     }
+  wait_lgkm0();  // this wave's reads of the weight rows (s_barrier alone waits for none)
   wg_barrier();  // every wave done with the weight rows: LDS takes the partial tiles
   epi.template add_shared<TM, NT, 512>([&](int tm, int t) -> v4f& { return acc[t][tm]; }, smem, 0, c0, M, lane,
                                        wave, 8);
@@ -100,6 +101,7 @@
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) red[((wave * NT + t) * TM + tm) * 64 + lane] = acc[t][tm];
+  wait_lgkm0();
   wg_barrier();
   // waves share the final sums: wave v adds and stores tiles (t, tm) with
   // t*TM + tm = v (mod 8), the partials in wave order
