@@ -690,8 +690,8 @@ size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k,
  *   lora_a       [adapters,rank,K] bf16, lora_b [adapters,N,rank] bf16,
  *                lora_scale [adapters] fp32, adapter_ids [M] int32, read only;
  *                an adapter of smaller rank is padded with zeros
- *   workspace    fp8q_proj_lora_workspace_bytes(M, N, K, rank) bytes; contents
- *                undefined on return; calls in flight must not share it
+ *   workspace    fp8q_proj_lora_workspace_bytes(M, N, K, rank) bytes (0 for M ==
+ *                0); contents undefined on return; calls in flight must not share it
  *   the other arguments as for fp8q_proj
  * 8 <= rank <= FP8Q_MAX_LORA_RANK, rank % 8 == 0, adapters >= 1; element counts
  * of one adapter's A and B below 2^32 (the stacks may be larger).  Rows of one

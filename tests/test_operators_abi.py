@@ -2,6 +2,9 @@
 needed, no kernel launched): every call here fails a check, or is an empty call
 that returns before anything is enqueued."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -167,3 +170,29 @@ def test_binding_refusals():
                       ("logits", torch.zeros(E, T).t())):
         with pytest.raises((ValueError, TypeError)):
             fp8q.fp8q_moe_route(*{**good, name: bad}.values(), None)
+
+
+def test_size_queries_of_any_numbers():
+    """The size and selection queries return for an empty batch and for numbers that no
+    call accepts (in a process of their own: a division by zero ends it)."""
+    code = """
+import itertools
+import w8a8_fp8_block_amd as fp8q
+L = fp8q.lib()
+rows = [0, 1, 16, 17, 256, 257, (1 << 31) - 1, 1 << 31, 2**32 - 256, 2**32 - 128, 2**32 - 32, 2**32 - 16, 2**32 - 1]
+cols = [0, 1, 128, 5120, 2**32 - 128, 2**32 - 1]
+few = [0, 1, 8, 128, 512, 2**32 - 1]
+for m, n, k, r in itertools.product(rows, cols, cols, few):
+    L.fp8q_proj_lora_workspace_bytes(m, n, k, r)
+    L.fp8q_moe_ffn_workspace_bytes(m, r, 2, n, k, 0)
+    L.fp8q_moe_ffn_workspace_bytes(m, 8, r, n, k, 2)
+for m, r, n in itertools.product(rows, few, cols):
+    L.fp8q_moe_route_workspace_bytes(m, r, n)
+    L.fp8q_group_rows_workspace_bytes(m, r)
+    L.fp8q_gemm_grouped_select(m, r, n)
+    L.fp8q_moe_ffn_select(m, r, 2, n)
+assert fp8q.fp8q_proj_lora_workspace_bytes(0, 512, 512, 16) == 0
+assert fp8q.fp8q_moe_ffn_workspace_bytes(0, 8, 2, 512, 512) == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0

@@ -6,6 +6,7 @@
 // of K), and the projection's own GEMM kernels run with an epilogue that adds scale * v . B^T to
 // their fp32 accumulators (lora.h), so that the sum is rounded once and out is
 // written once.
+#include <algorithm>
 #include <atomic>
 
 #include "gemm_pp.h"
@@ -352,10 +353,12 @@ hipError_t launch_pp(const Gemm& g, const LoraArgs& l, hipStream_t s) {
 uint32_t lora_ld(uint32_t rank) { return (rank + 31) / 32 * 32; }
 
 // Parts of K of the shrink: as many as keep the grid within 512 workgroups (two
-// a CU, one round), with at least four groups (one a wave) in each.
+// a CU, one round), with at least four groups (one a wave) in each.  (Any M: the
+// size query takes an empty batch and numbers no call accepts.)
 uint32_t lora_parts(uint32_t M, uint32_t K) {
-  const uint32_t wgs = M <= kShrinkSmallM ? (M + 15) / 16 * std::min(16u, M) : (M + 31) / 32;
-  return std::max(1u, std::min(std::min(kLoraMaxParts, 512 / wgs), K / (4 * kGroup)));
+  const uint64_t wgs = M <= kShrinkSmallM ? (M + 15) / 16 * std::min(16u, M) : ((uint64_t)M + 31) / 32;
+  const uint32_t fit = (uint32_t)(512 / std::max<uint64_t>(wgs, 1));
+  return std::max(1u, std::min(std::min(kLoraMaxParts, fit), K / (4 * kGroup)));
 }
 
 }  // namespace
