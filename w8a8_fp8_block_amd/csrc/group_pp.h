@@ -137,7 +137,7 @@ __device__ __forceinline__ void group_persist_body(const uint8_t* __restrict__ A
     const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, g.a_rows * K), rS = make_rsrc(As, G * Mp * 4);
     const __amdgpu_buffer_rsrc_t rO = make_rsrc(g.order ? g.order : g.offsets, g.order ? g.R * 4 : 4);
     __amdgpu_buffer_rsrc_t rW, rWs, rWs2;  // FFN: gate's (group 1) or up's (group 0) weights; gate's, up's scales
-    uint32_t s_off = 0, ws_off = 0;
+    uint32_t s_off = 0, ws_off = 0, ws_off2 = 0;  // ws_off: columns 0-127's scales, ws_off2: 128-255's
 
     // ---- load cursor: tile, block, and the set of the row table it uses ----
     Tile lt;
@@ -166,7 +166,8 @@ __device__ __forceinline__ void group_persist_body(const uint8_t* __restrict__ A
       } else {
         const uint32_t r = wm * C::WM + lane;
         s_off = src(min(r, lt.end - 1 - lt.m0)) * 4;
-        ws_off = lt.n0 / kGroup * G * 4;
+        ws_off = scale_row(lt.n0, 0, N) * G * 4;
+        ws_off2 = scale_row(lt.n0, 1, N) * G * 4;
         rWs = make_rsrc(Ws + (uint64_t)lt.expert * (N / kGroup) * G, (N / kGroup) * G * 4);
         if constexpr (FFN) rWs2 = make_rsrc(ffn.ws_up + (uint64_t)lt.expert * (N / kGroup) * G, (N / kGroup) * G * 4);
       }
@@ -207,7 +208,7 @@ __device__ __forceinline__ void group_persist_body(const uint8_t* __restrict__ A
         if constexpr (FFN)
           dma4_at(rWs2, 0, ws_off + kb * 4, lds + my_sc + 256);
         else
-          dma4_at(rWs, 0, ws_off + G * 4 + kb * 4, lds + my_sc + 256);
+          dma4_at(rWs, 0, ws_off2 + kb * 4, lds + my_sc + 256);
         dma4_at(rWs, 0, ws_off + kb * 4, lds + p_sc + 256);
       }
       // with a tile's first block: the row table of the tile after it (waves 0

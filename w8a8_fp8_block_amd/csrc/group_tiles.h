@@ -114,6 +114,15 @@ __device__ __forceinline__ bool group_tile(const Groups& g, uint32_t tiles_n, ui
   return true;
 }
 
+// Weight-scale row (of N / 128) of columns n0 + 128 * half .. + 127.  A 256-column
+// tile's second half may lie past N (N / 128 odd): its results are not stored, and it
+// takes the last row, since a scale's place is a load's scalar offset, which the
+// buffer's bound does not hold.
+__host__ __device__ __forceinline__ uint32_t scale_row(uint32_t n0, uint32_t half, uint32_t N) {
+  const uint32_t row = n0 / kGroup + half, last = N / kGroup - 1;
+  return row < last ? row : last;
+}
+
 // Most row tiles of bm rows that R rows in E groups can need.
 inline uint32_t max_row_tiles(uint32_t R, uint32_t E, uint32_t bm) {
   const uint64_t g = R < E ? R : E;
