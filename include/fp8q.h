@@ -607,7 +607,8 @@ size_t fp8q_group_rows_workspace_bytes(uint32_t n, uint32_t groups);
 
 /* out[t] = bf16_rne( sum over j, in order, of weights[t][j] * y[pos[t][j]] ) in
  * fp32: the experts' outputs y [R,H] bf16 (sorted rows) back to the tokens.
- * Slots without an expert add nothing; a token with none gets zeros.
+ * Slots without an expert add nothing; a token with none gets zeros.  Plans that
+ * are not groupings give unspecified rows; y is read in bounds.
  * H % 8 == 0, T*top_k < 2^31, R*H < 2^32. */
 fp8q_status fp8q_moe_combine(const uint16_t *y_bf16, const float *weights,
                              const int32_t *pos, const int32_t *offsets,
@@ -663,8 +664,8 @@ int fp8q_gemm_grouped_select(uint32_t R, uint32_t E, uint32_t N);
  * sums the output is off by about 3e-3 of its norm (2.4e-3 where the weights are
  * streamed, a few rows an expert: those products run in f16), the rounding of
  * the formats themselves included (1.7e-3).
- * H % 128 == 0, I % 128 == 0.  x is quantized once a token.  Limits as
- * fp8q_gemm_grouped (with R = T*top_k rows of H and of I). */
+ * H % 128 == 0, I % 128 == 0.  x is quantized once a token.  Limits, and plans that
+ * are not groupings, as for fp8q_gemm_grouped (with R = T*top_k rows of H and of I). */
 fp8q_status fp8q_moe_ffn(const uint16_t *x_bf16, const float *weights,
                          const int32_t *order, const int32_t *pos,
                          const int32_t *offsets, const uint8_t *w_gate,

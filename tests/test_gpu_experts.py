@@ -303,6 +303,32 @@ def test_combine(T, k, H):
         assert not got[0].any()
 
 
+@pytest.mark.parametrize("taken", [12, 17, 2 ** 31 - 1, -1])
+def test_combine_keeps_to_the_rows(taken):
+    """Whatever offsets[E] and pos hold, rows past the T * top_k of y are not read: such
+    slots add nothing.  (The rows behind y here are NaN.)"""
+    log(f"combine with offsets[E]={taken}")
+    T, k, H, E = 4, 3, 264, 5
+    rng = np.random.default_rng(3)
+    pos = rng.permutation(T * k).astype(np.int32)
+    pos[[0, 4, 5, 10]] = [T * k, T * k + 4, -1, np.iinfo(np.int32).min]
+    offsets = np.array([0, 2, 4, 6, 8, taken], np.int32)
+    behind = torch.full((2 * T * k, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    y = behind[:T * k]
+    y.copy_(torch.from_numpy(rng.normal(0, 3, (T * k, H)).astype(np.float32)))
+    w = rng.random((T, k)).astype(np.float32)
+    out = Guarded((T, H), torch.int16)
+    fp8q.fp8q_moe_combine(y, dev(w), dev(pos), dev(offsets), out.t)
+    torch.cuda.synchronize()
+    out.check_canary()
+    inside = ((pos >= 0) & (pos < T * k)).reshape(T, k)
+    rows = y.float().cpu().numpy().astype(np.float64)[np.where(inside.reshape(-1), pos, 0)].reshape(T, k, H)
+    terms = rows * np.where(inside, w, 0).astype(np.float64)[:, :, None]
+    ref, err = terms.sum(1), 32 * 2.0 ** -24 * np.abs(terms).sum(1)
+    got = bf16_bits_to_f64(host(out.t))
+    assert np.all((_bf16(ref - err) <= got) & (got <= _bf16(ref + err)))
+
+
 # ----------------------------------------------------------------- expert FFN
 def _ffn_inputs(orc, T, E, k, H, I, seed, holes=False):
     rng = np.random.default_rng(seed)

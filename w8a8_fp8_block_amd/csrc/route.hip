@@ -353,18 +353,19 @@ __global__ __launch_bounds__(kThreads) void place_kernel(const int32_t* ids, int
 }
 
 // out[t] = bf16( sum over j, in order, of weights[t][j] * y[pos[t][j]] ); slots
-// without an expert add nothing.  Eight columns per thread, summed in fp32.  Bound
+// without an expert, or past the R rows of y whatever the plan holds, add
+// nothing.  Eight columns per thread, summed in fp32.  Bound
 // by reading y: T = 4576, top 4, H = 5120: 38 us, 6.2 TB/s read and written.
 __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict__ y,
                                                       const float* __restrict__ weights,
                                                       const int32_t* __restrict__ pos,
                                                       const int32_t* __restrict__ offsets,
-                                                      uint16_t* __restrict__ out, uint32_t E,
+                                                      uint16_t* __restrict__ out, uint32_t R, uint32_t E,
                                                       uint32_t k, uint32_t H, uint32_t blocks_h) {
   const uint32_t t = blockIdx.x / blocks_h;
   const uint32_t h = (blockIdx.x % blocks_h) * 2048 + threadIdx.x * 8;
   if (h >= H) return;
-  const uint32_t taken = (uint32_t)offsets[E];
+  const uint32_t taken = min((uint32_t)offsets[E], R);
   float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (uint32_t j = 0; j < k; ++j) {
     const uint32_t p = (uint32_t)pos[(uint64_t)t * k + j];
@@ -460,7 +461,8 @@ hipError_t launch_combine(const uint16_t* y, const float* weights, const int32_t
                           const int32_t* offsets, uint16_t* out, uint32_t T, uint32_t E,
                           uint32_t top_k, uint32_t H, hipStream_t s) {
   const uint32_t blocks_h = (H + 2047) / 2048;
-  combine_kernel<<<dim3(T * blocks_h), dim3(256), 0, s>>>(y, weights, pos, offsets, out, E, top_k, H, blocks_h);
+  combine_kernel<<<dim3(T * blocks_h), dim3(256), 0, s>>>(y, weights, pos, offsets, out, T * top_k, E,
+                                                            top_k, H, blocks_h);
   return hipGetLastError();
 }
 
