@@ -687,7 +687,8 @@ size_t fp8q_moe_ffn_workspace_bytes(uint32_t T, uint32_t E, uint32_t top_k,
  *   a = adapter_ids[m]; rows whose id lies outside 0..adapters-1 are the
  *   projection alone
  * with x in bf16 for the adapter, the sums in fp32 (x . A^T is kept in fp32 and
- * enters the second product as two bf16 terms, about 16 bits), one rounding.
+ * enters the second product scaled, as two bf16 terms, about 16 bits; beyond fp32's
+ * range it is an infinity), one rounding.
  *   lora_a       [adapters,rank,K] bf16, lora_b [adapters,N,rank] bf16,
  *                lora_scale [adapters] fp32, adapter_ids [M] int32, read only;
  *                an adapter of smaller rank is padded with zeros

@@ -151,6 +151,54 @@ def test_adapters_do_not_reach_other_rows(orc, M, N, K, where):
         assert not np.array_equal(host(out), clean)
 
 
+@pytest.mark.parametrize("M,N,K", [(3, 256, 384), (16, 5120, 512), (40, 512, 640), (100, 1024, 8192), (200, 384, 512),
+                                   (1024, 5120, 384)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scaled_v_at_the_end_of_the_range(orc, M, N, K, sign):
+    """scale * (x . A^T) of 6e38 is an infinity, and so is the output, with the sign of
+    B; of 3.4e38, which bf16 rounds to an infinity, it is a number like others
+    (B there 2^-120 .. 2^-122: the adapter adds up to 256)."""
+    log(f"lora M={M} N={N} K={K} scaled v at the end of the range, sign {sign}")
+    rng = np.random.default_rng(M + K)
+    x = rng.normal(0, 1, (M, K)).astype(np.float32)
+    x[:, 0] = 2.0
+    x = synth.f32_to_bf16_bits(x)
+    wq, ws = orc.quant_weight_block(rng.normal(0, 0.02, (N, K)).astype(np.float32))
+    n, R = 3, 16
+    A = np.zeros((n, R, K), np.float32)
+    A[:, 5, 0] = 1.0  # v = 2 at rank 5, 0 elsewhere
+    B = rng.choice([-1, 1], (n, N, R)) * 2.0 ** rng.integers(-2, 1, (n, N, R))
+    B[2] *= 2.0 ** -120
+    A, B = synth.f32_to_bf16_bits(A), synth.f32_to_bf16_bits(B.astype(np.float32))
+    s = np.array([1.0, sign * 3e38, sign * 1.7e38], np.float32)
+    ids = (np.arange(M) % 4 - 1).astype(np.int32)
+    out = Guarded((M, N), torch.int16)
+    work = torch.empty(fp8q.fp8q_proj_lora_workspace_bytes(M, N, K, R), dtype=torch.uint8, device="cuda")
+    fp8q.fp8q_proj_lora(dev(x), dev(wq), dev(ws), dev(A), dev(B), dev(s), dev(ids), out.t,
+                        *fp8q.alloc_proj_scratch(M, K), work)
+    torch.cuda.synchronize()
+    out.check_canary()
+    got, b = bf16_bits_to_f64(host(out.t)), bf16_bits_to_f64(B)[:, :, 5]
+    ref = orc.gemm_ref(*orc.quant_act(x), wq, ws)
+    ref += np.where((ids >= 0)[:, None], 2.0 * s.astype(np.float64)[ids][:, None] * b[ids], 0)
+    over = ids == 1
+    assert np.array_equal(got[over], sign * np.sign(b[1]) * np.full((over.sum(), N), np.inf))
+    assert_tol(got[~over], ref[~over], "lora at the end of the range")
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 256, 384), (200, 384, 512)])
+@pytest.mark.parametrize("bits", [0x7FC00000, 0x7FFFFFFF, 0xFFFFFFFF])
+def test_nan_scale_of_any_payload(orc, M, N, K, bits):
+    """A NaN stays one in its rows, whatever its payload."""
+    log(f"lora M={M} scale {bits:#x}")
+    args, _ = _run(orc, M, N, K, 3, 16, "each", M)
+    args[5].copy_(torch.from_numpy(np.array([1, 1, bits], np.uint32).view(np.float32)))
+    fp8q.fp8q_proj_lora(*args)
+    torch.cuda.synchronize()
+    nan = np.isnan(bf16_bits_to_f64(host(args[7])))
+    assert np.array_equal(nan, np.repeat((host(args[6]) == 2)[:, None], N, 1))
+
+
 @pytest.mark.parametrize("M,N", [(1024, 5120), (1100, 4096)])
 @pytest.mark.parametrize("kind", ["each", "runs"])
 def test_prompts(orc, M, N, kind):

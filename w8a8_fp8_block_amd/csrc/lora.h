@@ -31,17 +31,22 @@ __device__ __forceinline__ v4f mfma_bf16_32(const u32x4& w, const u32x4& x, cons
                                                  0, 0);
 }
 
-// v * s as the sum of two bf16 numbers (its rounding and the rest), four at a time
+// v * s as the sum of two bf16 numbers (its rounding and the rest), four at a time.
+// The first is held to bf16's range: what lies beyond, up to an infinity or a NaN,
+// is the rest's (an infinity's own rest would be inf - inf).
 __device__ __forceinline__ void split_bf16(const v4f& v, float s, uint2& hi, uint2& lo) {
-  uint32_t h[4], r[4];
+#pragma clang fp contract(off)  // one f for both terms
+  typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
+  constexpr float kMost = 0x1.FEp127f;  // bf16's largest
+  v4f f, c;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float f = v[i] * s;
-    h[i] = bf16_rne(f);
-    r[i] = bf16_rne(f - __uint_as_float(h[i] << 16));
+    f[i] = v[i] * s;
+    c[i] = __builtin_amdgcn_fmed3f(f[i], -kMost, kMost);
   }
-  hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  lo = make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
+  const v4bf h = __builtin_convertvector(c, v4bf);
+  hi = __builtin_bit_cast(uint2, h);
+  lo = __builtin_bit_cast(uint2, __builtin_convertvector(f - __builtin_convertvector(h, v4f), v4bf));
 }
 
 // out[m, n] += scale[a] * sum_r v[m, r] * B[a][n, r] for the rows m of adapter
