@@ -196,3 +196,82 @@ assert fp8q.fp8q_moe_ffn_workspace_bytes(0, 8, 2, 512, 512) == 0
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     assert subprocess.run([sys.executable, "-c", code], cwd=root).returncode == 0
+
+
+@pytest.fixture
+def no_device(monkeypatch):
+    """The binding with any tensor's pointer taken and no call made: its checks alone."""
+    class Accepts:
+        def __getattr__(self, name):
+            return lambda *args: 0
+    monkeypatch.setattr(fp8q, "_ptr", lambda t: 0x1000)
+    monkeypatch.setattr(fp8q, "_stream", lambda stream=None: 0)
+    monkeypatch.setattr(fp8q, "lib", Accepts)
+
+
+def _each_refused(call, good, bad):
+    """The good arguments pass; with each bad one in turn the error names it."""
+    call(**good)
+    for name, t, error, what in bad:
+        with pytest.raises(error, match=what):
+            call(**{**good, name: t})
+
+
+def _fp8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
+def _bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def _i32(n):
+    return torch.zeros(n, dtype=torch.int32)
+
+
+def test_lora_binding_refusals(no_device):
+    M, N, K, n, R = 20, 256, 384, 3, 16
+    good = dict(x=_bf16(M, K), w=_fp8(N, K), w_scale=torch.zeros(2, 3), lora_a=_bf16(n, R, K), lora_b=_bf16(n, N, R),
+                lora_scale=torch.zeros(n), adapter_ids=_i32(M), out=_bf16(M, N), act_q=_fp8(M, K),
+                act_scale=torch.zeros(M, 3), act_scale_km=torch.zeros(3, 32), workspace=None)
+    bad = [(name, good[name].to(dt), TypeError, f"{name} must be") for name, dt in (
+        ("x", torch.float16), ("x", torch.float32), ("w", torch.bfloat16), ("w_scale", torch.float64),
+        ("lora_a", torch.float16), ("lora_a", torch.float32), ("lora_b", torch.float16), ("lora_b", torch.float32),
+        ("lora_scale", torch.bfloat16), ("adapter_ids", torch.int64), ("out", torch.uint8), ("out", torch.float32),
+        ("act_q", torch.float32), ("act_scale", torch.bfloat16), ("act_scale_km", torch.float16))]
+    bad += [("w_scale", torch.zeros(3, 2), ValueError, "w_scale"), ("act_q", _fp8(M - 1, K), ValueError, "act_q has"),
+            ("act_scale", torch.zeros(M - 1, 3), ValueError, "act_scale has"),
+            ("act_scale_km", torch.zeros(3, 16), ValueError, "act_scale_km has"),
+            ("adapter_ids", _i32(M + 1), ValueError, "adapter_ids has"), ("out", _bf16(M, N + 1), ValueError, "disagree"),
+            ("lora_scale", torch.zeros(n - 1), ValueError, "lora_scale has"), ("x", None, AttributeError, "shape")]
+    _each_refused(fp8q.fp8q_proj_lora, good, bad)
+    # scratch of a larger batch serves a smaller one
+    larger = dict(act_q=_fp8(M + 9, K), act_scale=torch.zeros(M + 9, 3), act_scale_km=torch.zeros(3, 48))
+    _each_refused(fp8q.fp8q_proj_lora, {**good, **larger}, [])
+
+
+def test_expert_binding_refusals(no_device):
+    T, E, k, H, I = 20, 4, 2, 256, 128
+    R = T * k
+    combine = dict(y=_bf16(R, H), weights=torch.zeros(T, k), pos=_i32(R), offsets=_i32(E + 1), out=_bf16(T, H))
+    _each_refused(fp8q.fp8q_moe_combine, combine, [
+        ("y", torch.zeros(R, H), TypeError, "y must be"), ("out", _fp8(T, H), TypeError, "out must be"),
+        ("y", _bf16(R, H).half(), TypeError, "y must be"), ("pos", _i32(R - 1), ValueError, "pos has"),
+        ("weights", _bf16(T, k), TypeError, "weights must be")])
+    grouped = dict(a=_fp8(T, H), a_scale_km=torch.zeros(2, 32), w=_fp8(E, I, H), w_scale=torch.zeros(E, 1, 2),
+                   offsets=_i32(E + 1), out=_bf16(R, I), order=_i32(R), top_k=k)
+    _each_refused(fp8q.fp8q_gemm_grouped, grouped, [
+        ("out", _fp8(R, I), TypeError, "out must be"), ("out", torch.zeros(R, I), TypeError, "out must be"),
+        ("a", _bf16(T, H), TypeError, "a must be"), ("w", _bf16(E, I, H), TypeError, "w must be"),
+        ("w_scale", _bf16(E, 1, 2), TypeError, "w_scale must be"), ("a_scale_km", torch.zeros(2, 16), ValueError, "scale"),
+        ("a_scale_km", _bf16(2, 32), TypeError, "a_scale_km must be"), ("offsets", _i32(E), ValueError, "offsets has")])
+    ffn = dict(x=_bf16(T, H), weights=torch.zeros(T, k), order=_i32(R), pos=_i32(R), offsets=_i32(E + 1),
+               w_gate=_fp8(E, I, H), w_gate_scale=torch.zeros(E, 1, 2), w_up=_fp8(E, I, H),
+               w_up_scale=torch.zeros(E, 1, 2), w_down=_fp8(E, H, I), w_down_scale=torch.zeros(E, 2, 1),
+               out=_bf16(T, H), workspace=None)
+    _each_refused(fp8q.fp8q_moe_ffn, ffn, [
+        ("x", torch.zeros(T, H), TypeError, "x must be"), ("x", _bf16(T, H).half(), TypeError, "x must be"),
+        ("out", _fp8(T, H), TypeError, "out must be"), ("w_gate", _bf16(E, I, H), TypeError, "w_gate must be"),
+        ("w_up", _bf16(E, I, H), TypeError, "w_up must be"), ("w_down", _bf16(E, H, I), TypeError, "w_down must be"),
+        ("w_up_scale", _bf16(E, 1, 2), TypeError, "w_up_scale must be"), ("order", _i32(R + 1), ValueError, "order has"),
+        ("weights", _bf16(T, k), TypeError, "weights must be")])

@@ -412,6 +412,28 @@ def _of(t, dtype, n, what) -> int:
     return _ptr(t)
 
 
+_BF16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+_E4M3 = frozenset((torch.uint8, torch.float8_e4m3fn))
+_F32 = frozenset((torch.float32,))
+
+
+def _wrong_type(**tensors):
+    """Raises for the first of what=(tensor, its dtypes) of another type.  (The callers
+    test the types first, in one expression: a call's host time counts at decode.)"""
+    for what, (t, dtypes) in tensors.items():
+        if t.dtype not in dtypes:
+            raise TypeError(f"{what} must be {' or '.join(sorted(map(str, dtypes)))}, got {t.dtype}")
+
+
+def _scratch(t, dtypes, n, what) -> int:
+    """Pointer of a scratch tensor of n elements or more."""
+    if t.dtype not in dtypes:
+        _wrong_type(**{what: (t, dtypes)})
+    if t.numel() < n:
+        raise ValueError(f"{what} has {t.numel()} elements, {n} needed")
+    return _ptr(t)
+
+
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
@@ -465,6 +487,8 @@ def fp8q_moe_combine(y, weights, pos, offsets, out, stream=None):
     if R != T * k or _dims(out, 2) != (T, H):
         raise ValueError("y, weights and out disagree in shape")
     E = offsets.numel() - 1
+    if not (y.dtype in _BF16 and out.dtype in _BF16):
+        _wrong_type(y=(y, _BF16), out=(out, _BF16))
     _check(lib().fp8q_moe_combine(_ptr(y), _of(weights, torch.float32, R, "weights"),
                                  _of(pos, torch.int32, R, "pos"), _of(offsets, torch.int32, E + 1, "offsets"),
                                  _ptr(out), T, E, k, H, _stream(stream)))
@@ -487,8 +511,11 @@ def fp8q_gemm_grouped(a, a_scale_km, w, w_scale, offsets, out, order=None, top_k
     R, N2 = _dims(out, 2)
     if K2 != K or N2 != N:
         raise ValueError("a, w and out disagree in shape")
-    if _dims(w_scale, 3) != (E, N // 128, K // 128) or _dims(a_scale_km, 2) != (K // 128, (rows + 15) // 16 * 16):
+    if w_scale.shape != (E, N // 128, K // 128) or a_scale_km.shape != (K // 128, (rows + 15) // 16 * 16):
         raise ValueError("a scale tensor's shape does not match")
+    if not (a.dtype in _E4M3 and a_scale_km.dtype in _F32 and w.dtype in _E4M3 and w_scale.dtype in _F32
+            and out.dtype in _BF16):
+        _wrong_type(a=(a, _E4M3), a_scale_km=(a_scale_km, _F32), w=(w, _E4M3), w_scale=(w_scale, _F32), out=(out, _BF16))
     _check(lib().fp8q_gemm_grouped(_ptr(a), _ptr(a_scale_km), _ptr(w), _ptr(w_scale),
                                   _of(offsets, torch.int32, E + 1, "offsets"),
                                   0 if order is None else _of(order, torch.int32, R, "order"), _ptr(out), rows,
@@ -516,14 +543,21 @@ def fp8q_moe_ffn(x, weights, order, pos, offsets, w_gate, w_gate_scale, w_up, w_
     E, I, H2 = _dims(w_gate, 3)
     if T2 != T or H2 != H or _dims(w_up, 3) != (E, I, H) or _dims(w_down, 3) != (E, H, I) or _dims(out, 2) != (T, H):
         raise ValueError("x, the weights and out disagree in shape")
-    if not (_dims(w_gate_scale, 3) == _dims(w_up_scale, 3) == (E, I // 128, H // 128)
-            and _dims(w_down_scale, 3) == (E, H // 128, I // 128)):
+    if not (w_gate_scale.shape == w_up_scale.shape == (E, I // 128, H // 128)
+            and w_down_scale.shape == (E, H // 128, I // 128)):
         raise ValueError("a scale tensor's shape does not match")
+    if not (x.dtype in _BF16 and out.dtype in _BF16 and w_gate.dtype in _E4M3 and w_up.dtype in _E4M3
+            and w_down.dtype in _E4M3 and w_gate_scale.dtype in _F32 and w_up_scale.dtype in _F32
+            and w_down_scale.dtype in _F32):
+        _wrong_type(x=(x, _BF16), w_gate=(w_gate, _E4M3), w_gate_scale=(w_gate_scale, _F32), w_up=(w_up, _E4M3),
+                    w_up_scale=(w_up_scale, _F32), w_down=(w_down, _E4M3), w_down_scale=(w_down_scale, _F32),
+                    out=(out, _BF16))
     R, i32 = T * k, torch.int32
     _check(lib().fp8q_moe_ffn(_ptr(x), _of(weights, torch.float32, R, "weights"), _of(order, i32, R, "order"),
-                             _of(pos, i32, R, "pos"), _of(offsets, i32, E + 1, "offsets"), _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up),
-                             _ptr(w_up_scale), _ptr(w_down), _ptr(w_down_scale), _ptr(out), _optr(workspace),
-                             _nbytes(workspace), T, E, k, H, I, variant, _stream(stream)))
+                             _of(pos, i32, R, "pos"), _of(offsets, i32, E + 1, "offsets"), _ptr(w_gate),
+                             _ptr(w_gate_scale), _ptr(w_up), _ptr(w_up_scale), _ptr(w_down), _ptr(w_down_scale),
+                             _ptr(out), _optr(workspace), _nbytes(workspace), T, E, k, H, I, variant,
+                             _stream(stream)))
 
 
 def fp8q_proj_lora_workspace_bytes(M: int, N: int, K: int, rank: int) -> int:
@@ -535,18 +569,27 @@ def fp8q_proj_lora(x, w, w_scale, lora_a, lora_b, lora_scale, adapter_ids, out, 
     """fp8q_proj plus each row's low-rank adapter: out[m] = proj(x)[m] +
     lora_scale[a] * (x[m] . lora_a[a]^T) . lora_b[a]^T, a = adapter_ids[m]
     (outside 0..n-1: none).  lora_a [n,rank,K], lora_b [n,N,rank] bf16,
-    lora_scale [n] float32, adapter_ids [M] int32; workspace: a device byte
-    tensor of fp8q_proj_lora_workspace_bytes(M, N, K, rank)."""
+    lora_scale [n] float32, adapter_ids [M] int32; act_q, act_scale, act_scale_km:
+    alloc_proj_scratch(M, K), or larger; workspace: a device byte tensor of
+    fp8q_proj_lora_workspace_bytes(M, N, K, rank)."""
     M, K = _dims(x, 2)
     N, K2 = _dims(w, 2)
     n, R, K3 = _dims(lora_a, 3)
     if K2 != K or K3 != K or _dims(lora_b, 3) != (n, N, R) or _dims(out, 2) != (M, N):
         raise ValueError("x, w, the adapters and out disagree in shape")
+    G = K // 128
+    if w_scale.shape != (N // 128, G):
+        raise ValueError("w_scale's shape does not match")
+    if not (x.dtype in _BF16 and w.dtype in _E4M3 and w_scale.dtype in _F32 and lora_a.dtype in _BF16
+            and lora_b.dtype in _BF16 and out.dtype in _BF16):
+        _wrong_type(x=(x, _BF16), w=(w, _E4M3), w_scale=(w_scale, _F32), lora_a=(lora_a, _BF16),
+                    lora_b=(lora_b, _BF16), out=(out, _BF16))
     _check(lib().fp8q_proj_lora(_ptr(x), _ptr(w), _ptr(w_scale), _ptr(lora_a), _ptr(lora_b),
                                _of(lora_scale, torch.float32, n, "lora_scale"),
-                               _of(adapter_ids, torch.int32, M, "adapter_ids"), _ptr(out), _ptr(act_q), _ptr(act_scale),
-                               _ptr(act_scale_km), _optr(workspace), _nbytes(workspace), M, N, K, n, R,
-                               _stream(stream)))
+                               _of(adapter_ids, torch.int32, M, "adapter_ids"), _ptr(out),
+                               _scratch(act_q, _E4M3, M * K, "act_q"), _scratch(act_scale, _F32, M * G, "act_scale"),
+                               _scratch(act_scale_km, _F32, G * ((M + 15) // 16 * 16), "act_scale_km"),
+                               _optr(workspace), _nbytes(workspace), M, N, K, n, R, _stream(stream)))
 
 
 def fp8q_default_select_params(cu_count: int) -> SelectParams:
