@@ -329,6 +329,23 @@ def test_combine_keeps_to_the_rows(taken):
     assert np.all((_bf16(ref - err) <= got) & (got <= _bf16(ref + err)))
 
 
+def test_combine_of_many_tokens():
+    """More tokens than one dimension of a launch has workgroups for (2^24 of 256
+    threads): weights are powers of two, so the results are exact."""
+    log("combine of 2^24 + 5 tokens")
+    T, H = (1 << 24) + 5, 8
+    g = torch.Generator("cuda").manual_seed(1)
+    y = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w = torch.tensor([0.5, 2.0, 1.0], device="cuda")[torch.arange(T, device="cuda") % 3].view(T, 1)
+    pos = torch.arange(T - 1, -1, -1, dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    out = Guarded((T, H), torch.int16)
+    fp8q.fp8q_moe_combine(y, w, pos, offsets, out.t)
+    torch.cuda.synchronize()
+    assert torch.equal(out.t.view(torch.bfloat16), (y.flip(0).float() * w).bfloat16())
+    out.check_canary()
+
+
 # ----------------------------------------------------------------- expert FFN
 def _ffn_inputs(orc, T, E, k, H, I, seed, holes=False):
     rng = np.random.default_rng(seed)

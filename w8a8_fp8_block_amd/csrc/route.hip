@@ -362,9 +362,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
                                                       const int32_t* __restrict__ offsets,
                                                       uint16_t* __restrict__ out, uint32_t R, uint32_t E,
                                                       uint32_t k, uint32_t H, uint32_t blocks_h) {
-  const uint32_t t = blockIdx.x / blocks_h;
+  const uint32_t t = blockIdx.y * (gridDim.x / blocks_h) + blockIdx.x / blocks_h;
   const uint32_t h = (blockIdx.x % blocks_h) * 2048 + threadIdx.x * 8;
-  if (h >= H) return;
+  if (t >= R / k || h >= H) return;
   const uint32_t taken = min((uint32_t)offsets[E], R);
   float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   for (uint32_t j = 0; j < k; ++j) {
@@ -460,9 +460,12 @@ hipError_t launch_group_rows(const int32_t* ids, int32_t* order, int32_t* pos, i
 hipError_t launch_combine(const uint16_t* y, const float* weights, const int32_t* pos,
                           const int32_t* offsets, uint16_t* out, uint32_t T, uint32_t E,
                           uint32_t top_k, uint32_t H, hipStream_t s) {
-  const uint32_t blocks_h = (H + 2047) / 2048;
-  combine_kernel<<<dim3(T * blocks_h), dim3(256), 0, s>>>(y, weights, pos, offsets, out, T * top_k, E,
-                                                            top_k, H, blocks_h);
+  // a launch holds fewer than 2^32 threads a dimension: 2^23 workgroups here, the
+  // tokens beyond in y (T * blocks_h < 2^30)
+  const uint32_t blocks_h = (uint32_t)(((uint64_t)H + 2047) / 2048);
+  const uint32_t tokens = std::min(T, (1u << 23) / blocks_h);
+  combine_kernel<<<dim3(tokens * blocks_h, (T + tokens - 1) / tokens), dim3(256), 0, s>>>(
+      y, weights, pos, offsets, out, T * top_k, E, top_k, H, blocks_h);
   return hipGetLastError();
 }
 
