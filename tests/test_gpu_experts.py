@@ -442,6 +442,93 @@ def test_ffn_is_its_parts(orc):
     assert np.linalg.norm(got - want) <= 1e-3 * np.linalg.norm(want)
 
 
+# (T, E, k, H, I) by the streaming instance that gate and up (f16 products), and the
+# down product (FP8), take on 256 CUs: rows a tile, columns x K blocks of a stage
+STREAMED = [(2, 8, 3, 512, 384),       # 16 rows, 32 x 4 both
+            (16, 24, 4, 1024, 640),    # 16 rows, 64 x 2 both
+            (20, 8, 2, 512, 512),      # 32 rows, 32 x 4 both
+            (30, 8, 2, 2048, 1024),    # 32 rows, 64 x 2 both
+            (64, 64, 6, 640, 256)]     # 32 rows, 128 x 1 both
+
+
+@pytest.mark.parametrize("T,E,k,H,I", STREAMED)
+@pytest.mark.parametrize("holes", [False, True])
+def test_streamed_ffn_against_the_definition(orc, T, E, k, H, I, holes):
+    """Every streaming instance.  Gate and up come from f16 products, off by 1e-7 of
+    their RMS at most, so that hardly one in 10^4 rounds to another bf16 value or code:
+    what is left are the bf16 roundings of each expert's output and of the sum, each
+    2^-7 / sqrt(12) of the value's power of two, up to 1.7e-3 of the norm, 2.4e-3
+    together; bound 3e-3 for the scatter of few elements."""
+    log(f"streamed moe_ffn T={T} E={E} k={k} H={H} I={I} holes={holes}")
+    assert fp8q.fp8q_gemm_grouped_select(T * k, E, 2 * I) == 1 and fp8q.fp8q_gemm_grouped_select(T * k, E, H) == 1
+    x, ids, w, order, pos, offsets, wg, wu, wd = _ffn_inputs(orc, T, E, k, H, I, 3 * T + E, holes)
+    ref = _ffn_ref(orc, x, ids, w, wg, wu, wd)
+    got = _ffn_gpu(x, w, order, pos, offsets, wg, wu, wd, 2)
+    rel = np.linalg.norm(got - ref) / max(np.linalg.norm(ref), 1e-30)
+    log(f"  relative error {rel:.2e}")
+    assert rel <= 3e-3
+    assert not got[(ids < 0).all(1)].any()
+
+
+@pytest.mark.parametrize("sizes,N", [([1, 0, 4, 2], 1024), ([3, 1, 0, 4] * 4, 2048),           # 16-row tiles
+                                     ([33, 0, 9, 17], 1024), ([40, 3, 0, 16, 17, 5, 32, 1], 2048),
+                                     ([20, 1, 0, 33] * 4, 2048)])                              # 32-row tiles
+@pytest.mark.parametrize("K", [640, 1408])
+def test_streamed_products(orc, sizes, N, K):
+    """Every streaming instance of the FP8 product, K blocks that do not fill the last stage."""
+    a, a_s, wq, ws, order, offsets, ref = _grouped_case(orc, sizes, N, K, 1, True, 0, N + K)
+    log(f"streamed product E={len(sizes)} R={len(order)} N={N} K={K}")
+    out = Guarded((len(order), N), torch.int16)
+    fp8q.fp8q_gemm_grouped(dev(a), dev(orc.scale_to_kmajor(a_s)), dev(wq), dev(ws), dev(offsets), out.t,
+                           order=dev(order), kernel=1)
+    torch.cuda.synchronize()
+    out.check_canary()
+    assert_tol(bf16_bits_to_f64(host(out.t)), ref, f"streamed product E {len(sizes)} N {N} K {K}")
+
+
+def _ffn_by_parts(x, w, order, pos, offsets, wg, wu, wd):
+    """The public steps: quantizer, gate and up on 128 x 128 tiles, intermediate, down
+    product on the automatic kernel, weighted sum."""
+    (T, H), k, (E, I, _) = x.shape, w.shape[1], wg[0].shape
+    R = T * k
+    xq, xs = Guarded((T, H), torch.uint8), Guarded((H // 128, synth.ceil16(T)), torch.float32)
+    fp8q.fp8q_quant_act_kmajor(dev(x), xq.t, None, xs.t)
+    g, u, y = (Guarded((R, n), torch.int16) for n in (I, I, H))
+    for wt, o in ((wg, g), (wu, u)):
+        fp8q.fp8q_gemm_grouped(xq.t, xs.t, dev(wt[0]), dev(wt[1]), dev(offsets), o.t, order=dev(order), top_k=k, kernel=2)
+    hq, hs = Guarded((R, I), torch.uint8), Guarded((I // 128, synth.ceil16(R)), torch.float32)
+    fp8q.fp8q_silu_mul_quant(g.t, u.t, hq.t, hs.t)
+    fp8q.fp8q_gemm_grouped(hq.t, hs.t, dev(wd[0]), dev(wd[1]), dev(offsets), y.t)
+    out = Guarded((T, H), torch.int16)
+    fp8q.fp8q_moe_combine(y.t, dev(w), dev(pos), dev(offsets), out.t)
+    torch.cuda.synchronize()
+    return host(out.t)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(120, 4, 2, 512, 256),    # persistent fused gate/up
+                                       (500, 3, 2, 640, 4096),   # the same, several tiles a workgroup
+                                       (300, 4, 2, 256, 384),    # H < 512: a workgroup a tile
+                                       (700, 3, 2, 384, 256), (257, 2, 1, 128, 640),
+                                       (600, 300, 2, 512, 256),  # more experts than the tables
+                                       (90, 300, 4, 256, 128)])
+@pytest.mark.parametrize("holes", [False, True])
+def test_fused_ffn_has_the_bits_of_its_parts(orc, T, E, k, H, I, holes):
+    """Both fused gate/up kernels, and the separate form on 128 x 128 tiles, give the
+    output of the public steps bit for bit; against the 64-bit definition as in
+    test_ffn_against_the_definition."""
+    log(f"fused moe_ffn T={T} E={E} k={k} H={H} I={I} holes={holes}")
+    x, ids, w, order, pos, offsets, wg, wu, wd = _ffn_inputs(orc, T, E, k, H, I, 7 * T + E, holes)
+    want = bf16_bits_to_f64(_ffn_by_parts(x, w, order, pos, offsets, wg, wu, wd))
+    variants = (1, 2) if fp8q.fp8q_gemm_grouped_select(T * k, E, 2 * I) != 1 else (1,)
+    for variant in variants:
+        got = _ffn_gpu(x, w, order, pos, offsets, wg, wu, wd, variant)
+        assert np.array_equal(got, want), f"variant {variant}"
+    ref = _ffn_ref(orc, x, ids, w, wg, wu, wd)
+    rel = np.linalg.norm(want - ref) / np.linalg.norm(ref)
+    log(f"  relative error {rel:.2e}, variants {variants}")
+    assert rel <= 8e-3
+
+
 # ------------------------------------------------------- streams and capture
 def test_side_stream_and_graph(orc):
     """The whole path on a stream of its own, then captured once and replayed with
