@@ -659,11 +659,12 @@ int fp8q_gemm_grouped_select(uint32_t R, uint32_t E, uint32_t N);
  *   variant  0 automatic, 1 fused gate/up kernel, 2 separate gate and up;
  *            0 takes 1 from a mean of 16 rows an expert where its tiles fill the
  *            device twice (fp8q_moe_ffn_select, on the current device)
- * The FP8 matrix instruction sums a 128-deep block to about 16 bits, which can
- * move gate and up across a bf16 rounding and h across a code's: against 64-bit
- * sums the output is off by about 3e-3 of its norm (2.4e-3 where the weights are
- * streamed, a few rows an expert: those products run in f16), the rounding of
- * the formats themselves included (1.7e-3).
+ * Accuracy, against 64-bit sums of the same quantized x: y and out are rounded to
+ * bf16, 1.7e-3 of the norm each, 2.4e-3 together, and that is all where the weights
+ * are streamed (a few rows an expert: gate and up run in f16 there).  Elsewhere the
+ * FP8 matrix instruction sums a 128-deep block to about 16 bits, which can move gate
+ * and up across a bf16 rounding and h across a code's: 2.2e-3 to 4.9e-3 at the sizes
+ * tested, as in fp8q_ffn.  The form, and so the error, goes by the size of the batch.
  * H % 128 == 0, I % 128 == 0.  x is quantized once a token.  Limits, and plans that
  * are not groupings, as for fp8q_gemm_grouped (with R = T*top_k rows of H and of I). */
 fp8q_status fp8q_moe_ffn(const uint16_t *x_bf16, const float *weights,

@@ -578,6 +578,11 @@ int moe_ffn_auto(uint32_t T, uint32_t E, uint32_t top_k, uint32_t I, uint32_t cu
 }
 
 // Workspace of fp8q_moe_ffn: regions in this order, each on a 256-byte boundary.
+// y, the experts' outputs, is bf16, as a projection's output is everywhere in this
+// library, so that the chain has the bits of its public steps.  That rounding is
+// 1.7e-3 of the output's norm, as much as the final one's.  fp32 rows would spare it
+// for 2 more bytes written and read a number: 375 MB at R = 18304, H = 5120, about 70
+// of that call's 770 us.
 struct MoeWorkspace {
   uint64_t xq, xs, hq, hs, g, u, y, total;
 };

@@ -26,7 +26,7 @@ namespace {
 //
 // Bound by the matrix pipe at many rows: 36608 rows of 64 experts, N = 2048, K =
 // 5120: 465 us, 1.65 PFLOP/s (1.83 with the partial tiles' rows), the pipe busy
-// 43.6% of the cycles at the clock the power limit allows (the dense kernel,
+// 43.8% of the cycles at the clock the power limit allows (the dense kernel,
 // without partial tiles: 1.9-2.1, 55%); a workgroup a tile of 256 rows took 506 us
 // there and 310 us for the FFN's down product (18304 rows, 32 experts, N = 5120, K =
 // 2048), this kernel 260.  The fused gate/up projection of those rows (H = 5120, I =

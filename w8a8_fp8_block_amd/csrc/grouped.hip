@@ -118,7 +118,7 @@ __device__ __forceinline__ v8h codes_f16(const v8i& c, int s) {
 // Where the result is rounded to bf16 and quantized again, as gate and up are,
 // that moves values across rounding boundaries: 16 tokens of 64 experts, H = 5120, I
 // = 1408, gave an expert FFN 3.7e-3 of its norm from the 64-bit value, against
-// 2.4e-3 with f16 (the formats' roundings alone: 1.7e-3).  The conversions and the
+// 2.4e-3 with f16, the bf16 roundings of the experts' outputs and of their sum.  The conversions and the
 // slower MFMA hide under the weight stream.
 template <int TM, int TN, int CW, int KS, bool F16>
 __global__ __launch_bounds__(64 * CW * KS) void group_stream_kernel(const uint8_t* __restrict__ A,
@@ -480,7 +480,10 @@ hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw,
   // mostly one row tile an expert: its weights are read once
   const bool once = g.R < (uint64_t)kReadOnceRows * g.E;
   switch (kernel) {
-    case kGroupStream:  // (two sets: gate and up)
+    // two sets: gate and up, in f16.  One product's result is only rounded to bf16
+    // (2^-9), which hides the FP8 sums' 1.4e-5: 3.7e-4 of its norm from that rounding
+    // of the 64-bit value.
+    case kGroupStream:
       return sets == 2 ? launch_stream_any<true>(a, as, gw, sets, g, N, K, cus, s)
                        : launch_stream_any<false>(a, as, gw, sets, g, N, K, cus, s);
     case kGroupPp:

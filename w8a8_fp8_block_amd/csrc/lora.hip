@@ -30,9 +30,10 @@ namespace {
 // a workgroup's first read its rows again, from L2.  Bound by reading A (decode:
 // a few rows an adapter) or x (prompts): 25 rows of 22 adapters, rank 64, K = 5120:
 // 7.7 us for 14 MB of A, a launch and two latencies; M = 1168, rank 24: 16 us; M =
-// 4576, K = 17408, rank 32: 97 us for 240 MB of x and codes, 2.5 TB/s.  There 70 us remain
-// without the quantization and 75 without A: the reads of 32 rows 34 KB apart; more
-// workgroups a CU (registers spill) and 64 rows a workgroup were slower.
+// 4576, K = 17408, rank 32: 95 us for 240 MB of x and codes, 2.5 TB/s.  There 70 us remain
+// without the quantization, 72 without A, and 56 with neither (2.8 TB/s: the reads of
+// 32 rows 34 KB apart); more workgroups a CU (registers spill) and 64 rows a workgroup
+// were slower.
 // ------------------------------------------------------------------------
 struct QuantOut {
   uint8_t* q;    // [M,K]
