@@ -546,9 +546,6 @@ fp8q_status check_grouped(const char* fn, uint32_t a_rows, uint32_t R, uint32_t 
   st = check_n(fn, R, N, K);
   if (st != FP8Q_OK) return st;
   if ((uint64_t)m_pad16(a_rows) * K > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: ceil16(rows)*K exceeds 2^32-1", fn);
-  // the largest grid: one row tile of 16 a row at most, one column tile of 16
-  if ((uint64_t)R * (N / 16) > 0x7FFFFFFFull)
-    return fail(FP8Q_ERR_SHAPE, "%s: %u rows of %u columns are too many tiles", fn, R, N);
   return FP8Q_OK;
 }
 

@@ -3,9 +3,9 @@
 //   r = order[p] / per_row (or p), e: offsets[e] <= p < offsets[e + 1],
 // with P the 128-deep e4m3 dot products of the dense GEMM (gemm.hip).
 #include <algorithm>
-#include <atomic>
 
 #include "group_pp.h"
+#include "launch.h"
 
 namespace fp8q {
 namespace {
@@ -332,21 +332,11 @@ __global__ __launch_bounds__(64 * CW * KS) void group_stream_kernel(const uint8_
   wait_vmcnt<0>();  // no direct load may still be writing LDS at exit
 }
 
-template <class F>
-hipError_t allow_lds(std::atomic<bool>& done, F* kernel, int bytes) {
-  if (done.load(std::memory_order_acquire)) return hipSuccess;  // idempotent: racing threads repeat it
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == hipSuccess) done.store(true, std::memory_order_release);
-  return e;
-}
-
 template <int TM, int TN, int CW, int KS, bool F16>
 hipError_t launch_stream(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                          const Groups& g, uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
   using C = StreamCfg<TM, TN, CW, KS>;
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_stream_kernel<TM, TN, CW, KS, F16>, C::LDS);
+  const hipError_t e = allow_lds<&group_stream_kernel<TM, TN, CW, KS, F16>, C::LDS>();
   if (e != hipSuccess) return e;
   const uint64_t units = (uint64_t)max_row_tiles(g.R, g.E, 16 * TM) * sets * (N / (16 * TN));
   const uint32_t grid = (uint32_t)(units < cus ? units : cus);
@@ -397,8 +387,7 @@ template <int WAUX>
 hipError_t launch_group_128(const uint8_t* a, const float* as, const GroupWeights& gw, uint32_t sets,
                             const Groups& g, uint32_t N, uint32_t K, hipStream_t s) {
   using C = TileCfg<128, 128, 2, 2, 2, false>;
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_tiled_kernel<128, 128, 2, 2, 2, WAUX>, C::LDS_BYTES);
+  const hipError_t e = allow_lds<&group_tiled_kernel<128, 128, 2, 2, 2, WAUX>, C::LDS_BYTES>();
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = N / 128;
   group_tiled_kernel<128, 128, 2, 2, 2, WAUX><<<dim3(max_row_tiles(g.R, g.E, 128) * tiles_n, sets), dim3(C::NT),
@@ -409,8 +398,7 @@ hipError_t launch_group_128(const uint8_t* a, const float* as, const GroupWeight
 template <int WAUX>
 hipError_t launch_group_persist(const uint8_t* a, const float* as, const GroupWeights& gw, const Groups& g,
                                 uint32_t N, uint32_t K, uint32_t cus, hipStream_t s) {
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_persist_kernel<WAUX>, PersistCfg::LDS);
+  const hipError_t e = allow_lds<&group_persist_kernel<WAUX>, PersistCfg::LDS>();
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = (N + 255) / 256;
   const uint64_t most = (uint64_t)max_row_tiles(g.R, g.E, 128) * tiles_n;
@@ -497,11 +485,6 @@ hipError_t launch_any(const uint8_t* a, const float* as, const GroupWeights& gw,
               : launch_group_128<0>(a, as, gw, sets, g, N, K, s);
 }
 
-Groups make_groups(const int32_t* offsets, const int32_t* order, uint32_t E, uint32_t R,
-                   uint32_t per_row, uint32_t a_rows) {
-  return Groups{offsets, order, E, R, per_row, a_rows};
-}
-
 }  // namespace
 
 int group_gemm_auto(uint32_t R, uint32_t E, uint32_t N, uint32_t cus) { return group_auto(R, E, N, cus); }
@@ -512,7 +495,7 @@ hipError_t launch_gemm_grouped(const uint8_t* a, const float* a_s_km, const uint
                                uint32_t E, uint32_t N, uint32_t K, uint32_t cus, int kernel,
                                hipStream_t s) {
   return launch_any(a, a_s_km, GroupWeights{{w, w}, {w_s, w_s}, {out, out}}, 1,
-                    make_groups(offsets, order, E, R, per_row, a_rows), N, K, cus, kernel, s);
+                    Groups{offsets, order, E, R, per_row, a_rows}, N, K, cus, kernel, s);
 }
 
 hipError_t launch_group_gate_and_up(const uint8_t* x, const float* x_s_km, const uint8_t* w_gate,
@@ -522,15 +505,14 @@ hipError_t launch_group_gate_and_up(const uint8_t* x, const float* x_s_km, const
                                     uint32_t E, uint32_t H, uint32_t I, uint32_t cus, int kernel,
                                     hipStream_t s) {
   return launch_any(x, x_s_km, GroupWeights{{w_gate, w_up}, {ws_gate, ws_up}, {gate, up}}, 2,
-                    make_groups(offsets, order, E, R, per_row, a_rows), I, H, cus, kernel, s);
+                    Groups{offsets, order, E, R, per_row, a_rows}, I, H, cus, kernel, s);
 }
 
 namespace {
 hipError_t launch_gate_up(const uint8_t* x, const float* x_s_km, const GroupWeights& gw, const FfnArgs& f,
                           const Groups& g, uint32_t H, uint32_t I, hipStream_t s) {
   using C = PpCfg<3, false, true>;
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_gate_up_kernel, C::LDS_BYTES);
+  const hipError_t e = allow_lds<&group_gate_up_kernel, C::LDS_BYTES>();
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = I / kGroup;
   group_gate_up_kernel<<<dim3(max_row_tiles(g.R, g.E, C::BM) * tiles_n), dim3(C::NT), C::LDS_BYTES, s>>>(
@@ -541,8 +523,7 @@ hipError_t launch_gate_up(const uint8_t* x, const float* x_s_km, const GroupWeig
 template <int WAUX>
 hipError_t launch_persist_ffn(const uint8_t* x, const float* x_s_km, const GroupWeights& gw, const FfnArgs& f,
                               const Groups& g, uint32_t H, uint32_t I, uint32_t cus, hipStream_t s) {
-  static std::atomic<bool> done{false};
-  const hipError_t e = allow_lds(done, &group_persist_ffn_kernel<WAUX>, PersistCfg::LDS);
+  const hipError_t e = allow_lds<&group_persist_ffn_kernel<WAUX>, PersistCfg::LDS>();
   if (e != hipSuccess) return e;
   const uint32_t tiles_n = I / kGroup;
   const uint64_t most = (uint64_t)max_row_tiles(g.R, g.E, 128) * tiles_n;
@@ -558,7 +539,7 @@ hipError_t launch_group_ffn_gate_up(const uint8_t* x, const float* x_s_km, const
                                     const int32_t* order, uint32_t per_row, uint32_t a_rows, uint32_t R,
                                     uint32_t E, uint32_t H, uint32_t I, uint32_t cus, hipStream_t s) {
   const GroupWeights gw{{w_gate, w_up}, {ws_gate, ws_up}, {nullptr, nullptr}};
-  const Groups g = make_groups(offsets, order, E, R, per_row, a_rows);
+  const Groups g{offsets, order, E, R, per_row, a_rows};
   const FfnArgs f{w_up, ws_up, hq, hs_km, m_pad16(R)};
   if (E > kPersistMaxExperts || H < kPersistMinBlocks * kGroup) return launch_gate_up(x, x_s_km, gw, f, g, H, I, s);
   return R < (uint64_t)kReadOnceRows * E ? launch_persist_ffn<kStreamOnce>(x, x_s_km, gw, f, g, H, I, cus, s)

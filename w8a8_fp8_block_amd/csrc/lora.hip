@@ -7,10 +7,10 @@
 // their fp32 accumulators (lora.h), so that the sum is rounded once and out is
 // written once.
 #include <algorithm>
-#include <atomic>
 
 #include "gemm_pp.h"
 #include "gemm_skinny.h"
+#include "launch.h"
 #include "lora.h"
 
 namespace fp8q {
@@ -268,16 +268,6 @@ __global__ __launch_bounds__(512) void lora_pp_kernel(Gemm g, uint32_t tiles_m, 
   gemm_pp_body<3, false, false>(g.a, g.as, g.w, g.ws, g.out, tmi * 256, tni * 128, g.N, g.K, g.Mp,
                                 FfnArgs{nullptr, nullptr, nullptr, nullptr, 0}, DenseRows{g.M, g.M},
                                 LoraEpilogue{l});
-}
-
-template <auto kernel, int BYTES>
-hipError_t allow_lds() {
-  static std::atomic<bool> done{false};  // idempotent: racing threads repeat it
-  if (done.load(std::memory_order_acquire)) return hipSuccess;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, BYTES);
-  if (e == hipSuccess) done.store(true, std::memory_order_release);
-  return e;
 }
 
 template <int TM, int TN, bool SPLIT>
