@@ -714,6 +714,145 @@ fp8q_status fp8q_proj_lora(const uint16_t *x_bf16, const uint8_t *w_e4m3,
 size_t fp8q_proj_lora_workspace_bytes(uint32_t M, uint32_t N, uint32_t K,
                                       uint32_t rank);
 
+/* ------------------------------------------- norm with FP8 output */
+
+/* RMS norm in front of a projection, with the residual's addition before it and
+ * the projection's quantizer after it:
+ *   h    = bf16_rne( x + residual )   (residual NULL: h = x)
+ *   rstd = 1 / sqrt( sum_k h[m,k]^2 / K + eps )
+ *   y    = h * rstd * weight          (fp32)
+ *   scale[m,g] = amax|y[m,128g..]| / 448,  q = e4m3_rne_sat( y / scale )
+ *   x_bf16, residual_bf16  [M,K], weight_bf16 [K], read only
+ *   h_bf16    [M,K] out, the new residual stream: required with a residual (it may
+ *             be x's or the residual's own array), NULL without
+ *   y_bf16    [M,K] out or NULL: y rounded to bf16, for consumers that take bf16
+ *             (a router, the token codes of a gradient)
+ *   q_e4m3    [M,K] out; scale_rm [M,K/128] and scale_km [K/128, ceil16(M)] out, one
+ *             at least (pad slots of scale_km are written +0.0)
+ *   rstd      [M] fp32 out or NULL: what fp8q_add_rmsnorm_grad reads
+ * Sums, rstd and y are fp32; y is quantized from fp32, not from its bf16 copy.  A
+ * row with a NaN or an infinity, or whose squares leave fp32's range, gets NaN
+ * scales.  K % 128 == 0, K <= FP8Q_MAX_NORM_K; eps from 2^-126 up, finite, else
+ * FP8Q_ERR_VARIANT.  M == 0: nothing.  Otherwise as fp8q_quant_act. */
+#define FP8Q_MAX_NORM_K 32768
+fp8q_status fp8q_add_rmsnorm_quant(const uint16_t *x_bf16, const uint16_t *residual_bf16,
+                                   const uint16_t *weight_bf16, uint16_t *h_bf16,
+                                   uint16_t *y_bf16, uint8_t *q_e4m3, float *scale_rm,
+                                   float *scale_km, float *rstd, float eps, uint32_t M,
+                                   uint32_t K, hipStream_t stream);
+
+/* Its gradient, from dy (of y) and dh (of the residual stream h):
+ *   g = weight * dy, xhat = h * rstd
+ *   dx[m,k]     = bf16_rne( dh + rstd * (g - xhat * sum_k(g * xhat) / K) )
+ *   dweight[k]  = sum_m dy[m,k] * xhat[m,k]
+ *   dy_bf16, h_bf16 [M,K], weight_bf16 [K], rstd [M] as the forward call gave it;
+ *             dh_bf16 [M,K] or NULL (no gradient of h itself)
+ *   dx_bf16   [M,K] out: the gradient of x and of the residual alike; it may be dy's,
+ *             dh's or h's own array
+ *   dweight   [K] fp32 out (M == 0: zeros)
+ *   workspace fp8q_add_rmsnorm_grad_workspace_bytes(M, K) bytes; contents undefined
+ *             on return; calls in flight must not share it
+ * fp32 throughout, no atomics: results do not depend on scheduling. */
+fp8q_status fp8q_add_rmsnorm_grad(const uint16_t *dy_bf16, const uint16_t *dh_bf16,
+                                  const uint16_t *h_bf16, const uint16_t *weight_bf16,
+                                  const float *rstd, uint16_t *dx_bf16, float *dweight,
+                                  void *workspace, size_t workspace_bytes, uint32_t M,
+                                  uint32_t K, hipStream_t stream);
+size_t fp8q_add_rmsnorm_grad_workspace_bytes(uint32_t M, uint32_t K);
+
+/* ------------------------------------- gradients of the projection */
+
+/* Two-way quantizer: what the two gradient products below read of a matrix, from one
+ * pass over it.
+ *   x_bf16    [M,K], read only: a gradient dy, or the activations
+ *   q_e4m3, scale_km   row codes, as fp8q_quant_act_kmajor writes them bit for bit
+ *             ([M,K]; [K/128, ceil16(M)]); both NULL: not wanted
+ *   q_tok     [M,K] out, token codes: q_tok[m,k] = e4m3_rne( x[m,k] / 2^e ), e the
+ *             least integer >= -127 with amax <= 448 * 2^e over the 128 tokens
+ *             128*(m/128) .. of column k (the last block may be shorter)
+ *   exp_tok   [ceil(M/512), K, 4] bytes out: entry [i/4, k, i%4] = e + 127 of token
+ *             block i and column k (0 for a block of zeros; 255, the scale NaN, where
+ *             the block holds a NaN or an infinity); entries past the last block are 0
+ * K % 128 == 0.  M == 0: nothing. */
+fp8q_status fp8q_quant_act_dual(const uint16_t *x_bf16, uint8_t *q_e4m3, float *scale_km,
+                                uint8_t *q_tok, uint8_t *exp_tok, uint32_t M, uint32_t K,
+                                hipStream_t stream);
+
+/* Gradient of the projection's input:
+ *   dx[m,k] = bf16_rne( sum_nb dy_scale_km[nb*Mp + m] * w_scale[nb][k/128]
+ *                       * sum_{j<128} dec(dy[m,128nb+j]) * dec(w[128nb+j,k]) )
+ *   dy_e4m3, dy_scale_km  row codes [M,N] and K-major scales [N/128, ceil16(M)] of the
+ *             output's gradient (fp8q_quant_act_dual, fp8q_quant_act_kmajor)
+ *   w_e4m3, w_scale       [N,K] and [N/128, K/128]: the forward call's own arrays
+ *   dx_bf16   [M,K] out
+ *   workspace fp8q_gemm_dgrad_workspace_bytes(M, N, K) bytes (may be NULL when that
+ *             is 0); contents undefined on return; calls in flight must not share it
+ * Accumulation, reproducibility and errors as fp8q_gemm_blockscaled. */
+fp8q_status fp8q_gemm_dgrad(const uint8_t *dy_e4m3, const float *dy_scale_km,
+                            const uint8_t *w_e4m3, const float *w_scale,
+                            uint16_t *dx_bf16, void *workspace, size_t workspace_bytes,
+                            uint32_t M, uint32_t N, uint32_t K, hipStream_t stream);
+size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
+
+/* Gradient of the projection's weights:
+ *   dw[n,k] = bf16_rne( sum_i 2^(dy_exp(i,n) + x_exp(i,k) - 254)
+ *                       * sum_{m in token block i} dec(dy_tok[m,n]) * dec(x_tok[m,k]) )
+ *   dy_tok, dy_exp, x_tok, x_exp   token codes and bytes of dy [M,N] and x [M,K] from
+ *             fp8q_quant_act_dual
+ *   dw_bf16   [N,K] out (M == 0: zeros)
+ *   workspace fp8q_gemm_wgrad_workspace_bytes(M, N, K) bytes, as above
+ * N % 128 == 0, K % 128 == 0; element counts below 2^32.  The FP8 matrix instruction
+ * sums a 128-token block to about 16 bits and adds the blocks in fp32: 1.5e-5 of the
+ * result's norm, a hundredth of the bf16 rounding.  Reproducible run to run. */
+fp8q_status fp8q_gemm_wgrad(const uint8_t *dy_tok, const uint8_t *dy_exp,
+                            const uint8_t *x_tok, const uint8_t *x_exp, uint16_t *dw_bf16,
+                            void *workspace, size_t workspace_bytes, uint32_t M,
+                            uint32_t N, uint32_t K, hipStream_t stream);
+size_t fp8q_gemm_wgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
+
+/* ---------------------------------------- gradients of the routing */
+
+/* Balance loss of a router, from its logits and the choices of fp8q_moe_route:
+ *   p[t] = softmax(logits[t]) over the experts that can be chosen (as in the routing:
+ *          not -inf or NaN; +inf counts as the largest finite value)
+ *   n    = tokens with such an expert
+ *   counts[e] = slots with id e, prob[e] = sum_t p[t][e] / n
+ *   loss = coef * E * sum_e counts[e] / (n * top_k) * prob[e]
+ *   logits   [T,E] fp32 (logits_bf16 = 0) or bf16 (1); ids [T,top_k] int32, ids outside
+ *            0..E-1 count nowhere; read only
+ *   counts   [E+1] int32 out, counts[E] = n;  prob [E] and loss [1] fp32 out (zeros
+ *            where n is 0, T == 0 among it)
+ *   workspace of fp8q_moe_balance_workspace_bytes(T, E) bytes (may be NULL when that is
+ *            0); contents undefined on return; calls in flight must not share it
+ * fp32 sums in a fixed order: results do not depend on scheduling.  Limits and errors
+ * as fp8q_moe_route. */
+fp8q_status fp8q_moe_balance(const void *logits, int logits_bf16, const int32_t *ids,
+                             int32_t *counts, float *prob, float *loss, void *workspace,
+                             size_t workspace_bytes, float coef, uint32_t T, uint32_t E,
+                             uint32_t top_k, hipStream_t stream);
+size_t fp8q_moe_balance_workspace_bytes(uint32_t T, uint32_t E);
+
+/* Gradient of the router's logits, through the weights, the balance loss or both:
+ *   dlogits = d(weights) + d(loss), counts held constant:
+ *   d(weights)[e] = w[e] * (D[e] - m[e] * sum_i w[i] D[i])   renormalize = 1, w the
+ *                   softmax over the chosen slots, m[e] of which hold expert e
+ *                 = p[e] * (D[e] - sum_i p[i] D[i])          renormalize = 0
+ *                   D[e] = sum of dweights over the slots of expert e
+ *   d(loss)[e]    = p[e] * (c[e] - sum_i p[i] c[i]), c[e] = dloss * coef * E
+ *                   * counts[e] / (n * top_k) / n
+ *   ids, dweights  [T,top_k] int32 and fp32 (both NULL: no gradient of the weights);
+ *                  slots whose id lies outside 0..E-1 are left out
+ *   counts         [E+1] as fp8q_moe_balance gave them (NULL: no balance loss); sums
+ *                  over several ranks' tokens do as well
+ *   dloss          [1] fp32, the loss's own gradient (NULL: 1)
+ *   dlogits        [T,E] out, of the logits' type; 0 where an expert cannot be chosen
+ * One of ids and counts at least.  top_k as in the forward calls.  T == 0: nothing. */
+fp8q_status fp8q_moe_route_grad(const void *logits, int logits_bf16, const int32_t *ids,
+                                const float *dweights, const int32_t *counts,
+                                const float *dloss, void *dlogits, float coef, uint32_t T,
+                                uint32_t E, uint32_t top_k, int renormalize,
+                                hipStream_t stream);
+
 /* ------------------------------------------------- measurement support */
 
 /* Clock stamp, for measuring the sustained shader clock over a region of a

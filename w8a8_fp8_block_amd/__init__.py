@@ -26,6 +26,13 @@ Names match the C entry points:
   fp8q_moe_combine(y, weights, pos, offsets, out)
   fp8q_proj_lora(x, w, w_scale, lora_a, lora_b, lora_scale, adapter_ids, out, act_q, act_scale,
                  act_scale_km, workspace)
+  fp8q_add_rmsnorm_quant(x, residual, weight, h, y, q, scale_rm, scale_km, rstd, eps=1e-6)
+  fp8q_add_rmsnorm_grad(dy, dh, h, weight, rstd, dx, dweight, workspace)
+  fp8q_quant_act_dual(x, q, scale_km, q_tok, exp_tok)
+  fp8q_gemm_dgrad(dy, dy_scale_km, w, w_scale, dx, workspace)
+  fp8q_gemm_wgrad(dy_tok, dy_exp, x_tok, x_exp, dw, workspace)
+  fp8q_moe_balance(logits, ids, counts, prob, loss, workspace, coef=1.0)
+  fp8q_moe_route_grad(logits, ids, dweights, counts, dloss, dlogits, renormalize=True, coef=1.0)
   fp8q_m_pad(m), fp8q_quant_select(M, K, cu_count), ...
 
 Dtypes: bf16 tensors may be torch.bfloat16 or torch.uint16/int16 views;
@@ -49,6 +56,7 @@ _P = ctypes.c_void_p
 _U = ctypes.c_uint32
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
 
 
 class SelectParams(ctypes.Structure):
@@ -114,6 +122,17 @@ _SIGS = {
     "fp8q_proj_lora": (_I, [_P] * 12 + [_SZ, _U, _U, _U, _U, _U, _P]),
     "fp8q_proj_lora_workspace_bytes": (_SZ, [_U, _U, _U, _U]),
     "fp8q_moe_ffn_workspace_bytes": (_SZ, [_U, _U, _U, _U, _U, _I]),
+    "fp8q_add_rmsnorm_quant": (_I, [_P] * 9 + [_F, _U, _U, _P]),
+    "fp8q_add_rmsnorm_grad": (_I, [_P] * 8 + [_SZ, _U, _U, _P]),
+    "fp8q_add_rmsnorm_grad_workspace_bytes": (_SZ, [_U, _U]),
+    "fp8q_quant_act_dual": (_I, [_P] * 5 + [_U, _U, _P]),
+    "fp8q_gemm_dgrad": (_I, [_P] * 6 + [_SZ, _U, _U, _U, _P]),
+    "fp8q_gemm_dgrad_workspace_bytes": (_SZ, [_U, _U, _U]),
+    "fp8q_gemm_wgrad": (_I, [_P] * 6 + [_SZ, _U, _U, _U, _P]),
+    "fp8q_gemm_wgrad_workspace_bytes": (_SZ, [_U, _U, _U]),
+    "fp8q_moe_balance": (_I, [_P, _I] + [_P] * 5 + [_SZ, _F, _U, _U, _U, _P]),
+    "fp8q_moe_balance_workspace_bytes": (_SZ, [_U, _U]),
+    "fp8q_moe_route_grad": (_I, [_P, _I] + [_P] * 5 + [_F, _U, _U, _U, _I, _P]),
 }
 
 _lib = None
@@ -590,6 +609,147 @@ def fp8q_proj_lora(x, w, w_scale, lora_a, lora_b, lora_scale, adapter_ids, out, 
                                _scratch(act_q, _E4M3, M * K, "act_q"), _scratch(act_scale, _F32, M * G, "act_scale"),
                                _scratch(act_scale_km, _F32, G * ((M + 15) // 16 * 16), "act_scale_km"),
                                _optr(workspace), _nbytes(workspace), M, N, K, n, R, _stream(stream)))
+
+
+_I32 = frozenset((torch.int32,))
+_U8 = frozenset((torch.uint8,))
+
+
+def _arg(t, dtypes, shape, what) -> int:
+    """Pointer of a tensor of one of `dtypes` and of `shape`, contiguous and on the
+    current device (whose stream the call goes to)."""
+    if t.dtype not in dtypes:
+        _wrong_type(**{what: (t, dtypes)})
+    if t.shape != shape:
+        raise ValueError(f"{what} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} must be on the current GPU, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _oarg(t, dtypes, shape, what) -> int:
+    return 0 if t is None else _arg(t, dtypes, shape, what)
+
+
+def _work(t):
+    """(pointer, bytes) of a workspace."""
+    return (0, 0) if t is None else (_arg(t, _U8, t.shape, "workspace"), t.numel())
+
+
+def fp8q_add_rmsnorm_quant(x, residual, weight, h, y, q, scale_rm, scale_km, rstd, eps: float = 1e-6, stream=None):
+    """h = x + residual (bf16, [M,K]); q, scale_rm [M,K/128] and scale_km
+    [K/128, ceil16(M)] = the FP8 codes and scales of h * rstd * weight, y the same in
+    bf16, rstd [M] float32 = 1 / sqrt(mean(h^2) + eps).  residual and h go together
+    (None: h is x); y, rstd and one of the scales may be None."""
+    M, K = shape = _dims(x, 2)
+    _check(lib().fp8q_add_rmsnorm_quant(
+        _arg(x, _BF16, shape, "x"), _oarg(residual, _BF16, shape, "residual"), _arg(weight, _BF16, (K,), "weight"),
+        _oarg(h, _BF16, shape, "h"), _oarg(y, _BF16, shape, "y"), _arg(q, _E4M3, shape, "q"),
+        _oarg(scale_rm, _F32, (M, K // 128), "scale_rm"),
+        _oarg(scale_km, _F32, (K // 128, (M + 15) // 16 * 16), "scale_km"), _oarg(rstd, _F32, (M,), "rstd"), eps, M, K,
+        _stream(stream)))
+
+
+def fp8q_add_rmsnorm_grad_workspace_bytes(M: int, K: int) -> int:
+    return int(lib().fp8q_add_rmsnorm_grad_workspace_bytes(M, K))
+
+
+def fp8q_add_rmsnorm_grad(dy, dh, h, weight, rstd, dx, dweight, workspace, stream=None):
+    """The gradient of fp8q_add_rmsnorm_quant: dx [M,K] bf16 (of x and of the residual)
+    from dy (of y) and dh (of h; None: none), dweight [K] float32; workspace: a uint8
+    tensor of fp8q_add_rmsnorm_grad_workspace_bytes(M, K)."""
+    M, K = shape = _dims(h, 2)
+    work, nbytes = _work(workspace)
+    _check(lib().fp8q_add_rmsnorm_grad(
+        _arg(dy, _BF16, shape, "dy"), _oarg(dh, _BF16, shape, "dh"), _arg(h, _BF16, shape, "h"),
+        _arg(weight, _BF16, (K,), "weight"), _arg(rstd, _F32, (M,), "rstd"), _arg(dx, _BF16, shape, "dx"),
+        _arg(dweight, _F32, (K,), "dweight"), work, nbytes, M, K, _stream(stream)))
+
+
+def fp8q_quant_act_dual(x, q, scale_km, q_tok, exp_tok, stream=None):
+    """Codes of x [M,K] bf16 along its rows (q, scale_km as fp8q_quant_act_kmajor's;
+    both None: not wanted) and along its tokens (q_tok [M,K], exp_tok
+    [ceil(M/512),K,4] uint8)."""
+    M, K = shape = _dims(x, 2)
+    _check(lib().fp8q_quant_act_dual(
+        _arg(x, _BF16, shape, "x"), _oarg(q, _E4M3, shape, "q"),
+        _oarg(scale_km, _F32, (K // 128, (M + 15) // 16 * 16), "scale_km"), _arg(q_tok, _E4M3, shape, "q_tok"),
+        _arg(exp_tok, _U8, ((M + 511) // 512, K, 4), "exp_tok"), M, K, _stream(stream)))
+
+
+def fp8q_gemm_dgrad_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().fp8q_gemm_dgrad_workspace_bytes(M, N, K))
+
+
+def fp8q_gemm_dgrad(dy, dy_scale_km, w, w_scale, dx, workspace, stream=None):
+    """dx [M,K] bf16 = dy [M,N] times w [N,K] (row codes of dy with K-major scales; w as
+    the forward call reads it); workspace: a uint8 tensor of
+    fp8q_gemm_dgrad_workspace_bytes(M, N, K), or None when that is 0."""
+    M, N = shape = _dims(dy, 2)
+    K = _dims(w, 2)[1]
+    work, nbytes = _work(workspace)
+    _check(lib().fp8q_gemm_dgrad(
+        _arg(dy, _E4M3, shape, "dy"), _arg(dy_scale_km, _F32, (N // 128, (M + 15) // 16 * 16), "dy_scale_km"),
+        _arg(w, _E4M3, (N, K), "w"), _arg(w_scale, _F32, (N // 128, K // 128), "w_scale"),
+        _arg(dx, _BF16, (M, K), "dx"), work, nbytes, M, N, K, _stream(stream)))
+
+
+def fp8q_gemm_wgrad_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib().fp8q_gemm_wgrad_workspace_bytes(M, N, K))
+
+
+def fp8q_gemm_wgrad(dy_tok, dy_exp, x_tok, x_exp, dw, workspace, stream=None):
+    """dw [N,K] bf16 = the transpose of dy [M,N] times x [M,K], both as
+    fp8q_quant_act_dual's token codes and bytes; workspace: a uint8 tensor of
+    fp8q_gemm_wgrad_workspace_bytes(M, N, K), or None when that is 0."""
+    M, N = shape = _dims(dy_tok, 2)
+    K = _dims(x_tok, 2)[1]
+    packs = (M + 511) // 512
+    work, nbytes = _work(workspace)
+    _check(lib().fp8q_gemm_wgrad(
+        _arg(dy_tok, _E4M3, shape, "dy_tok"), _arg(dy_exp, _U8, (packs, N, 4), "dy_exp"),
+        _arg(x_tok, _E4M3, (M, K), "x_tok"), _arg(x_exp, _U8, (packs, K, 4), "x_exp"), _arg(dw, _BF16, (N, K), "dw"),
+        work, nbytes, M, N, K, _stream(stream)))
+
+
+_LOGITS = frozenset((torch.float32, torch.bfloat16))
+
+
+def fp8q_moe_balance_workspace_bytes(T: int, E: int) -> int:
+    return int(lib().fp8q_moe_balance_workspace_bytes(T, E))
+
+
+def fp8q_moe_balance(logits, ids, counts, prob, loss, workspace, coef: float = 1.0, stream=None):
+    """Balance loss of router logits [T,E] (float32 or bfloat16) and choices ids
+    [T,top_k] int32: counts [E+1] int32 (the last: tokens with an expert to choose),
+    prob [E] and loss [1] float32; workspace: a uint8 tensor of
+    fp8q_moe_balance_workspace_bytes(T, E), or None when that is 0."""
+    T, E = shape = _dims(logits, 2)
+    k = _dims(ids, 2)[1]
+    work, nbytes = _work(workspace)
+    _check(lib().fp8q_moe_balance(
+        _arg(logits, _LOGITS, shape, "logits"), logits.dtype is torch.bfloat16, _arg(ids, _I32, (T, k), "ids"),
+        _arg(counts, _I32, (E + 1,), "counts"), _arg(prob, _F32, (E,), "prob"), _arg(loss, _F32, (1,), "loss"), work,
+        nbytes, coef, T, E, k, _stream(stream)))
+
+
+def fp8q_moe_route_grad(logits, ids, dweights, counts, dloss, dlogits, renormalize: bool = True, coef: float = 1.0,
+                        top_k: int = None, stream=None):
+    """dlogits [T,E], of the logits' type, through the weights of fp8q_moe_route (ids and
+    their gradients dweights [T,top_k] float32; both None: not) and the balance loss
+    (counts [E+1] of fp8q_moe_balance, dloss [1] float32 or None for 1; counts None:
+    not).  top_k: needed where ids is None."""
+    T, E = shape = _dims(logits, 2)
+    k = top_k if ids is None else _dims(ids, 2)[1]
+    if k is None:
+        raise ValueError("top_k is needed without ids")
+    _check(lib().fp8q_moe_route_grad(
+        _arg(logits, _LOGITS, shape, "logits"), logits.dtype is torch.bfloat16, _oarg(ids, _I32, (T, k), "ids"),
+        _oarg(dweights, _F32, (T, k), "dweights"), _oarg(counts, _I32, (E + 1,), "counts"),
+        _oarg(dloss, _F32, (1,), "dloss"), _arg(dlogits, (logits.dtype,), shape, "dlogits"), coef, T, E, k,
+        bool(renormalize), _stream(stream)))
 
 
 def fp8q_default_select_params(cu_count: int) -> SelectParams:

@@ -46,6 +46,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
     if (!aligned16(p)) return fail(FP8Q_ERR_ALIGN, "%s: " #p " is not 16-byte aligned", fn); \
   } while (0)
 
+// An optional array.
+#define REQUIRE_ALIGNED(p)                                                          \
+  do {                                                                              \
+    if (!aligned16(p)) return fail(FP8Q_ERR_ALIGN, "%s: " #p " is not 16-byte aligned", fn); \
+  } while (0)
+
 constexpr uint64_t kMaxElems = 0xFFFFFFFFull;
 
 fp8q_status check_k(const char* fn, uint32_t K) {
@@ -602,6 +608,46 @@ MoeWorkspace moe_workspace(uint32_t T, uint32_t top_k, uint32_t H, uint32_t I, i
   return w;
 }
 
+// ---- a training step ----
+fp8q_status check_norm(const char* fn, uint32_t M, uint32_t K) {
+  fp8q_status st = check_mk(fn, M, K);
+  if (st != FP8Q_OK) return st;
+  if (K > kMaxNormK) return fail(FP8Q_ERR_SHAPE, "%s: K=%u exceeds %u", fn, K, kMaxNormK);
+  if ((uint64_t)m_pad16(M) * K > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: ceil16(M)*K exceeds 2^32-1", fn);
+  return FP8Q_OK;
+}
+
+// dy [M,N], x and dx [M,K], w and dw [N,K]
+bool grad_shape(uint32_t M, uint32_t N, uint32_t K) {
+  const uint64_t Mp = ((uint64_t)M + 15) / 16 * 16;  // (m_pad16 would wrap for M near 2^32)
+  return N && K && N % kGroup == 0 && K % kGroup == 0 && Mp * N <= kMaxElems && Mp * K <= kMaxElems &&
+         (uint64_t)N * K <= kMaxElems;
+}
+fp8q_status check_grad(const char* fn, uint32_t M, uint32_t N, uint32_t K) {
+  if (grad_shape(M, N, K)) return FP8Q_OK;
+  return fail(FP8Q_ERR_SHAPE,
+              "%s: M=%u N=%u K=%u (N and K positive multiples of 128; ceil16(M)*N, ceil16(M)*K and N*K up to 2^32-1)",
+              fn, M, N, K);
+}
+
+uint32_t dgrad_splits(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
+  return 1;
+}
+uint32_t wgrad_splits(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
+  return 1;
+}
+
+// A router's logits [T,E] and choices [T,top_k].
+fp8q_status check_router(const char* fn, uint32_t T, uint32_t E, uint32_t top_k) {
+  fp8q_status st = check_groups(fn, E);
+  if (st != FP8Q_OK) return st;
+  st = check_slots(fn, T, top_k);
+  if (st != FP8Q_OK) return st;
+  if (top_k > E) return fail(FP8Q_ERR_SHAPE, "%s: top_k=%u of %u experts", fn, top_k, E);
+  if ((uint64_t)T * E > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: T*E exceeds 2^32-1", fn);
+  return FP8Q_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -917,6 +963,189 @@ fp8q_status fp8q_gemm_blockscaled_splitk(const uint8_t* a_e4m3, const float* a_s
                                         stream));
 }
 
+fp8q_status fp8q_add_rmsnorm_quant(const uint16_t* x_bf16, const uint16_t* residual_bf16,
+                                   const uint16_t* weight_bf16, uint16_t* h_bf16, uint16_t* y_bf16,
+                                   uint8_t* q_e4m3, float* scale_rm, float* scale_km, float* rstd, float eps,
+                                   uint32_t M, uint32_t K, hipStream_t stream) {
+  const char* fn = "fp8q_add_rmsnorm_quant";
+  if (!(eps >= 0x1p-126f && eps <= 3.402823466e38f))
+    return fail(FP8Q_ERR_VARIANT, "%s: eps=%g (finite, 2^-126 or more)", fn, (double)eps);
+  fp8q_status st = check_norm(fn, M, K);
+  if (st != FP8Q_OK) return st;
+  if (M == 0) return ok();
+  REQUIRE_PTR(x_bf16);
+  REQUIRE_PTR(weight_bf16);
+  REQUIRE_PTR(q_e4m3);
+  if (residual_bf16) {
+    REQUIRE_ALIGNED(residual_bf16);
+    REQUIRE_PTR(h_bf16);
+  } else if (h_bf16) {
+    return fail(FP8Q_ERR_NULL, "%s: h_bf16 without residual_bf16 (h is x then)", fn);
+  }
+  REQUIRE_ALIGNED(y_bf16);
+  if (!scale_rm && !scale_km) return fail(FP8Q_ERR_NULL, "%s: scale_rm and scale_km are NULL", fn);
+  REQUIRE_ALIGNED(scale_rm);
+  REQUIRE_ALIGNED(scale_km);
+  REQUIRE_ALIGNED(rstd);
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_norm_quant(x_bf16, residual_bf16, weight_bf16, h_bf16, y_bf16, q_e4m3, scale_rm,
+                                        scale_km, rstd, eps, M, K, stream));
+}
+
+fp8q_status fp8q_add_rmsnorm_grad(const uint16_t* dy_bf16, const uint16_t* dh_bf16, const uint16_t* h_bf16,
+                                  const uint16_t* weight_bf16, const float* rstd, uint16_t* dx_bf16,
+                                  float* dweight, void* workspace, size_t workspace_bytes, uint32_t M, uint32_t K,
+                                  hipStream_t stream) {
+  const char* fn = "fp8q_add_rmsnorm_grad";
+  fp8q_status st = check_norm(fn, M, K);
+  if (st != FP8Q_OK) return st;
+  REQUIRE_PTR(dweight);
+  if (M > 0) {
+    REQUIRE_PTR(dy_bf16);
+    REQUIRE_ALIGNED(dh_bf16);
+    REQUIRE_PTR(h_bf16);
+    REQUIRE_PTR(weight_bf16);
+    REQUIRE_PTR(rstd);
+    REQUIRE_PTR(dx_bf16);
+  }
+  st = check_workspace(fn, workspace, workspace_bytes, norm_grad_workspace_bytes(M, K));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_norm_grad(dy_bf16, dh_bf16, h_bf16, weight_bf16, rstd, dx_bf16, dweight, workspace, M,
+                                       K, stream));
+}
+
+size_t fp8q_add_rmsnorm_grad_workspace_bytes(uint32_t M, uint32_t K) {
+  if (K == 0 || K % kGroup != 0 || K > kMaxNormK) return 0;
+  return (size_t)norm_grad_workspace_bytes(M, K);
+}
+
+fp8q_status fp8q_quant_act_dual(const uint16_t* x_bf16, uint8_t* q_e4m3, float* scale_km, uint8_t* q_tok,
+                                uint8_t* exp_tok, uint32_t M, uint32_t K, hipStream_t stream) {
+  const char* fn = "fp8q_quant_act_dual";
+  fp8q_status st = check_mk(fn, M, K);
+  if (st != FP8Q_OK) return st;
+  if ((uint64_t)m_pad16(M) * K > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: ceil16(M)*K exceeds 2^32-1", fn);
+  if (M == 0) return ok();
+  REQUIRE_PTR(x_bf16);
+  REQUIRE_PTR(q_tok);
+  REQUIRE_PTR(exp_tok);
+  if (q_e4m3 || scale_km) {
+    REQUIRE_PTR(q_e4m3);
+    REQUIRE_PTR(scale_km);
+  }
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_quant_dual(x_bf16, q_e4m3, scale_km, q_tok, exp_tok, M, K, stream));
+}
+
+fp8q_status fp8q_gemm_dgrad(const uint8_t* dy_e4m3, const float* dy_scale_km, const uint8_t* w_e4m3,
+                            const float* w_scale, uint16_t* dx_bf16, void* workspace, size_t workspace_bytes,
+                            uint32_t M, uint32_t N, uint32_t K, hipStream_t stream) {
+  const char* fn = "fp8q_gemm_dgrad";
+  fp8q_status st = check_grad(fn, M, N, K);
+  if (st != FP8Q_OK) return st;
+  if (M == 0) return ok();
+  REQUIRE_PTR(dy_e4m3);
+  REQUIRE_PTR(dy_scale_km);
+  REQUIRE_PTR(w_e4m3);
+  REQUIRE_PTR(w_scale);
+  REQUIRE_PTR(dx_bf16);
+  const uint32_t splits = dgrad_splits(M, N, K, current_cus());
+  st = check_workspace(fn, workspace, workspace_bytes, splitk_workspace(M, K, splits));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_gemm_dgrad(dy_e4m3, dy_scale_km, w_e4m3, w_scale, dx_bf16,
+                                        static_cast<float*>(workspace), M, N, K, splits, stream));
+}
+
+size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K) {
+  if (!grad_shape(M, N, K) || M == 0) return 0;
+  return (size_t)splitk_workspace(M, K, dgrad_splits(M, N, K, current_cus()));
+}
+
+fp8q_status fp8q_gemm_wgrad(const uint8_t* dy_tok, const uint8_t* dy_exp, const uint8_t* x_tok,
+                            const uint8_t* x_exp, uint16_t* dw_bf16, void* workspace, size_t workspace_bytes,
+                            uint32_t M, uint32_t N, uint32_t K, hipStream_t stream) {
+  const char* fn = "fp8q_gemm_wgrad";
+  fp8q_status st = check_grad(fn, M, N, K);
+  if (st != FP8Q_OK) return st;
+  REQUIRE_PTR(dw_bf16);
+  if (M > 0) {
+    REQUIRE_PTR(dy_tok);
+    REQUIRE_PTR(dy_exp);
+    REQUIRE_PTR(x_tok);
+    REQUIRE_PTR(x_exp);
+  }
+  const uint32_t splits = wgrad_splits(M, N, K, current_cus());
+  st = check_workspace(fn, workspace, workspace_bytes, splitk_workspace(N, K, splits));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_gemm_wgrad(dy_tok, dy_exp, x_tok, x_exp, dw_bf16, static_cast<float*>(workspace), M, N,
+                                        K, splits, stream));
+}
+
+size_t fp8q_gemm_wgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K) {
+  if (!grad_shape(M, N, K)) return 0;
+  return (size_t)splitk_workspace(N, K, wgrad_splits(M, N, K, current_cus()));
+}
+
+fp8q_status fp8q_moe_balance(const void* logits, int logits_bf16, const int32_t* ids, int32_t* counts, float* prob,
+                             float* loss, void* workspace, size_t workspace_bytes, float coef, uint32_t T,
+                             uint32_t E, uint32_t top_k, hipStream_t stream) {
+  const char* fn = "fp8q_moe_balance";
+  if (logits_bf16 < 0 || logits_bf16 > 1)
+    return fail(FP8Q_ERR_VARIANT, "%s: logits_bf16=%d (0 or 1)", fn, logits_bf16);
+  fp8q_status st = check_router(fn, T, E, top_k);
+  if (st != FP8Q_OK) return st;
+  REQUIRE_PTR(counts);
+  REQUIRE_PTR(prob);
+  REQUIRE_PTR(loss);
+  if (T > 0) {
+    REQUIRE_PTR(logits);
+    REQUIRE_PTR(ids);
+  }
+  st = check_workspace(fn, workspace, workspace_bytes, balance_workspace_bytes(T, E));
+  if (st != FP8Q_OK) return st;
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_balance(logits, logits_bf16 != 0, ids, counts, prob, loss, workspace, coef, T, E, top_k,
+                                     stream));
+}
+
+size_t fp8q_moe_balance_workspace_bytes(uint32_t T, uint32_t E) {
+  if (E == 0 || E > kMaxExperts) return 0;
+  return (size_t)balance_workspace_bytes(T, E);
+}
+
+fp8q_status fp8q_moe_route_grad(const void* logits, int logits_bf16, const int32_t* ids, const float* dweights,
+                                const int32_t* counts, const float* dloss, void* dlogits, float coef, uint32_t T,
+                                uint32_t E, uint32_t top_k, int renormalize, hipStream_t stream) {
+  const char* fn = "fp8q_moe_route_grad";
+  if (logits_bf16 < 0 || logits_bf16 > 1 || renormalize < 0 || renormalize > 1)
+    return fail(FP8Q_ERR_VARIANT, "%s: logits_bf16=%d, renormalize=%d (0 or 1)", fn, logits_bf16, renormalize);
+  fp8q_status st = check_router(fn, T, E, top_k);
+  if (st != FP8Q_OK) return st;
+  if (T == 0) return ok();
+  if (!ids && !dweights && !counts) return fail(FP8Q_ERR_NULL, "%s: neither ids and dweights nor counts", fn);
+  if (ids || dweights) {
+    REQUIRE_PTR(ids);
+    REQUIRE_PTR(dweights);
+  }
+  REQUIRE_ALIGNED(counts);
+  REQUIRE_ALIGNED(dloss);
+  REQUIRE_PTR(logits);
+  REQUIRE_PTR(dlogits);
+  st = check_device(fn);
+  if (st != FP8Q_OK) return st;
+  return launched(fn, launch_route_grad(logits, logits_bf16 != 0, ids, dweights, counts, dloss, dlogits, coef, T, E,
+                                        top_k, renormalize != 0, stream));
+}
+
 fp8q_status fp8q_clock_stamp(unsigned long long* stamps, uint32_t n, hipStream_t stream) {
   const char* fn = "fp8q_clock_stamp";
   REQUIRE_PTR(stamps);
@@ -1137,12 +1366,8 @@ fp8q_status fp8q_moe_route(const void* logits, int logits_bf16, int32_t* ids, fl
   const char* fn = "fp8q_moe_route";
   if (logits_bf16 < 0 || logits_bf16 > 1 || renormalize < 0 || renormalize > 1)
     return fail(FP8Q_ERR_VARIANT, "%s: logits_bf16=%d, renormalize=%d (0 or 1)", fn, logits_bf16, renormalize);
-  fp8q_status st = check_groups(fn, E);
+  fp8q_status st = check_router(fn, T, E, top_k);
   if (st != FP8Q_OK) return st;
-  st = check_slots(fn, T, top_k);
-  if (st != FP8Q_OK) return st;
-  if (top_k > E) return fail(FP8Q_ERR_SHAPE, "%s: top_k=%u of %u experts", fn, top_k, E);
-  if ((uint64_t)T * E > kMaxElems) return fail(FP8Q_ERR_SHAPE, "%s: T*E exceeds 2^32-1", fn);
   REQUIRE_PTR(offsets);
   if (T > 0) {
     REQUIRE_PTR(logits);

@@ -203,6 +203,37 @@ hipError_t launch_lora_gemm(const uint8_t* a, const float* a_s_km, const uint8_t
                             uint32_t adapters, uint32_t rank, uint32_t cus, int kernel, uint32_t splits,
                             hipStream_t s);
 
+// ---- a training step through the projection ----
+// RMS norm (norm.hip): h = bf16(x + r) (r NULL: h = x, h unused), codes q of
+// h * rstd * w with their scales in either layout, bf16 y and rstd where not NULL.
+constexpr uint32_t kMaxNormK = 32768;
+hipError_t launch_norm_quant(const uint16_t* x, const uint16_t* r, const uint16_t* w, uint16_t* h, uint16_t* y,
+                             uint8_t* q, float* scale_rm, float* scale_km, float* rstd, float eps, uint32_t M,
+                             uint32_t K, hipStream_t s);
+// Its gradient: dx = dh + d(norm) (dh NULL: none), dw [K] fp32; M = 0: dw = 0.
+uint64_t norm_grad_workspace_bytes(uint32_t M, uint32_t K);
+hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* w,
+                            const float* rstd, uint16_t* dx, float* dw, void* workspace, uint32_t M, uint32_t K,
+                            hipStream_t s);
+// Row codes with K-major scales (q NULL: not wanted) and token codes with their
+// exponent bytes [ceil(M/512), K, 4] (quant_dual.hip).
+hipError_t launch_quant_dual(const uint16_t* x, uint8_t* q, float* scale_km, uint8_t* q_tok, uint8_t* exp_tok,
+                             uint32_t M, uint32_t K, hipStream_t s);
+// Gradients of the block-scaled product (grad.hip): dx [M,K] from row codes dy
+// [M,N] and w [N,K]; dw [N,K] from token codes dy [M,N] and x [M,K].  splits >= 2:
+// the sum cut into as many ranges, their fp32 results in part.
+hipError_t launch_gemm_dgrad(const uint8_t* dy, const float* dy_s_km, const uint8_t* w, const float* w_s, uint16_t* dx,
+                             float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, hipStream_t s);
+hipError_t launch_gemm_wgrad(const uint8_t* dy, const uint8_t* ey, const uint8_t* x, const uint8_t* ex, uint16_t* dw,
+                             float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, hipStream_t s);
+// Balance loss of a router and the gradient of its logits (balance.hip).
+uint64_t balance_workspace_bytes(uint32_t T, uint32_t E);
+hipError_t launch_balance(const void* logits, bool bf16, const int32_t* ids, int32_t* counts, float* prob, float* loss,
+                          void* workspace, float coef, uint32_t T, uint32_t E, uint32_t top_k, hipStream_t s);
+hipError_t launch_route_grad(const void* logits, bool bf16, const int32_t* ids, const float* dweights,
+                             const int32_t* counts, const float* dloss, void* dlogits, float coef, uint32_t T,
+                             uint32_t E, uint32_t top_k, bool renorm, hipStream_t s);
+
 // Clock stamps (measurement support): n one-wave workgroups each write
 // {XCD id, HW_ID, shader clock counter, 100 MHz counter} to dst[4*i .. 4*i+3].
 hipError_t launch_clock_stamp(unsigned long long* dst, uint32_t n, hipStream_t s);

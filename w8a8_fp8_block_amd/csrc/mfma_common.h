@@ -83,6 +83,31 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r & 7u) ^ ((r >> 3) & 1u); }
 
+// Transposing LDS reads, for a matrix whose rows are the sum's index: a panel of
+// 128 rows x 128 bytes (columns), 16-byte chunk c of row r at chunk position
+// c ^ swz_t(r).  ds_read_b64_tr_b8 takes 8 bytes from each lane of a 16-lane row
+// and gives lane l byte l % 8 of the lanes 2j + l / 8, j = 0..7: with lane 2j + h
+// at row j, bytes 8h.. of a chunk, lane l gets column l of the chunk's 16 in 8
+// rows.  Four of them, 8 rows apart, fill the 32 K elements that lane group
+// q4 = lane / 16 holds of a fragment (rows 32 q4 ..), in order.  swz_t spreads the
+// 8 rows of a 16-lane row over the 8 chunk positions, and those of the lane groups
+// q4 and q4 + 1, which are read together, over chunks of different parity.
+__device__ __forceinline__ uint32_t swz_t(uint32_t r) { return (r & 7u) ^ ((r >> 5) & 1u); }
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+// This lane's byte offset in a panel for chunk 0; for chunk c, the offset ^ 16c.
+__device__ __forceinline__ uint32_t transposed_lane(uint32_t lane) {
+  const uint32_t row = 32 * (lane >> 4) + ((lane & 15) >> 1);
+  return row * 128 + swz_t(row) * 16 + (lane & 1) * 8;
+}
+// half h of the fragment whose lane offset (the chunk included) p is: 16 rows
+__device__ __forceinline__ v4i ld_transposed(const uint8_t* p, int h) {
+  typedef __attribute__((address_space(3))) v2i lds_v2i;
+  const v2i a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(p + h * 2048));
+  const v2i b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(p + h * 2048 + 1024));
+  return v4i{a.x, a.y, b.x, b.y};
+}
+
 // s_waitcnt vmcnt(n) leaving expcnt/lgkmcnt unconstrained (gfx9 encoding).
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {

@@ -1,0 +1,338 @@
+// RMS norm with the residual's addition and FP8 output, and its gradient, for
+// gfx950.
+//
+//   h    = bf16(x + r)                     (h = x where there is no residual)
+//   rstd = 1 / sqrt(mean(h^2) + eps)
+//   y    = h * rstd * w                    (fp32)
+//   per (token, 128 columns): scale = amax|y| / 448, q = e4m3(y / scale)
+//
+// h is rounded to bf16 before it is normalised: it is the residual stream that
+// the next layer and the gradient read, so all of them see one value.  y is
+// quantized from fp32 (one rounding, to 8 bits); the bf16 copy of y, for
+// consumers that take bf16, is rounded by itself.  Sums and statistics are fp32.
+//
+// The gradient, with g = w * dy and xhat = h * rstd:
+//   dx = dh + rstd * (g - xhat * mean(g * xhat)),   dw = sum over rows of dy * xhat
+//
+// Both are bound by memory: each element is loaded once into registers, reduced
+// over the row and finished from there.  A row belongs to W waves, lane t
+// holding the 8-value chunks t, t + 64 W, ...: 16 consecutive lanes hold a scale
+// group, whose maximum is one DPP reduction.
+#include <algorithm>
+
+#include "wave_common.h"
+
+namespace fp8q {
+namespace {
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
+}
+// Scale of a group of fp32 values from its maximum's bits, amax / 448 (as
+// group_scale, within an ulp here); a NaN or infinite maximum stays one.
+__device__ __forceinline__ float group_scale_f32(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits);
+  constexpr float k = 1.0f / 448.0f;
+  const float q0 = a * k;
+  const float s = __builtin_fmaf(-__builtin_fmaf(q0, 448.0f, -a), k, q0);
+  return amax_bits >= 0x7F800000u ? a : s;
+}
+
+// 1 / sqrt(v), v normal: the hardware's (1 ulp) and one Newton step; NaN for v
+// infinite (the square sum left fp32's range).
+__device__ __forceinline__ float rsqrt_f32(float v) {
+  const float r = __builtin_amdgcn_rsqf(v);
+  return __builtin_fmaf(r * 0.5f, __builtin_fmaf(-v * r, r, 1.0f), r);
+}
+
+// Sum over the W waves of this wave's row; red: one float a wave.  Called by the
+// whole workgroup; the next call must use the other half of a double buffer.
+template <uint32_t W>
+__device__ __forceinline__ float row_sum(float v, float* red, uint32_t wave) {
+  v = wave_sum_f32(v);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    const uint32_t first = wave / W * W;
+    v = red[first];
+#pragma unroll
+    for (uint32_t i = 1; i < W; ++i) v += red[first + i];
+  }
+  return v;
+}
+
+struct NormArgs {
+  const u32x4 *x, *r, *w;  // r NULL: no residual
+  u32x4 *h, *y;            // either may be NULL
+  u32x2* q;
+  float *srm, *skm, *rstd;  // any may be NULL
+  float eps;
+  uint32_t M, K, Mp;
+};
+
+constexpr uint32_t kNormMaxWaves = 16;
+
+// W waves a row, C chunks a lane; blockDim.x / (64 W) rows a workgroup.
+template <uint32_t W, uint32_t C>
+__global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
+  extern __shared__ float scales[];  // [rows][G]: the K-major scales' staging
+  __shared__ float red[kNormMaxWaves];
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t rows = (blockDim.x >> 6) / W, row = wave / W;
+  const uint32_t m0 = blockIdx.x * rows, m = m0 + row;
+  const uint32_t t = (wave % W) * 64 + lane, chunks = a.K / 8, G = a.K / kGroup;
+  const bool live = m < a.M;
+  const uint64_t base = (uint64_t)m * chunks;
+
+  // every load of the row before the first store (h may be x's or r's own array)
+  u32x4 h[C];
+#pragma unroll
+  for (uint32_t i = 0; i < C; ++i) {
+    const uint32_t c = t + 64 * W * i;
+    h[i] = u32x4{0, 0, 0, 0};
+    if (live && c < chunks) h[i] = a.x[base + c];
+  }
+  if (a.r) {
+    u32x4 r[C];
+#pragma unroll
+    for (uint32_t i = 0; i < C; ++i) {
+      const uint32_t c = t + 64 * W * i;
+      r[i] = u32x4{0, 0, 0, 0};
+      if (live && c < chunks) r[i] = a.r[base + c];
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < C; ++i) {
+      const uint32_t c = t + 64 * W * i;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        h[i][j] = pack_bf16(bf_lo(h[i][j]) + bf_lo(r[i][j]), bf_hi(h[i][j]) + bf_hi(r[i][j]));
+      if (live && c < chunks) a.h[base + c] = h[i];
+    }
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (uint32_t i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ss = __builtin_fmaf(bf_lo(h[i][j]), bf_lo(h[i][j]), ss);
+      ss = __builtin_fmaf(bf_hi(h[i][j]), bf_hi(h[i][j]), ss);
+    }
+  ss = row_sum<W>(ss, red, wave);
+  const float rstd = rsqrt_f32(ss / (float)a.K + a.eps);
+  if (live && t == 0 && a.rstd) a.rstd[m] = rstd;
+
+#pragma unroll
+  for (uint32_t i = 0; i < C; ++i) {
+    const uint32_t c = t + 64 * W * i;
+    if (live && c < chunks) {  // uniform over a group's 16 lanes
+      const u32x4 w = a.w[c];
+      float y[8], qv[8];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[2 * j] = bf_lo(h[i][j]) * rstd * bf_lo(w[j]);
+        y[2 * j + 1] = bf_hi(h[i][j]) * rstd * bf_hi(w[j]);
+        amax = max(amax, max(__float_as_uint(y[2 * j]) & 0x7FFFFFFFu, __float_as_uint(y[2 * j + 1]) & 0x7FFFFFFFu));
+      }
+      amax = dpp_row_max_u32(amax);
+      const float s = group_scale_f32(amax);
+      quotients<8>(y, s, qv);
+      a.q[base + c] = u32x2{encode4(qv), encode4(qv + 4)};
+      if (a.y) {
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+        a.y[base + c] = o;
+      }
+      if ((lane & 15) == 0) {
+        if (a.srm) a.srm[(uint64_t)m * G + c / 16] = s;
+        scales[row * G + c / 16] = s;
+      }
+    }
+  }
+  if (a.skm) {
+    // the K-major scales of the workgroup's rows, runs of `rows` along the
+    // tokens; the last workgroup writes the pad slots too
+    __syncthreads();
+    const uint32_t end = m0 + rows >= a.M ? a.Mp - m0 : rows;
+    for (uint32_t i = threadIdx.x; i < G * end; i += blockDim.x) {
+      const uint32_t g = i / end, r = i % end;
+      a.skm[(uint64_t)g * a.Mp + m0 + r] = m0 + r < a.M ? scales[r * G + g] : 0.0f;
+    }
+  }
+}
+
+struct NormGradArgs {
+  const u32x4 *dy, *dh, *h, *w;  // dh may be NULL
+  const float* rstd;
+  u32x4* dx;
+  float* part;  // [gridDim.x][K]
+  uint32_t M, K;
+};
+
+// A workgroup of W waves takes the rows b, b + gridDim.x, ... and keeps its share
+// of dw in registers.
+template <uint32_t W, uint32_t C>
+__global__ __launch_bounds__(64 * W) void norm_grad_kernel(NormGradArgs a) {
+  __shared__ float red[2][kNormMaxWaves];
+  const uint32_t wave = threadIdx.x >> 6, t = threadIdx.x, chunks = a.K / 8;
+  const float inv_k = 1.0f / (float)a.K;
+
+  float dw[C][8];
+#pragma unroll
+  for (uint32_t i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  uint32_t turn = 0;
+  for (uint32_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+    const uint64_t base = (uint64_t)m * chunks;
+    const float rstd = a.rstd[m];
+    u32x4 dy[C], h[C];
+    float s = 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < C; ++i) {
+      const uint32_t c = t + 64 * W * i;
+      dy[i] = h[i] = u32x4{0, 0, 0, 0};
+      if (c < chunks) {
+        dy[i] = a.dy[base + c];
+        h[i] = a.h[base + c];
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < C; ++i) {
+      const uint32_t c = t + 64 * W * i;
+      const u32x4 w = c < chunks ? a.w[c] : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float l = bf_lo(dy[i][j]) * (bf_lo(h[i][j]) * rstd), u = bf_hi(dy[i][j]) * (bf_hi(h[i][j]) * rstd);
+        dw[i][2 * j] += l;
+        dw[i][2 * j + 1] += u;
+        s = __builtin_fmaf(l, bf_lo(w[j]), s);
+        s = __builtin_fmaf(u, bf_hi(w[j]), s);
+      }
+    }
+    s = row_sum<W>(s, red[turn], wave) * inv_k;
+#pragma unroll
+    for (uint32_t i = 0; i < C; ++i) {
+      const uint32_t c = t + 64 * W * i;
+      if (c < chunks) {
+        const u32x4 w = a.w[c];
+        const u32x4 d = a.dh ? a.dh[base + c] : u32x4{0, 0, 0, 0};
+        u32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float l = rstd * (bf_lo(dy[i][j]) * bf_lo(w[j]) - bf_lo(h[i][j]) * rstd * s);
+          const float u = rstd * (bf_hi(dy[i][j]) * bf_hi(w[j]) - bf_hi(h[i][j]) * rstd * s);
+          o[j] = pack_bf16(l + bf_lo(d[j]), u + bf_hi(d[j]));
+        }
+        a.dx[base + c] = o;
+      }
+    }
+  }
+  float* out = a.part + (uint64_t)blockIdx.x * a.K;
+#pragma unroll
+  for (uint32_t i = 0; i < C; ++i) {
+    const uint32_t c = t + 64 * W * i;
+    if (c < chunks) {
+      float4* o = reinterpret_cast<float4*>(out + 8 * c);
+      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+    }
+  }
+}
+
+// dw[k] = sum of the parts, 16 waves taking each 16th one, then in wave order.
+__global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dw,
+                                                       uint32_t parts, uint32_t K) {
+  __shared__ float sum[16][64];
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, k = blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  for (uint32_t p = wave; p < parts; p += 16) s += part[(uint64_t)p * K + k];
+  sum[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += sum[w][lane];
+    dw[k] = s;
+  }
+}
+
+// Waves a row: the fewest whose lanes hold the row in `most` chunks.
+uint32_t row_waves(uint32_t K, uint32_t most) {
+  uint32_t w = 1;
+  while (w < kNormMaxWaves && K / 8 > 64 * w * most) w *= 2;
+  return w;
+}
+
+template <uint32_t W>
+hipError_t launch_norm_w(const NormArgs& a, uint32_t rows, hipStream_t s) {
+  const uint32_t C = (a.K / 8 + 64 * W - 1) / (64 * W);
+  const dim3 grid((a.M + rows - 1) / rows), block(64 * W * rows);
+  const size_t lds = (size_t)rows * (a.K / kGroup) * 4;
+  if (C <= 1) norm_quant_kernel<W, 1><<<grid, block, lds, s>>>(a);
+  else if (C <= 2) norm_quant_kernel<W, 2><<<grid, block, lds, s>>>(a);
+  else if (C <= 3) norm_quant_kernel<W, 3><<<grid, block, lds, s>>>(a);
+  else if (C <= 4) norm_quant_kernel<W, 4><<<grid, block, lds, s>>>(a);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+template <uint32_t W>
+hipError_t launch_norm_grad_w(const NormGradArgs& a, uint32_t grid, hipStream_t s) {
+  const uint32_t C = (a.K / 8 + 64 * W - 1) / (64 * W);
+  const dim3 block(64 * W);
+  if (C <= 1) norm_grad_kernel<W, 1><<<grid, block, 0, s>>>(a);
+  else if (C <= 2) norm_grad_kernel<W, 2><<<grid, block, 0, s>>>(a);
+  else if (C <= 3) norm_grad_kernel<W, 3><<<grid, block, 0, s>>>(a);
+  else if (C <= 4) norm_grad_kernel<W, 4><<<grid, block, 0, s>>>(a);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+constexpr uint32_t kNormGradParts = 256;
+
+}  // namespace
+
+hipError_t launch_norm_quant(const uint16_t* x, const uint16_t* r, const uint16_t* w, uint16_t* h, uint16_t* y,
+                             uint8_t* q, float* scale_rm, float* scale_km, float* rstd, float eps, uint32_t M,
+                             uint32_t K, hipStream_t s) {
+  const NormArgs a{reinterpret_cast<const u32x4*>(x), reinterpret_cast<const u32x4*>(r),
+                   reinterpret_cast<const u32x4*>(w), reinterpret_cast<u32x4*>(h), reinterpret_cast<u32x4*>(y),
+                   reinterpret_cast<u32x2*>(q), scale_rm, scale_km, rstd, eps, M, K, m_pad16(M)};
+  const uint32_t W = row_waves(K, 4);
+  switch (W) {
+    case 1: return launch_norm_w<1>(a, 8, s);
+    case 2: return launch_norm_w<2>(a, 4, s);
+    case 4: return launch_norm_w<4>(a, 2, s);
+    case 8: return launch_norm_w<8>(a, 1, s);
+    default: return launch_norm_w<16>(a, 1, s);
+  }
+}
+
+uint64_t norm_grad_workspace_bytes(uint32_t M, uint32_t K) {
+  return (uint64_t)std::min(M, kNormGradParts) * K * 4;
+}
+
+hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* w,
+                            const float* rstd, uint16_t* dx, float* dw, void* workspace, uint32_t M, uint32_t K,
+                            hipStream_t s) {
+  const NormGradArgs a{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(dh),
+                       reinterpret_cast<const u32x4*>(h), reinterpret_cast<const u32x4*>(w), rstd,
+                       reinterpret_cast<u32x4*>(dx), static_cast<float*>(workspace), M, K};
+  const uint32_t parts = std::min(M, kNormGradParts);
+  if (M > 0) {
+    hipError_t e;
+    switch (row_waves(K, 4)) {
+      case 1: e = launch_norm_grad_w<1>(a, parts, s); break;
+      case 2: e = launch_norm_grad_w<2>(a, parts, s); break;
+      case 4: e = launch_norm_grad_w<4>(a, parts, s); break;
+      case 8: e = launch_norm_grad_w<8>(a, parts, s); break;
+      default: e = launch_norm_grad_w<16>(a, parts, s); break;
+    }
+    if (e != hipSuccess) return e;
+  }
+  norm_dw_kernel<<<dim3(K / 64), dim3(1024), 0, s>>>(a.part, dw, parts, K);
+  return hipGetLastError();
+}
+
+}  // namespace fp8q
