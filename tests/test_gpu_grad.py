@@ -148,7 +148,8 @@ def test_dgrad_pad_slots_are_not_used():
 
 WGRAD = [(1, 128, 128), (16, 256, 128), (25, 128, 384), (127, 384, 256), (128, 128, 128), (129, 640, 256),
          (409, 2048, 1408), (511, 256, 384), (512, 128, 256), (513, 384, 128), (640, 256, 256), (1000, 1152, 640),
-         (1168, 128, 2048), (4576, 256, 256), (30, 2560, 2048), (4576, 512, 1024)]
+         (1168, 128, 2048), (4576, 256, 256), (30, 2560, 2048), (4576, 512, 1024), (1, 4096, 2048),
+         (129, 2816, 2944), (300, 2048, 4224), (640, 3968, 2048)]
 
 
 def _wgrad(y, x, M, N, K):

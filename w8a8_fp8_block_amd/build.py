@@ -12,7 +12,8 @@ Flags:
                                       it does not know the feature: harmless)
   -mllvm -amdgpu-mfma-vgpr-form       MFMA results in VGPRs: every GEMM partial
                                       product is consumed by VALU fmas, which
-                                      cannot read AGPRs
+                                      cannot read AGPRs (not for the sources in
+                                      AGPR_SOURCES: 256 accumulators a lane)
   -fgpu-flush-denormals-to-zero is NOT given: the quantizer relies on IEEE
   subnormal fp32 arithmetic (the default).
 """
@@ -30,17 +31,24 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libfp8q.so")
 SOURCES = ["fp8q_api.hip", "quant.hip", "relayout.hip", "gemm.hip", "gemm_bf16.hip", "dequant.hip",
            "ffn.hip", "route.hip", "grouped.hip", "lora.hip",
-           "norm.hip", "quant_dual.hip", "grad.hip", "balance.hip", "clock.hip"]
+           "norm.hip", "quant_dual.hip", "dgrad.hip", "wgrad.hip", "balance.hip", "clock.hip"]
+AGPR_SOURCES = {"wgrad.hip"}
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 JOBS = 8
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wall", "-Wno-unused-function", "-Wno-unknown-pragmas",
     "-I", os.path.join(ROOT, "include"),
 ]
+
+
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+
+
+def _flags(source: str):
+    return FLAGS if source in AGPR_SOURCES else FLAGS + VGPR_FORM
 
 
 def _run(cmd, verbose: bool):
@@ -59,7 +67,7 @@ def build(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp"
     with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(JOBS) as pool:
         out = [os.path.join(objs, s + ".o") for s in SOURCES]
-        list(pool.map(lambda so: _run([HIPCC, *FLAGS, "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+        list(pool.map(lambda so: _run([HIPCC, *_flags(so[0]), "-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
                       zip(SOURCES, out)))
         _run([HIPCC, "--offload-arch=gfx950", "-shared", *out, "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)

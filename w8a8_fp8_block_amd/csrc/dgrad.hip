@@ -1,13 +1,11 @@
-// The gradients of the block-scaled projection on gfx950.
+// The gradient of the block-scaled projection's input on gfx950:
 //
-//   dx[m,k] = sum_n dy[m,n] * w[n,k]   (launch_gemm_dgrad)
-//   dw[n,k] = sum_m dy[m,n] * x[m,k]   (launch_gemm_wgrad, gemm_wgrad.h)
+//   dx[m,k] = sum_n dy[m,n] * w[n,k]
 //
-// The activations' gradient is the forward GEMM's main loop (gemm_tile.h,
+// It is the forward GEMM's main loop (gemm_tile.h,
 // gemm_pp.h) over the weights in their forward layout: the sum's index n runs
 // along w's rows, and the weight fragments come through the transposing LDS read.
 #include "gemm_pp.h"
-#include "gemm_wgrad.h"
 #include "launch.h"
 
 namespace fp8q {
@@ -40,32 +38,6 @@ hipError_t launch_dgrad_tiled(const uint8_t* dy, const float* dys, const uint8_t
   return hipGetLastError();
 }
 
-using Wgrad128 = WgradCfg<128, 128, 2, 2, 2>;
-
-template <bool SPLIT>
-__global__ __launch_bounds__(256, 2) void wgrad_tiled_kernel(WgradArgs a) {
-  uint32_t ti, tj, split = 0;
-  if constexpr (SPLIT)
-    tile_split_coords(a.tiles_n, a.tiles_k, a.splits, ti, tj, split);
-  else
-    tile_coords(a.tiles_n, a.tiles_k, ti, tj);
-  const uint32_t blocks = (a.M + 127) / 128;
-  const uint32_t b0 = SPLIT ? split * blocks / a.splits : 0;
-  const uint32_t G = SPLIT ? (split + 1) * blocks / a.splits - b0 : blocks;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  gemm_wgrad_body<Wgrad128, SPLIT>(a, ti * 128, tj * 128, b0, G, wave >> 1, wave & 1, split);
-}
-
-template <bool SPLIT>
-hipError_t launch_wgrad_128(WgradArgs a, hipStream_t s) {
-  const hipError_t e = allow_lds<&wgrad_tiled_kernel<SPLIT>, Wgrad128::LDS_BYTES>();
-  if (e != hipSuccess) return e;
-  a.tiles_n = a.N / 128;
-  a.tiles_k = a.K / 128;
-  wgrad_tiled_kernel<SPLIT><<<dim3(a.tiles_n * a.tiles_k * a.splits), dim3(Wgrad128::NT), Wgrad128::LDS_BYTES, s>>>(a);
-  return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_gemm_dgrad(const uint8_t* dy, const float* dy_s_km, const uint8_t* w, const float* w_s, uint16_t* dx,
@@ -75,17 +47,6 @@ hipError_t launch_gemm_dgrad(const uint8_t* dy, const float* dy_s_km, const uint
     return e != hipSuccess ? e : launch_splitk_reduce(part, dx, M, K, splits, s);
   }
   return launch_dgrad_tiled<2, false>(dy, dy_s_km, w, w_s, dx, nullptr, M, N, K, 1, s);
-}
-
-hipError_t launch_gemm_wgrad(const uint8_t* dy, const uint8_t* ey, const uint8_t* x, const uint8_t* ex, uint16_t* dw,
-                             float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, hipStream_t s) {
-  const WgradArgs a{dy, x, reinterpret_cast<const uint32_t*>(ey), reinterpret_cast<const uint32_t*>(ex), dw, part,
-                    M,  N, K, 0, 0, splits};
-  if (splits >= 2) {
-    const hipError_t e = launch_wgrad_128<true>(a, s);
-    return e != hipSuccess ? e : launch_splitk_reduce(part, dw, N, K, splits, s);
-  }
-  return launch_wgrad_128<false>(a, s);
 }
 
 }  // namespace fp8q

@@ -1080,13 +1080,13 @@ fp8q_status fp8q_gemm_wgrad(const uint8_t* dy_tok, const uint8_t* dy_exp, const 
     REQUIRE_PTR(x_tok);
     REQUIRE_PTR(x_exp);
   }
-  const uint32_t splits = wgrad_splits(M, N, K, current_cus());
+  const uint32_t cus = current_cus(), splits = wgrad_splits(M, N, K, cus);
   st = check_workspace(fn, workspace, workspace_bytes, splitk_workspace(N, K, splits));
   if (st != FP8Q_OK) return st;
   st = check_device(fn);
   if (st != FP8Q_OK) return st;
   return launched(fn, launch_gemm_wgrad(dy_tok, dy_exp, x_tok, x_exp, dw_bf16, static_cast<float*>(workspace), M, N,
-                                        K, splits, stream));
+                                        K, splits, cus, stream));
 }
 
 size_t fp8q_gemm_wgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K) {

@@ -219,13 +219,14 @@ hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16
 // exponent bytes [ceil(M/512), K, 4] (quant_dual.hip).
 hipError_t launch_quant_dual(const uint16_t* x, uint8_t* q, float* scale_km, uint8_t* q_tok, uint8_t* exp_tok,
                              uint32_t M, uint32_t K, hipStream_t s);
-// Gradients of the block-scaled product (grad.hip): dx [M,K] from row codes dy
+// Gradients of the block-scaled product (dgrad.hip, wgrad.hip): dx [M,K] from row codes dy
 // [M,N] and w [N,K]; dw [N,K] from token codes dy [M,N] and x [M,K].  splits >= 2:
 // the sum cut into as many ranges, their fp32 results in part.
 hipError_t launch_gemm_dgrad(const uint8_t* dy, const float* dy_s_km, const uint8_t* w, const float* w_s, uint16_t* dx,
                              float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, hipStream_t s);
 hipError_t launch_gemm_wgrad(const uint8_t* dy, const uint8_t* ey, const uint8_t* x, const uint8_t* ex, uint16_t* dw,
-                             float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, hipStream_t s);
+                             float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, uint32_t cus,
+                             hipStream_t s);
 // Balance loss of a router and the gradient of its logits (balance.hip).
 uint64_t balance_workspace_bytes(uint32_t T, uint32_t E);
 hipError_t launch_balance(const void* logits, bool bf16, const int32_t* ids, int32_t* counts, float* prob, float* loss,

@@ -7,14 +7,36 @@
 // The sum runs along the rows of both matrices, so their fragments come through
 // the transposing LDS read (mfma_common.h) and no transposed copy exists.  The
 // scales are the matrix instruction's own operands, a byte a lane: the partial
-// products need no fp32 multiply of their own and accumulate in the instruction's
-// accumulators (measured as exact as scaled fp32 additions: 1.5e-5 of the
-// result's norm over 4608 tokens either way, the instruction's own rounding of a
-// 128-deep sum).
+// products need no fp32 multiply of their own and add up in the instruction's
+// accumulators (as exact as scaled fp32 additions: 1.5e-5 of the result's norm over
+// 4608 tokens either way, the instruction's own rounding of its sum).
 //
-// Workgroup tile BM (columns n of dy) x BN (columns k of x), panels of 128 columns
-// x 128 tokens in LDS, a ring of STAGES.  Tokens past M lie past the buffer
-// resources' ends and load as zeros.
+// Pipeline.  A workgroup of four waves computes a tile of BM = 64 TM columns of dy
+// by BN = 64 TN columns of x, its waves in a 2 x 2 grid.  The tokens pass in halves
+// of a block, 64 at a time, through a ring of SLOTS LDS slots filled by direct loads:
+// [panel of 128 columns][64 tokens][128 bytes], then the columns' scale dwords.  Of
+// each half a wave holds its TM + TN fragments in registers, read while the products
+// of the half before it run: one set of fragments per parity, one barrier a half.
+// The reads, the direct loads and the barrier lie between matrix instructions, each
+// in the shadow of one (64 cycles); left in a row at the start of a half, the loads
+// alone cost 10%.
+//
+// LDS bounds the tile: a wave of 64 x 64 reads 8 KB for 256 cycles of matrix
+// instructions, 32 bytes a cycle, and four SIMDs of them the 128 that LDS delivers,
+// with the direct loads' writes to come; at 128 x 128 it is half of that.  That
+// takes 256 accumulators a lane, so one wave a SIMD, which issues instructions of all
+// kinds by itself.  (Two waves of 128 x 64 a SIMD: 2634 TFLOP/s over 4096 x 4096 x
+// 18304 tokens against 2800; the same two taking turns between reading and computing:
+// 2546.  hipBLASLt's FP8 product with one scale for all, 8192^3: 2642.)
+//
+// The direct loads are issued in assembly: the compiler takes a transposing read
+// for one of any LDS in flight and waits for every load before it, which costs half
+// the speed.  Waits are counted here instead; the loads have no result registers.
+//
+// Fragments of 32 columns x 64 tokens: lane l holds column l % 32, tokens
+// 32 (l / 32) ..; the transposing read takes chunk 2 t + (l / 16) % 2 of the panel for
+// the 16 lanes of l's row.  Tokens past M lie past the buffer resources' ends and
+// load as zeros.
 #pragma once
 
 #include "mfma_common.h"
@@ -22,138 +44,269 @@
 namespace fp8q {
 namespace {
 
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
+
 struct WgradArgs {
   const uint8_t *dy, *x;     // codes [M,N], [M,K]
   const uint32_t *ey, *ex;   // [ceil(M/512)][N], [K]: four token blocks' bytes a dword
   uint16_t* out;             // [N,K] bf16
-  float* part;               // SPLIT: [splits][N][K]
+  float* part;               // split form: [splits][N][K]
   uint32_t M, N, K, tiles_n, tiles_k, splits;
 };
 
-template <int BM, int BN, int WGM, int WGN, int STAGES_>
-struct WgradCfg {
-  static constexpr int STAGES = STAGES_;
-  static constexpr int NW = WGM * WGN, NT = 64 * NW;
-  static constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
-  static constexpr int PANEL = 128 * 128;
-  static constexpr int DY_BYTES = BM / 128 * PANEL, X_BYTES = BN / 128 * PANEL;
-  static constexpr int SC_M = (WM + 63) / 64, SC_N = (WN + 63) / 64;  // scale loads a wave
-  static constexpr int SCW_BYTES = (SC_M + SC_N) * 256;
-  static constexpr int STAGE_BYTES = DY_BYTES + X_BYTES + NW * SCW_BYTES;
-  static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
-  static constexpr int CH = (DY_BYTES + X_BYTES) / 1024 / NW;  // 1 KB loads a wave
-  static constexpr int LOADS = CH + SC_M + SC_N;
-  static_assert(WM % 64 == 0 && WN % 64 == 0 && BM % 128 == 0 && BN % 128 == 0, "tile");
-  static_assert((DY_BYTES + X_BYTES) / 1024 % NW == 0 && LDS_BYTES <= 160 * 1024, "loads, LDS");
-  static_assert((STAGES - 1) * LOADS < 64, "vmcnt range");
-};
-
-__device__ __forceinline__ v4f mfma_e4m3_128_scaled(const v8i& a, const v8i& b, const v4f& c, uint32_t ea, uint32_t eb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, (int)ea, 0, (int)eb);
+// Raw buffer resource words (as make_rsrc) for the loads in assembly.
+__device__ __forceinline__ u32x4s rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return u32x4s{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+// Lanes copy 16 or 4 bytes each from base + voff + soff + OFF to lds + LDS_OFF onwards (the
+// instruction adds its offset on both sides; M0 holds no other value in the kernels that
+// use these).
+template <int OFF, int LDS_OFF>
+__device__ __forceinline__ void dma16_asm(u32x4s r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen offset:%5 lds"
+               :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(LDS_OFF - OFF), "n"(OFF) : "memory", "scc");
+}
+template <int LDS_OFF>
+__device__ __forceinline__ void dma4_asm(u32x4s r, uint32_t voff, uint32_t soff, uint32_t lds) {
+  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(LDS_OFF) : "memory", "scc");
 }
 
-// The tile n0.., k0.. over the token blocks b0 .. b0 + G - 1.
-template <class C, bool SPLIT>
-__device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t n0, uint32_t k0, uint32_t b0, uint32_t G,
-                                                uint32_t wm, uint32_t wn, uint32_t split) {
-  constexpr int TM = C::TM, TN = C::TN, STAGES = C::STAGES;
+template <int TM_, int TN_>
+struct WgradCfg {
+  static constexpr int TM = TM_, TN = TN_, SLOTS = 4;
+  static constexpr int BM = 64 * TM, BN = 64 * TN;  // 2 x 2 waves of TM x TN 32 x 32 tiles
+  static constexpr int PY = BM / 128, PX = BN / 128, PANELS = (BM + BN) / 128, PANEL = 64 * 128;
+  static constexpr int SC = PANELS * PANEL;  // the scales' place in a slot: 512 bytes a panel
+  static constexpr int SLOT_BYTES = SC + PANELS * 512, LDS_BYTES = SLOTS * SLOT_BYTES;
+  // loads of a wave and half: two 1 KB chunks (8 rows) of each panel, and 256 bytes of
+  // each operand's scales (with one panel two waves load the same)
+  static constexpr int CH = 2 * PANELS, LOADS = CH + 2;
+  static constexpr int OPS = 3 * (TM + TN);          // LDS reads of a half: fragment halves, scales
+  // where in the half's TM * TN products the barrier and the reads lie, and how far behind
+  // the barrier the loads begin
+  static constexpr int BAR = TM * TN >= 8 ? 1 : 0, READS_END = TM * TN - (TM * TN >= 8 ? 3 : 0);
+  static constexpr int LOADS_FROM = TM * TN >= 16 ? 2 : 0;
+  static_assert(BM % 128 == 0 && BN % 128 == 0 && LDS_BYTES <= 160 * 1024, "tile");
+  static_assert((SLOTS - 1) * LOADS < 64, "vmcnt range");
+};
+
+// Quads of halves (two token blocks; one round of the ring) that `blocks` blocks take.
+__device__ __forceinline__ uint32_t wgrad_quads(uint32_t blocks) { return (blocks + 1) / 2; }
+
+// The tiles next(u) -> (n0, k0), u = 0 .. units - 1, one after the other, each over the
+// tokens m0 .. m1 - 1 (m0 a multiple of 128, m0 < m1, units > 0).  The ring runs on from
+// one tile into the next, so a tile's stores lie over the next one's loads.
+template <class C, bool SPLIT, class Next>
+__device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t units, uint32_t m0, uint32_t m1,
+                                                uint32_t split, const Next& next) {
+  constexpr int TM = C::TM, TN = C::TN, SLOTS = C::SLOTS;
+  static_assert(SLOTS == 4, "a quad of halves is one round of the ring");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  const uint32_t tid = threadIdx.x, lane = tid & 63;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const uint32_t M = a.M, N = a.N, K = a.K, packs = (M + 511) / 512;
-  const __amdgpu_buffer_rsrc_t rY = make_rsrc(a.dy, M * N), rX = make_rsrc(a.x, M * K);
-  const __amdgpu_buffer_rsrc_t rEy = make_rsrc(a.ey, packs * N * 4), rEx = make_rsrc(a.ex, packs * K * 4);
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t wm = wave >> 1, wn = wave & 1;
+  const uint32_t N = a.N, K = a.K, packs = (a.M + 511) / 512;
+  const uint32_t Q = wgrad_quads((m1 - m0 + 127) / 128), h_end = (m1 + 63) / 64;
 
-  // 1 KB chunk ch of a stage: 8 token rows of panel ch / 16 (dy's panels first)
-  uint32_t off[C::CH], step[C::CH];
-  bool is_y[C::CH];
+  // ---- loads: a quad ahead of the products ----
+  // Wave w's chunks of a panel hold its rows 16 w + 8 j ..; row r's 16-byte chunk p lies
+  // at p ^ swz_t(r).  The resources start at the tile's first column.
+  const uint32_t lrow = lane >> 3, lcol = ((lane & 7) ^ lrow ^ (wave >> 1)) * 16;
+  const uint32_t y_off[2] = {(16 * wave + lrow) * N + lcol, (16 * wave + lrow + 8) * N + lcol};
+  const uint32_t x_off[2] = {(16 * wave + lrow) * K + lcol, (16 * wave + lrow + 8) * K + lcol};
+  const uint32_t sc_y = wave % (2 * C::PY) * 256, sc_x = wave % (2 * C::PX) * 256;
+  const uint32_t ey_off = sc_y + lane * 4, ex_off = sc_x + lane * 4;
+  const uint32_t lds_w = lds_addr(smem) + wave * 2048;
+  const uint32_t lds_ey = lds_addr(smem) + C::SC + sc_y, lds_ex = lds_addr(smem) + C::SC + C::PY * 512 + sc_x;
+  u32x4s rY, rX, rEy, rEx;
+  uint32_t lh = m0 / 64;  // the quad's first half
+  auto aim_tile = [&](bool some, uint32_t n0, uint32_t k0) {
+    rY = rsrc_words(a.dy + n0, some ? m1 * N - n0 : 0);
+    rX = rsrc_words(a.x + k0, some ? m1 * K - k0 : 0);
+    rEy = rsrc_words(a.ey + n0, some ? (packs * N - n0) * 4 : 0);
+    rEx = rsrc_words(a.ex + k0, some ? (packs * K - k0) * 4 : 0);
+  };
+  // Load J of the quad's half S.  Past the last token (or tile) the base is the bound, which
+  // leaves nothing before it: zeros, no traffic.  (A base past the bound would leave
+  // everything: the bound less the base is what offsets are held against.)
+  auto load_op = [&](auto sc, auto jc) {
+    constexpr uint32_t S = decltype(sc)::value, J = decltype(jc)::value, P = J / 2;
+    constexpr int SLOT = S * C::SLOT_BYTES;
+    if constexpr (J < 2u * C::PY)
+      dma16_asm<P * 128, SLOT + P * C::PANEL + J % 2 * 1024>(
+          rY, y_off[J % 2], min(min(lh + S, h_end) * 64 * N, rY[2]), lds_w);
+    else if constexpr (J < (uint32_t)C::CH)
+      dma16_asm<(P - C::PY) * 128, SLOT + P * C::PANEL + J % 2 * 1024>(
+          rX, x_off[J % 2], min(min(lh + S, h_end) * 64 * K, rX[2]), lds_w);
+    else if constexpr (J == (uint32_t)C::CH)
+      dma4_asm<SLOT>(rEy, ey_off, min(((lh + S) >> 3) * N * 4, rEy[2]), lds_ey);
+    else
+      dma4_asm<SLOT>(rEx, ex_off, min(((lh + S) >> 3) * K * 4, rEx[2]), lds_ex);
+  };
+
+  // ---- fragments ----
+  const uint32_t l32 = lane & 31, row = 32 * (lane >> 5) + ((lane & 15) >> 1);
+  const uint32_t lt = row * 128 + (swz_t(row) ^ ((lane >> 4) & 1)) * 16 + (lane & 1) * 8;
+  const uint32_t sy = C::SC + (wm * 32 * TM + l32) * 4, sx = C::SC + C::PY * 512 + (wn * 32 * TN + l32) * 4;
+  uint32_t ly[TM], lx[TN];
 #pragma unroll
-  for (int j = 0; j < C::CH; ++j) {
-    const uint32_t ch = wave * C::CH + j, panel = ch / 16, row = (ch % 16) * 8 + (lane >> 3);
-    is_y[j] = panel < (uint32_t)(C::DY_BYTES / C::PANEL);
-    const uint32_t ld = is_y[j] ? N : K;
-    const uint32_t col = is_y[j] ? n0 + panel * 128 : k0 + (panel - C::DY_BYTES / C::PANEL) * 128;
-    off[j] = row * ld + col + ((lane & 7) ^ swz_t(row)) * 16;
-    step[j] = 128 * ld;
+  for (int t = 0; t < TM; ++t) {
+    const uint32_t col = wm * 32 * TM + t * 32;
+    ly[t] = col / 128 * C::PANEL + (lt ^ (col % 128));
   }
-  const uint32_t sc = C::DY_BYTES + C::X_BYTES + wave * C::SCW_BYTES;
-  const uint32_t band_n = n0 + wm * C::WM, band_k = k0 + wn * C::WN;
-  auto issue = [&](uint32_t b, uint32_t slot) {
-    uint8_t* base = smem + slot * C::STAGE_BYTES;
 #pragma unroll
-    for (int j = 0; j < C::CH; ++j) dma16(is_y[j] ? rY : rX, off[j], b * step[j], base + (wave * C::CH + j) * 1024);
-#pragma unroll
-    for (int j = 0; j < C::SC_M; ++j) dma4(rEy, (band_n + j * 64 + lane) * 4, (b >> 2) * N * 4, base + sc + j * 256);
-#pragma unroll
-    for (int j = 0; j < C::SC_N; ++j)
-      dma4(rEx, (band_k + j * 64 + lane) * 4, (b >> 2) * K * 4, base + sc + (C::SC_M + j) * 256);
+  for (int t = 0; t < TN; ++t) {
+    const uint32_t col = wn * 32 * TN + t * 32;
+    lx[t] = (C::PY + col / 128) * C::PANEL + (lt ^ (col % 128));
+  }
+  v8i fy[2][TM], fx[2][TN];
+  uint32_t ey[2][TM], ex[2][TN];
+  auto read_op = [&](const uint8_t* base, auto set_c, auto q_c) {
+    constexpr int S = decltype(set_c)::value, O = decltype(q_c)::value;
+    if constexpr (O < 2 * TN) {
+      if constexpr (O & 1) fx[S][O / 2].hi = ld_transposed(base + lx[O / 2], 1);
+      else fx[S][O / 2].lo = ld_transposed(base + lx[O / 2], 0);
+    } else if constexpr (O < 2 * TN + 2 * TM) {
+      constexpr int P = O - 2 * TN;
+      if constexpr (P & 1) fy[S][P / 2].hi = ld_transposed(base + ly[P / 2], 1);
+      else fy[S][P / 2].lo = ld_transposed(base + ly[P / 2], 0);
+    } else if constexpr (O < 2 * TN + 3 * TM) {
+      constexpr int P = O - 2 * TN - 2 * TM;
+      ey[S][P] = *reinterpret_cast<const uint32_t*>(base + sy + P * 128);
+    } else {
+      constexpr int P = O - 2 * TN - 3 * TM;
+      ex[S][P] = *reinterpret_cast<const uint32_t*>(base + sx + P * 128);
+    }
   };
 
-  const uint32_t l16 = lane & 15, lt = transposed_lane(lane);
-  // fragment of the 16 columns col.. (of the operand's panels at `panels`)
-  auto frag = [&](const uint8_t* panels, uint32_t col) -> v8i {
-    const uint8_t* p = panels + col / 128 * C::PANEL + (lt ^ (col % 128));
-    v8i f;
-    f.lo = ld_transposed(p, 0);
-    f.hi = ld_transposed(p, 1);
-    return f;
-  };
-
-  v4f acc[TM][TN];
+  v16f acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  if (G > 0) {
-    const uint32_t last = b0 + G - 1;
+  uint32_t n0, k0;
+  next(0, n0, k0);
+  aim_tile(true, n0, k0);
+  unroll_seq(
+      [&](auto s) { unroll_seq([&](auto j) { load_op(s, j); }, std::make_integer_sequence<int, C::LOADS>{}); },
+      std::make_integer_sequence<int, SLOTS>{});
+  wait_vmcnt<(SLOTS - 1) * C::LOADS>();
+  wg_barrier();
+  unroll_seq([&](auto q) { read_op(smem, std::integral_constant<int, 0>{}, q); },
+             std::make_integer_sequence<int, C::OPS>{});
+
+  // Products of the quad's half S, whose fragments are in set S % 2; the next half's
+  // fragments into the other set, half S of the next quad into the slot.
+  uint32_t sh0 = 0;  // the place of the quad's first scale byte
+  auto step = [&](auto sc) {
+    constexpr int S = decltype(sc)::value, F = S & 1;
+    const uint8_t* nx = smem + (S + 1) % SLOTS * C::SLOT_BYTES;
+    const uint32_t sh = (sh0 + S / 2 * 8) & 31;
+    wait_lgkm0();  // this half's fragments are in registers
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) issue(min(b0 + s, last), s);
-    for (uint32_t i = 0; i < G; ++i) {
-      const uint32_t slot = i % STAGES;
-      const uint8_t* base = smem + slot * C::STAGE_BYTES;
-      wait_vmcnt<(STAGES - 1) * C::LOADS>();
-      wg_barrier();
-      v8i fy[TM], fx[TN];
-      uint32_t ey[TM], ex[TN];
-      const uint32_t sh = 8 * ((b0 + i) & 3);
+    for (int t = 0; t < TM; ++t) ey[F][t] >>= sh;
 #pragma unroll
-      for (int t = 0; t < TM; ++t) {
-        fy[t] = frag(base, wm * C::WM + t * 16);
-        ey[t] = *reinterpret_cast<const uint32_t*>(base + sc + (t * 16 + l16) * 4) >> sh;
+    for (int t = 0; t < TN; ++t) ex[F][t] >>= sh;
+    sched_fence();
+    unroll_seq(
+        [&](auto ic) {
+          constexpr int I = decltype(ic)::value, P = TM * TN;
+          if constexpr (I == C::BAR) {
+            // the next half has landed (two more halves' loads are younger, and a tile's
+            // stores, which only make the wait longer); every wave has read this half's slot
+            wait_vmcnt<(SLOTS - 2) * C::LOADS>();
+            sched_fence();
+            wg_barrier();
+            sched_fence();
+          }
+          acc[I / TN][I % TN] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              fx[F][I % TN], fy[F][I / TN], acc[I / TN][I % TN], 0, 0, 0, (int)ex[F][I % TN], 0, (int)ey[F][I / TN]);
+          if constexpr (I >= C::BAR) {
+            constexpr int R = I - C::BAR, RN = C::READS_END - C::BAR;
+            if constexpr (R < RN) {
+              constexpr int O0 = R * C::OPS / RN, O1 = (R + 1) * C::OPS / RN;
+              unroll_seq([&](auto q) { read_op(nx, std::integral_constant<int, 1 - F>{},
+                                               std::integral_constant<int, O0 + decltype(q)::value>{}); },
+                         std::make_integer_sequence<int, O1 - O0>{});
+            }
+            constexpr int L = R - C::LOADS_FROM, LN = P - C::BAR - C::LOADS_FROM;
+            if constexpr (L >= 0) {
+              constexpr int J0 = L * C::LOADS / LN, J1 = (L + 1) * C::LOADS / LN;
+              unroll_seq([&](auto j) { load_op(sc, std::integral_constant<int, J0 + decltype(j)::value>{}); },
+                         std::make_integer_sequence<int, J1 - J0>{});
+            }
+          }
+          sched_fence();
+        },
+        std::make_integer_sequence<int, TM * TN>{});
+  };
+#pragma unroll 1
+  for (uint32_t u = 0;;) {
+    // The loads' aim changes between quads only: a branch among a quad's products, and the
+    // compiler moves them behind it.
+    uint32_t nn0 = 0, nk0 = 0;
+#pragma unroll 1
+    for (uint32_t q = 0; q < Q; ++q) {
+      sh0 = (8 * (m0 / 128) + 16 * q) & 31;
+      if (q + 1 < Q) {
+        lh += 4;
+      } else {
+        lh = m0 / 64;
+        if (u + 1 < units) next(u + 1, nn0, nk0);
+        aim_tile(u + 1 < units, nn0, nk0);
       }
-#pragma unroll
-      for (int t = 0; t < TN; ++t) {
-        fx[t] = frag(base + C::DY_BYTES, wn * C::WN + t * 16);
-        ex[t] = *reinterpret_cast<const uint32_t*>(base + sc + C::SC_M * 256 + (t * 16 + l16) * 4) >> sh;
-      }
-      wait_lgkm0();
-      wg_barrier();  // every wave has read the slot
-      issue(min(b0 + i + STAGES, last), slot);
-#pragma unroll
-      for (int i2 = 0; i2 < TM; ++i2)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i2][j] = mfma_e4m3_128_scaled(fx[j], fy[i2], acc[i2][j], ex[j], ey[i2]);
+      unroll_seq([&](auto s) { step(s); }, std::make_integer_sequence<int, SLOTS>{});
     }
-    wait_vmcnt<0>();  // no direct load may still be writing LDS when the workgroup ends
-  }
-  // lane: row n = band + 16 i + l16, columns k = band + 16 j + 4 (lane / 16) ..
+    // N and K are multiples of 128: a wave's share lies inside whole or not at all
+    // (its stores go nowhere then)
+    const bool inside = n0 + wm * 32 * TM < N && k0 + wn * 32 * TN < K;
+    sched_fence();
+    // lane: row n = 32 i + l32, columns k = 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4; a row
+    // group's place is uniform, the lane's within it below 2^32 bytes
+    const uint32_t at = l32 * K * (SPLIT ? 4 : 2) + 16 * (lane >> 5);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const uint32_t n = band_n + i * 16 + l16;
-    if (n < N) {
+    for (int i = 0; i < TM; ++i) {
+      const uint64_t band = (uint64_t)(n0 + wm * 32 * TM + 32 * i) * K + (k0 + wn * 32 * TN);
+      const __amdgpu_buffer_rsrc_t rO = make_rsrc(a.out + band, inside ? 0xFFFFFFFFu : 0);
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        const uint32_t k = band_k + j * 16 + 4 * (lane >> 4);
-        if (k < K) {
-          if constexpr (SPLIT)
-            *reinterpret_cast<v4f*>(a.part + ((uint64_t)split * N + n) * K + k) = acc[i][j];
-          else
-            *reinterpret_cast<uint2*>(a.out + (uint64_t)n * K + k) = pack_bf16x4(acc[i][j]);
+        v16f& c = acc[i][j];
+        if constexpr (SPLIT) {
+          uint8_t* p = reinterpret_cast<uint8_t*>(a.part + (uint64_t)split * N * K + band + 32 * j);
+#pragma unroll
+          for (int r = 0; r < 16; r += 4)
+            *reinterpret_cast<v4f*>(p + 8 * r + at) = v4f{c[r], c[r + 1], c[r + 2], c[r + 3]};
+        } else {
+          // 8 columns a lane: the halves of the wave swap every other four
+#pragma unroll
+          for (int r = 0; r < 16; r += 8) {
+            const uint2 lo = pack_bf16x4(v4f{c[r], c[r + 1], c[r + 2], c[r + 3]});
+            const uint2 hi = pack_bf16x4(v4f{c[r + 4], c[r + 5], c[r + 6], c[r + 7]});
+            const auto s0 = __builtin_amdgcn_permlane32_swap(lo.x, hi.x, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(lo.y, hi.y, false, false);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, rO, at, 64 * j + 4 * r, 0);
+          }
         }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) c[r] = 0.0f;
+        sched_fence();  // one tile's accumulators out at a time
       }
     }
+    if (++u == units) break;
+    n0 = nn0;
+    k0 = nk0;
   }
+  // no direct load may still be writing LDS when the workgroup ends, or another
+  // body's loads begin
+  wait_vmcnt<0>();
+  wait_lgkm0();
+  wg_barrier();
 }
 
 }  // namespace
