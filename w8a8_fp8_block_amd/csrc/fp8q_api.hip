@@ -261,9 +261,7 @@ constexpr uint64_t kFusedKmajorMaxGroups = 1u << 19;
 constexpr uint32_t kTailRuleMinM = 512;  // the stream-K form from here
 constexpr uint32_t kRoundRuleMinM = 129;
 
-int gemm_auto_kernel(uint32_t M, uint32_t N, uint32_t cus) {
-  if (M <= kSkinnyAutoMaxM || (M <= kSkinnyWideMaxM && N <= kSkinnyWideMaxN)) return 2;
-  if (M < kRoundRuleMinM) return 1;
+int rounds_kernel(uint32_t M, uint32_t N, uint32_t cus) {
   const uint64_t c = cus ? cus : 1;
   const uint64_t nt = N / kGroup;
   const uint64_t t_pp = (M + 255) / 256 * nt, t_128 = (M + 127) / 128 * nt;
@@ -272,6 +270,12 @@ int gemm_auto_kernel(uint32_t M, uint32_t N, uint32_t cus) {
   const uint64_t tail = t_128 % (2 * c);
   const uint64_t c_128 = 2 * (t_128 / (2 * c)) + (tail == 0 ? 0 : tail > c ? 2 : 1);
   return c_pp <= c_128 ? 5 : 1;
+}
+
+int gemm_auto_kernel(uint32_t M, uint32_t N, uint32_t cus) {
+  if (M <= kSkinnyAutoMaxM || (M <= kSkinnyWideMaxM && N <= kSkinnyWideMaxN)) return 2;
+  if (M < kRoundRuleMinM) return 1;
+  return rounds_kernel(M, N, cus);
 }
 
 // Split-K (fp8q_gemm_blockscaled_splitk).  Above kSplitMinM rows, wherever
@@ -630,11 +634,37 @@ fp8q_status check_grad(const char* fn, uint32_t M, uint32_t N, uint32_t K) {
               fn, M, N, K);
 }
 
+// Ranges of the sum (N) that fp8q_gemm_dgrad cuts: as many as fill two workgroups a CU
+// with 128 x 128 tiles, of 10 blocks at least (or 2, for up to 4 ranges) and 12 at most,
+// where the blocks saved, 0.7 us each, outweigh the second launch and the ranges' sums,
+// written and read at 4 TB/s.  Back to back over rotating inputs (256 CUs), us without ->
+// with: N = 17408, K = 5120: 138 -> 26 at M = 16, 144 -> 38 at 128, 137 -> 68 at 409; N =
+// 5120, K = 6144: 31 -> 14 at 16, 35 -> 19 at 128, 37 -> 35 at 409, 39 either way at 640;
+// N = 2048, K = 1408: 11.3 -> 7.8 at 16, 14.3 -> 14.1 at 409, 14.5 without at 640 (16.1
+// with); more ranges than fill the device were slower throughout.
+constexpr uint64_t kGradSplitMax = 12, kGradBlockNs = 700, kGradSplitNs = 2200, kGradBytesNs = 4000;
+
 uint32_t dgrad_splits(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
-  return 1;
+  const uint64_t tiles = (uint64_t)((M + 127) / 128) * (K / kGroup), blocks = N / kGroup;
+  if (tiles == 0) return 1;
+  const uint64_t cap = std::min(std::max(blocks / 10, std::min<uint64_t>(4, blocks / 2)), kGradSplitMax);
+  const uint64_t s = std::min<uint64_t>(2ull * cus / tiles, cap);
+  if (s < 2) return 1;
+  const uint64_t saved = kGradBlockNs * (blocks - blocks / s);
+  return saved > kGradSplitNs + s * M * K * 8 / kGradBytesNs ? (uint32_t)s : 1;
 }
+
+// Ranges of the tokens that fp8q_gemm_wgrad cuts: where 128 x 128 tiles are few, as many
+// as one a CU, of 12 blocks at least.  us without -> with, as above: 512 x 512: 17.6 -> 12.2
+// over 4576 tokens, 52 -> 17 over 16384; 1024 x 512: 17.6 -> 14.3, 51 -> 23; 1024 x 1024: 18.0
+// -> 16.9, 70 -> 35; 2048 x 1408 (176 tiles): 21.5 -> 28, 86 -> 81.
+constexpr uint32_t kWgradSplitTiles = 64, kWgradSplitBlocks = 12;
+
 uint32_t wgrad_splits(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
-  return 1;
+  const uint64_t tiles = (uint64_t)(N / kGroup) * (K / kGroup), blocks = ((uint64_t)M + 127) / 128;
+  if (tiles > kWgradSplitTiles) return 1;
+  const uint64_t s = std::min<uint64_t>(std::min<uint64_t>(cus / tiles, blocks / kWgradSplitBlocks), kSplitMaxUser);
+  return s < 2 ? 1 : (uint32_t)s;
 }
 
 // A router's logits [T,E] and choices [T,top_k].
@@ -1053,13 +1083,14 @@ fp8q_status fp8q_gemm_dgrad(const uint8_t* dy_e4m3, const float* dy_scale_km, co
   REQUIRE_PTR(w_e4m3);
   REQUIRE_PTR(w_scale);
   REQUIRE_PTR(dx_bf16);
-  const uint32_t splits = dgrad_splits(M, N, K, current_cus());
+  const uint32_t cus = current_cus(), splits = dgrad_splits(M, N, K, cus);
   st = check_workspace(fn, workspace, workspace_bytes, splitk_workspace(M, K, splits));
   if (st != FP8Q_OK) return st;
   st = check_device(fn);
   if (st != FP8Q_OK) return st;
   return launched(fn, launch_gemm_dgrad(dy_e4m3, dy_scale_km, w_e4m3, w_scale, dx_bf16,
-                                        static_cast<float*>(workspace), M, N, K, splits, stream));
+                                        static_cast<float*>(workspace), M, N, K, splits,
+                                        rounds_kernel(M, K, cus), cus, stream));
 }
 
 size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K) {

@@ -224,13 +224,13 @@ __device__ __forceinline__ void gemm_pp_body(
   const uint32_t G = K / kGroup;
   const uint32_t nb = n0 / kGroup;
 
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, rows.total * K);
-  const __amdgpu_buffer_rsrc_t rW = make_rsrc(W, N * K);
-  const __amdgpu_buffer_rsrc_t rS = make_rsrc(As, G * Mp * 4);
-  const __amdgpu_buffer_rsrc_t rWs = make_rsrc(Ws, ROW ? N * 4 : (N / kGroup) * G * 4);
+  const auto rA = rsrc_for<WT>(A, rows.total * K);
+  const auto rW = rsrc_for<WT>(W, N * K);
+  const auto rS = rsrc_for<WT>(As, G * Mp * 4);
+  const auto rWs = rsrc_for<WT>(Ws, ROW ? N * 4 : (N / kGroup) * G * 4);
   // FFN mode: the up weights and their scales
-  const __amdgpu_buffer_rsrc_t rW2 = FFN ? make_rsrc(ffn.w_up, N * K) : rW;
-  const __amdgpu_buffer_rsrc_t rWs2 = FFN ? make_rsrc(ffn.ws_up, (N / kGroup) * G * 4) : rWs;
+  const auto rW2 = FFN ? rsrc_for<WT>(ffn.w_up, N * K) : rW;
+  const auto rWs2 = FFN ? rsrc_for<WT>(ffn.ws_up, (N / kGroup) * G * 4) : rWs;
 
   // Operand chunks of this wave (LDS chunk c covers 8 rows of 128 bytes:
   // activations first, then weights; FFN mode: activations 0-15, gate

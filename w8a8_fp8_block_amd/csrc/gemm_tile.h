@@ -124,10 +124,10 @@ __device__ __forceinline__ void gemm_tiled_body(
   const uint32_t nb = (n0 + wn * C::WN) / kGroup;  // this wave's weight-scale block row
 
   // ---- buffer resources and per-lane source offsets (K block 0) ----
-  const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, rows.total * K);
-  const __amdgpu_buffer_rsrc_t rW = make_rsrc(W, N * K);
-  const __amdgpu_buffer_rsrc_t rS = make_rsrc(As, GK * Mp * 4);
-  const __amdgpu_buffer_rsrc_t rWs = make_rsrc(Ws, ROW ? N * 4 : (N / kGroup) * GK * 4);
+  const auto rA = rsrc_for<WT>(A, rows.total * K);
+  const auto rW = rsrc_for<WT>(W, N * K);
+  const auto rS = rsrc_for<WT>(As, GK * Mp * 4);
+  const auto rWs = rsrc_for<WT>(Ws, ROW ? N * 4 : (N / kGroup) * GK * 4);
   uint32_t a_off[C::DA], w_off[C::DW], s_off[C::SA];
 #pragma unroll
   for (int j = 0; j < C::DA; ++j) {

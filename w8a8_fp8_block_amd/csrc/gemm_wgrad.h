@@ -29,9 +29,8 @@
 // 18304 tokens against 2800; the same two taking turns between reading and computing:
 // 2546.  hipBLASLt's FP8 product with one scale for all, 8192^3: 2642.)
 //
-// The direct loads are issued in assembly: the compiler takes a transposing read
-// for one of any LDS in flight and waits for every load before it, which costs half
-// the speed.  Waits are counted here instead; the loads have no result registers.
+// The direct loads are issued in assembly (mfma_common.h says why: the waits that the
+// compiler would add cost half the speed).
 //
 // Fragments of 32 columns x 64 tokens: lane l holds column l % 32, tokens
 // 32 (l / 32) ..; the transposing read takes chunk 2 t + (l / 16) % 2 of the panel for
@@ -45,8 +44,6 @@ namespace fp8q {
 namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
-
 struct WgradArgs {
   const uint8_t *dy, *x;     // codes [M,N], [M,K]
   const uint32_t *ey, *ex;   // [ceil(M/512)][N], [K]: four token blocks' bytes a dword
@@ -55,11 +52,6 @@ struct WgradArgs {
   uint32_t M, N, K, tiles_n, tiles_k, splits;
 };
 
-// Raw buffer resource words (as make_rsrc) for the loads in assembly.
-__device__ __forceinline__ u32x4s rsrc_words(const void* base, uint32_t bytes) {
-  const uint64_t p = (uint64_t)base;
-  return u32x4s{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
-}
 // Lanes copy 16 or 4 bytes each from base + voff + soff + OFF to lds + LDS_OFF onwards (the
 // instruction adds its offset on both sides; M0 holds no other value in the kernels that
 // use these).

@@ -76,6 +76,35 @@ __device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t r, uint32_t voff,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(size_t)lds,
                                            4, voff, soff, 0, 0);
 }
+// The same in assembly, on a resource's words: for kernels that read LDS through
+// ld_transposed.  The compiler takes that read for one of any LDS in flight and would
+// wait for every direct load it knows of before it; these it does not know, and every
+// wait is the kernel's own.  (M0 holds no other value in those kernels.)
+typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4s rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t p = (uint64_t)base;
+  return u32x4s{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+__device__ __forceinline__ void dma16(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(r), "s"(soff), "s"((uint32_t)(size_t)(__attribute__((address_space(3))) void*)lds) : "memory");
+}
+__device__ __forceinline__ void dma4(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(r), "s"(soff), "s"((uint32_t)(size_t)(__attribute__((address_space(3))) void*)lds) : "memory");
+}
+template <int AUX>
+__device__ __forceinline__ void dma16_aux(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
+  static_assert(AUX == 0, "default cache policy");
+  dma16(r, voff, soff, lds);
+}
+// a resource for either kind
+template <bool ASM>
+__device__ __forceinline__ auto rsrc_for(const void* base, uint32_t bytes) {
+  if constexpr (ASM) return rsrc_words(base, bytes);
+  else return make_rsrc(base, bytes);
+}
+
 // LDS byte address of a pointer into a __shared__ array
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)p;
