@@ -66,6 +66,21 @@ __device__ __forceinline__ void dma4_asm(u32x4s r, uint32_t voff, uint32_t soff,
                :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(LDS_OFF) : "memory", "scc");
 }
 
+// Two bf16 (round to nearest even, NaN kept) in one instruction.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
+// 16 bytes a lane to base + voff + OFF.  (In assembly for the uniform base: with an address
+// a lane, the tile's end spills, and each reload waits for the stores.  The data's
+// registers may be written two instructions later.)
+template <int OFF>
+__device__ __forceinline__ void store16_asm(uint64_t base, uint32_t voff, u32x4s v) {
+  asm volatile("global_store_dwordx4 %0, %1, %2 offset:%3\n\ts_nop 1" :: "v"(voff), "v"(v), "s"(base), "n"(OFF) : "memory");
+}
+
 template <int TM_, int TN_>
 struct WgradCfg {
   static constexpr int TM = TM_, TN = TN_, SLOTS = 4;
@@ -255,41 +270,50 @@ __device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t uni
       }
       unroll_seq([&](auto s) { step(s); }, std::make_integer_sequence<int, SLOTS>{});
     }
-    // N and K are multiples of 128: a wave's share lies inside whole or not at all
-    // (its stores go nowhere then)
+    // N and K are multiples of 128: a wave's share lies inside whole or not at all.  Lane:
+    // row n = 32 i + l32, columns k = 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4; a row
+    // group's place is uniform, the lane's within it below 2^32 bytes.
     const bool inside = n0 + wm * 32 * TM < N && k0 + wn * 32 * TN < K;
     sched_fence();
-    // lane: row n = 32 i + l32, columns k = 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4; a row
-    // group's place is uniform, the lane's within it below 2^32 bytes
     const uint32_t at = l32 * K * (SPLIT ? 4 : 2) + 16 * (lane >> 5);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const uint64_t band = (uint64_t)(n0 + wm * 32 * TM + 32 * i) * K + (k0 + wn * 32 * TN);
-      const __amdgpu_buffer_rsrc_t rO = make_rsrc(a.out + band, inside ? 0xFFFFFFFFu : 0);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        v16f& c = acc[i][j];
-        if constexpr (SPLIT) {
-          uint8_t* p = reinterpret_cast<uint8_t*>(a.part + (uint64_t)split * N * K + band + 32 * j);
-#pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<v4f*>(p + 8 * r + at) = v4f{c[r], c[r + 1], c[r + 2], c[r + 3]};
-        } else {
-          // 8 columns a lane: the halves of the wave swap every other four
-#pragma unroll
-          for (int r = 0; r < 16; r += 8) {
-            const uint2 lo = pack_bf16x4(v4f{c[r], c[r + 1], c[r + 2], c[r + 3]});
-            const uint2 hi = pack_bf16x4(v4f{c[r + 4], c[r + 5], c[r + 6], c[r + 7]});
-            const auto s0 = __builtin_amdgcn_permlane32_swap(lo.x, hi.x, false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(lo.y, hi.y, false, false);
-            __builtin_amdgcn_raw_buffer_store_b128(u32x4{s0[0], s1[0], s0[1], s1[1]}, rO, at, 64 * j + 4 * r, 0);
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) c[r] = 0.0f;
-        sched_fence();  // one tile's accumulators out at a time
-      }
+    const uint64_t corner = (uint64_t)(n0 + wm * 32 * TM) * K + (k0 + wn * 32 * TN);
+    const uint64_t base = SPLIT ? (uint64_t)(a.part + (uint64_t)split * N * K + corner) : (uint64_t)(a.out + corner);
+    if (inside) {
+      unroll_seq(
+          [&](auto ic) {
+            constexpr int i = decltype(ic)::value / TN, j = decltype(ic)::value % TN;
+            const v16f& c = acc[i][j];
+            const uint64_t band = base + (uint64_t)(32 * i) * K * (SPLIT ? 4 : 2);
+            if constexpr (SPLIT) {
+              unroll_seq(
+                  [&](auto rc) {
+                    constexpr int r = 4 * decltype(rc)::value;
+                    store16_asm<128 * j + 8 * r>(band, at, __builtin_bit_cast(u32x4s, v4f{c[r], c[r + 1], c[r + 2], c[r + 3]}));
+                  },
+                  std::make_integer_sequence<int, 4>{});
+            } else {
+              // 8 columns a lane: the halves of the wave swap every other four
+              unroll_seq(
+                  [&](auto rc) {
+                    constexpr int r = 8 * decltype(rc)::value;
+                    const auto s0 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r], c[r + 1]),
+                                                                     cvt_bf16x2(c[r + 4], c[r + 5]), false, false);
+                    const auto s1 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r + 2], c[r + 3]),
+                                                                     cvt_bf16x2(c[r + 6], c[r + 7]), false, false);
+                    store16_asm<64 * j + 4 * r>(band, at, u32x4s{s0[0], s1[0], s0[1], s1[1]});
+                  },
+                  std::make_integer_sequence<int, 2>{});
+            }
+            sched_fence();  // one tile's accumulators out at a time
+          },
+          std::make_integer_sequence<int, TM * TN>{});
     }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
     if (++u == units) break;
     n0 = nn0;
     k0 = nk0;
