@@ -271,11 +271,12 @@ __device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t uni
       unroll_seq([&](auto s) { step(s); }, std::make_integer_sequence<int, SLOTS>{});
     }
     // N and K are multiples of 128: a wave's share lies inside whole or not at all.  Lane:
-    // row n = 32 i + l32, columns k = 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4; a row
-    // group's place is uniform, the lane's within it below 2^32 bytes.
+    // row n = 32 i + l32, columns k = 32 j + 8 (r / 4) + 4 (lane / 32) + r % 4.  A row
+    // group's place is uniform, the lane's within it (at) below 2^32 bytes.
     const bool inside = n0 + wm * 32 * TM < N && k0 + wn * 32 * TN < K;
     sched_fence();
-    const uint32_t at = l32 * K * (SPLIT ? 4 : 2) + 16 * (lane >> 5);
+    const uint32_t at = SPLIT ? l32 * K * 4 + 16 * (lane >> 5)
+                              : (lane & 15) * K * 2 + 32 * ((lane >> 4) & 1) + 16 * (lane >> 5);
     const uint64_t corner = (uint64_t)(n0 + wm * 32 * TM) * K + (k0 + wn * 32 * TN);
     const uint64_t base = SPLIT ? (uint64_t)(a.part + (uint64_t)split * N * K + corner) : (uint64_t)(a.out + corner);
     if (inside) {
@@ -292,17 +293,27 @@ __device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t uni
                   },
                   std::make_integer_sequence<int, 4>{});
             } else {
-              // 8 columns a lane: the halves of the wave swap every other four
+              // Lane l holds four columns in four of each row's eight places.  The halves of
+              // the wave swap (8 columns a lane), then the odd and even 16-lane rows: a store
+              // covers 16 rows x 64 bytes, not 32 x 32.
+              uint32_t v[2][4];
               unroll_seq(
                   [&](auto rc) {
-                    constexpr int r = 8 * decltype(rc)::value;
+                    constexpr int s = decltype(rc)::value, r = 8 * s;
                     const auto s0 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r], c[r + 1]),
                                                                      cvt_bf16x2(c[r + 4], c[r + 5]), false, false);
                     const auto s1 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r + 2], c[r + 3]),
                                                                      cvt_bf16x2(c[r + 6], c[r + 7]), false, false);
-                    store16_asm<64 * j + 4 * r>(band, at, u32x4s{s0[0], s1[0], s0[1], s1[1]});
+                    v[s][0] = s0[0], v[s][1] = s1[0], v[s][2] = s0[1], v[s][3] = s1[1];
                   },
                   std::make_integer_sequence<int, 2>{});
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                const auto s = __builtin_amdgcn_permlane16_swap(v[0][d], v[1][d], false, false);
+                v[0][d] = s[0], v[1][d] = s[1];
+              }
+              store16_asm<64 * j>(band, at, u32x4s{v[0][0], v[0][1], v[0][2], v[0][3]});
+              store16_asm<64 * j>(band + (uint64_t)16 * K * 2, at, u32x4s{v[1][0], v[1][1], v[1][2], v[1][3]});
             }
             sched_fence();  // one tile's accumulators out at a time
           },
