@@ -90,7 +90,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
   for (uint32_t i = 0; i < C; ++i) {
     const uint32_t c = t + 64 * W * i;
     h[i] = u32x4{0, 0, 0, 0};
-    if (live && c < chunks) h[i] = a.x[base + c];
+    if (live && c < chunks) h[i] = __builtin_nontemporal_load(&a.x[base + c]);
   }
   if (a.r) {
     u32x4 r[C];
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
     for (uint32_t i = 0; i < C; ++i) {
       const uint32_t c = t + 64 * W * i;
       r[i] = u32x4{0, 0, 0, 0};
-      if (live && c < chunks) r[i] = a.r[base + c];
+      if (live && c < chunks) r[i] = __builtin_nontemporal_load(&a.r[base + c]);
     }
 #pragma unroll
     for (uint32_t i = 0; i < C; ++i) {
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         h[i][j] = pack_bf16(bf_lo(h[i][j]) + bf_lo(r[i][j]), bf_hi(h[i][j]) + bf_hi(r[i][j]));
-      if (live && c < chunks) a.h[base + c] = h[i];
+      if (live && c < chunks) __builtin_nontemporal_store(h[i], &a.h[base + c]);
     }
   }
   float ss = 0.0f;
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
         u32x4 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
-        a.y[base + c] = o;
+        __builtin_nontemporal_store(o, &a.y[base + c]);
       }
       if ((lane & 15) == 0) {
         if (a.srm) a.srm[(uint64_t)m * G + c / 16] = s;
@@ -170,12 +170,15 @@ struct NormGradArgs {
   uint32_t M, K;
 };
 
-// A workgroup of W waves takes the rows b, b + gridDim.x, ... and keeps its share
-// of dw in registers.
-template <uint32_t W, uint32_t C>
-__global__ __launch_bounds__(64 * W) void norm_grad_kernel(NormGradArgs a) {
+// Row groups of W waves take the rows g, g + groups, ... and keep their share of dw in
+// registers; the row groups of a workgroup (blockDim.x / (64 W)) meet in LDS at the end.
+// T: the workgroup's threads at most.
+template <uint32_t W, uint32_t C, uint32_t T>
+__global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
+  extern __shared__ float dws[];  // [K], where a workgroup holds several row groups
   __shared__ float red[2][kNormMaxWaves];
-  const uint32_t wave = threadIdx.x >> 6, t = threadIdx.x, chunks = a.K / 8;
+  const uint32_t wave = threadIdx.x >> 6, rows = (blockDim.x >> 6) / W, row = wave / W;
+  const uint32_t t = threadIdx.x % (64 * W), chunks = a.K / 8;
   const float inv_k = 1.0f / (float)a.K;
 
   float dw[C][8];
@@ -184,20 +187,23 @@ __global__ __launch_bounds__(64 * W) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   uint32_t turn = 0;
-  for (uint32_t m = blockIdx.x; m < a.M; m += gridDim.x, turn ^= 1) {
+  for (uint64_t m0 = blockIdx.x * rows; m0 < a.M; m0 += gridDim.x * rows, turn ^= 1) {  // uniform
+    const uint32_t m = (uint32_t)m0 + row;
+    const bool live = m < a.M;
     const uint64_t base = (uint64_t)m * chunks;
-    const float rstd = a.rstd[m];
-    u32x4 dy[C], h[C];
-    float s = 0.0f;
+    const float rstd = live ? a.rstd[m] : 0.0f;
+    u32x4 dy[C], h[C], d[C];
 #pragma unroll
     for (uint32_t i = 0; i < C; ++i) {
       const uint32_t c = t + 64 * W * i;
-      dy[i] = h[i] = u32x4{0, 0, 0, 0};
-      if (c < chunks) {
-        dy[i] = a.dy[base + c];
-        h[i] = a.h[base + c];
+      dy[i] = h[i] = d[i] = u32x4{0, 0, 0, 0};
+      if (live && c < chunks) {
+        dy[i] = __builtin_nontemporal_load(&a.dy[base + c]);
+        h[i] = __builtin_nontemporal_load(&a.h[base + c]);
+        if (a.dh) d[i] = __builtin_nontemporal_load(&a.dh[base + c]);
       }
     }
+    float s = 0.0f;
 #pragma unroll
     for (uint32_t i = 0; i < C; ++i) {
       const uint32_t c = t + 64 * W * i;
@@ -215,28 +221,39 @@ __global__ __launch_bounds__(64 * W) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (uint32_t i = 0; i < C; ++i) {
       const uint32_t c = t + 64 * W * i;
-      if (c < chunks) {
+      if (live && c < chunks) {
         const u32x4 w = a.w[c];
-        const u32x4 d = a.dh ? a.dh[base + c] : u32x4{0, 0, 0, 0};
         u32x4 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float l = rstd * (bf_lo(dy[i][j]) * bf_lo(w[j]) - bf_lo(h[i][j]) * rstd * s);
           const float u = rstd * (bf_hi(dy[i][j]) * bf_hi(w[j]) - bf_hi(h[i][j]) * rstd * s);
-          o[j] = pack_bf16(l + bf_lo(d[j]), u + bf_hi(d[j]));
+          o[j] = pack_bf16(l + bf_lo(d[i][j]), u + bf_hi(d[i][j]));
         }
-        a.dx[base + c] = o;
+        __builtin_nontemporal_store(o, &a.dx[base + c]);
       }
     }
   }
   float* out = a.part + (uint64_t)blockIdx.x * a.K;
+  for (uint32_t r = 0; r < rows; ++r) {  // the row groups in order; the last one writes
+    if (r) __syncthreads();
+    if (row == r) {
 #pragma unroll
-  for (uint32_t i = 0; i < C; ++i) {
-    const uint32_t c = t + 64 * W * i;
-    if (c < chunks) {
-      float4* o = reinterpret_cast<float4*>(out + 8 * c);
-      o[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-      o[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      for (uint32_t i = 0; i < C; ++i) {
+        const uint32_t c = t + 64 * W * i;
+        if (c < chunks) {
+          float4* o = reinterpret_cast<float4*>((r + 1 == rows ? out : dws) + 8 * c);
+          float4 lo = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+          float4 hi = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+          if (r) {
+            const float4* b = reinterpret_cast<const float4*>(dws + 8 * c);
+            lo.x += b[0].x, lo.y += b[0].y, lo.z += b[0].z, lo.w += b[0].w;
+            hi.x += b[1].x, hi.y += b[1].y, hi.z += b[1].z, hi.w += b[1].w;
+          }
+          o[0] = lo;
+          o[1] = hi;
+        }
+      }
     }
   }
 }
@@ -247,6 +264,7 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__
   __shared__ float sum[16][64];
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, k = blockIdx.x * 64 + lane;
   float s = 0.0f;
+#pragma unroll 16
   for (uint32_t p = wave; p < parts; p += 16) s += part[(uint64_t)p * K + k];
   sum[wave][lane] = s;
   __syncthreads();
@@ -257,39 +275,53 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__
   }
 }
 
-// Waves a row: the fewest whose lanes hold the row in `most` chunks.
+// Waves that a row takes, of those below: the fewest whose lanes hold it in `most` chunks
+// each, or 16.
+constexpr uint32_t kRowWaves[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
 uint32_t row_waves(uint32_t K, uint32_t most) {
-  uint32_t w = 1;
-  while (w < kNormMaxWaves && K / 8 > 64 * w * most) w *= 2;
-  return w;
+  for (uint32_t w : kRowWaves)
+    if (K / 8 <= 64 * w * most) return w;
+  return 16;
 }
 
-template <uint32_t W>
-hipError_t launch_norm_w(const NormArgs& a, uint32_t rows, hipStream_t s) {
-  const uint32_t C = (a.K / 8 + 64 * W - 1) / (64 * W);
-  const dim3 grid((a.M + rows - 1) / rows), block(64 * W * rows);
-  const size_t lds = (size_t)rows * (a.K / kGroup) * 4;
-  if (C <= 1) norm_quant_kernel<W, 1><<<grid, block, lds, s>>>(a);
-  else if (C <= 2) norm_quant_kernel<W, 2><<<grid, block, lds, s>>>(a);
-  else if (C <= 3) norm_quant_kernel<W, 3><<<grid, block, lds, s>>>(a);
-  else if (C <= 4) norm_quant_kernel<W, 4><<<grid, block, lds, s>>>(a);
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
+// f(W, C) for a row's waves and chunks a lane
+template <class F>
+hipError_t for_row(uint32_t K, uint32_t most, F&& f) {
+  using std::integral_constant;
+  const uint32_t w = row_waves(K, most), c = (K / 8 + 64 * w - 1) / (64 * w);
+  auto chunks = [&](auto W) -> hipError_t {
+    if (c <= 1) return f(W, integral_constant<uint32_t, 1>{});
+    if (c <= 2) return f(W, integral_constant<uint32_t, 2>{});
+    if constexpr (decltype(W)::value == 16) {
+      if (c <= 3) return f(W, integral_constant<uint32_t, 3>{});
+      if (c <= 4) return f(W, integral_constant<uint32_t, 4>{});
+    }
+    return hipErrorInvalidValue;
+  };
+  switch (w) {
+    case 1: return chunks(integral_constant<uint32_t, 1>{});
+    case 2: return chunks(integral_constant<uint32_t, 2>{});
+    case 3: return chunks(integral_constant<uint32_t, 3>{});
+    case 4: return chunks(integral_constant<uint32_t, 4>{});
+    case 5: return chunks(integral_constant<uint32_t, 5>{});
+    case 6: return chunks(integral_constant<uint32_t, 6>{});
+    case 8: return chunks(integral_constant<uint32_t, 8>{});
+    case 10: return chunks(integral_constant<uint32_t, 10>{});
+    case 12: return chunks(integral_constant<uint32_t, 12>{});
+    default: return chunks(integral_constant<uint32_t, 16>{});
+  }
 }
 
-template <uint32_t W>
-hipError_t launch_norm_grad_w(const NormGradArgs& a, uint32_t grid, hipStream_t s) {
-  const uint32_t C = (a.K / 8 + 64 * W - 1) / (64 * W);
-  const dim3 block(64 * W);
-  if (C <= 1) norm_grad_kernel<W, 1><<<grid, block, 0, s>>>(a);
-  else if (C <= 2) norm_grad_kernel<W, 2><<<grid, block, 0, s>>>(a);
-  else if (C <= 3) norm_grad_kernel<W, 3><<<grid, block, 0, s>>>(a);
-  else if (C <= 4) norm_grad_kernel<W, 4><<<grid, block, 0, s>>>(a);
-  else return hipErrorInvalidValue;
-  return hipGetLastError();
-}
+// Row groups of a workgroup, about 12 waves
+constexpr uint32_t group_rows(uint32_t W) { return W >= 8 ? 1 : 12 / W; }
 
-constexpr uint32_t kNormGradParts = 256;
+// Up to this many rows each has a workgroup and twice the waves.
+constexpr uint32_t kNormFewRows = 256;
+constexpr uint32_t kNormGradParts = 256;  // workgroups of a gradient call: one a CU (256 CUs)
+uint32_t norm_grad_parts(uint32_t M, uint32_t K) {
+  const uint32_t rows = group_rows(row_waves(K, 2));
+  return std::min((M + rows - 1) / rows, kNormGradParts);
+}
 
 }  // namespace
 
@@ -299,18 +331,15 @@ hipError_t launch_norm_quant(const uint16_t* x, const uint16_t* r, const uint16_
   const NormArgs a{reinterpret_cast<const u32x4*>(x), reinterpret_cast<const u32x4*>(r),
                    reinterpret_cast<const u32x4*>(w), reinterpret_cast<u32x4*>(h), reinterpret_cast<u32x4*>(y),
                    reinterpret_cast<u32x2*>(q), scale_rm, scale_km, rstd, eps, M, K, m_pad16(M)};
-  const uint32_t W = row_waves(K, 4);
-  switch (W) {
-    case 1: return launch_norm_w<1>(a, 8, s);
-    case 2: return launch_norm_w<2>(a, 4, s);
-    case 4: return launch_norm_w<4>(a, 2, s);
-    case 8: return launch_norm_w<8>(a, 1, s);
-    default: return launch_norm_w<16>(a, 1, s);
-  }
+  return for_row(K, M <= kNormFewRows ? 1 : 2, [&](auto W, auto C) {
+    const uint32_t rows = M <= kNormFewRows ? 1 : group_rows(W);
+    norm_quant_kernel<W, C><<<dim3((M + rows - 1) / rows), dim3(64 * W * rows), rows * (K / kGroup) * 4, s>>>(a);
+    return hipGetLastError();
+  });
 }
 
 uint64_t norm_grad_workspace_bytes(uint32_t M, uint32_t K) {
-  return (uint64_t)std::min(M, kNormGradParts) * K * 4;
+  return (uint64_t)norm_grad_parts(M, K) * K * 4;
 }
 
 hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* w,
@@ -319,19 +348,16 @@ hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16
   const NormGradArgs a{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(dh),
                        reinterpret_cast<const u32x4*>(h), reinterpret_cast<const u32x4*>(w), rstd,
                        reinterpret_cast<u32x4*>(dx), static_cast<float*>(workspace), M, K};
-  const uint32_t parts = std::min(M, kNormGradParts);
   if (M > 0) {
-    hipError_t e;
-    switch (row_waves(K, 4)) {
-      case 1: e = launch_norm_grad_w<1>(a, parts, s); break;
-      case 2: e = launch_norm_grad_w<2>(a, parts, s); break;
-      case 4: e = launch_norm_grad_w<4>(a, parts, s); break;
-      case 8: e = launch_norm_grad_w<8>(a, parts, s); break;
-      default: e = launch_norm_grad_w<16>(a, parts, s); break;
-    }
+    const hipError_t e = for_row(K, 2, [&](auto W, auto C) {
+      constexpr uint32_t rows = group_rows(W);
+      norm_grad_kernel<W, C, 64 * W * rows><<<dim3(norm_grad_parts(M, K)), dim3(64 * W * rows),
+                                              rows > 1 ? K * 4 : 0, s>>>(a);
+      return hipGetLastError();
+    });
     if (e != hipSuccess) return e;
   }
-  norm_dw_kernel<<<dim3(K / 64), dim3(1024), 0, s>>>(a.part, dw, parts, K);
+  norm_dw_kernel<<<dim3(K / 64), dim3(1024), 0, s>>>(a.part, dw, norm_grad_parts(M, K), K);
   return hipGetLastError();
 }
 

@@ -35,7 +35,7 @@ __device__ __forceinline__ uint32_t token_byte(uint32_t amax) {
 }
 
 template <bool ROWS>
-__global__ __launch_bounds__(kDualThreads) void quant_dual_kernel(
+__global__ __launch_bounds__(kDualThreads, 5) void quant_dual_kernel(
     const u32x4* __restrict__ x, u32x2* __restrict__ q, float* __restrict__ skm, u32x2* __restrict__ qt,
     uint8_t* __restrict__ et, uint32_t M, uint32_t K, uint32_t Mp, uint32_t gtiles) {
   __shared__ uint32_t cmax[4][16][4];
