@@ -264,8 +264,13 @@ __global__ __launch_bounds__(1024) void norm_dw_kernel(const float* __restrict__
   __shared__ float sum[16][64];
   const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, k = blockIdx.x * 64 + lane;
   float s = 0.0f;
-#pragma unroll 16
-  for (uint32_t p = wave; p < parts; p += 16) s += part[(uint64_t)p * K + k];
+  for (uint32_t p0 = wave; p0 < parts; p0 += 128) {  // eight loads in flight
+    float v[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) v[i] = p0 + 16 * i < parts ? part[(uint64_t)(p0 + 16 * i) * K + k] : 0.0f;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) s += v[i];
+  }
   sum[wave][lane] = s;
   __syncthreads();
   if (wave == 0) {
