@@ -12,10 +12,12 @@
 // p or, renormalised, the softmax over the chosen slots alone, m[e] slots holding e:
 //   dl[e] += w[e] * (sum_{j: e_j = e} dw_j - (m[e] or 1) * sum_j w[e_j] dw_j)
 //
-// A wave takes its tokens one after the other, lane l holding the logits l, l + 64,
-// ...  Probabilities are summed in registers, then over a workgroup's waves and over
-// the workgroups in a fixed order; counts are integers, so their LDS atomics give
-// the same result in any order.
+// A wave takes four tokens at a time, one a 16-lane row, lane l of it holding the logits
+// l, l + 16, ...: a reduction is four DPP steps for all four.  (One token a wave, its
+// reductions over 64 lanes, was bound by the vector instructions: 13 us a launch at 16384
+// tokens of 160 experts, twice the present.)  Probabilities are summed in registers, then
+// over a workgroup's waves and over the workgroups in a fixed order; counts are integers,
+// so their LDS atomics give the same result in any order.
 #include <algorithm>
 
 #include "wave_common.h"
@@ -26,36 +28,47 @@ namespace {
 constexpr uint32_t kWaves = 16, kThreads = 64 * kWaves;
 // One workgroup takes up to this many tokens alone (one launch); beyond, at least
 // kBlockTokens a workgroup and at most kMaxBlocks of them, summed by a second one.
-constexpr uint32_t kLoneTokens = 128, kBlockTokens = 32, kMaxBlocks = 128;
+constexpr uint32_t kLoneTokens = 128, kBlockTokens = 64, kMaxBlocks = 256;
 
 uint32_t balance_blocks(uint32_t T) {
   return T <= kLoneTokens ? 1 : std::min((T + kBlockTokens - 1) / kBlockTokens, kMaxBlocks);
 }
 
-// This lane's logits of token t as fp32; -inf where there is none or NaN.
-template <int NV>
-__device__ __forceinline__ void load_logits(const void* logits, bool bf16, uint32_t t, uint32_t E, uint32_t lane,
-                                            float (&l)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const uint32_t e = 64 * i + lane;
-    const uint64_t at = (uint64_t)t * E + min(e, E - 1);
-    const float v = bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16)
-                         : static_cast<const float*>(logits)[at];
-    l[i] = e < E ? clean_logit(v) : -INFINITY;
-  }
+__device__ __forceinline__ float dpp_row_sum_f32(float v) {
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  v += dpp_f32<0x141>(v);
+  return v + dpp_f32<0x140>(v);
 }
 
-// The key of the largest logit.
+// This lane's logits of token t (the row's) as fp32; -inf where there is none or NaN.
+template <int NV>
+__device__ __forceinline__ void load_logits(const void* logits, bool bf16, uint32_t t, uint32_t E, uint32_t l16,
+                                            float (&l)[NV]) {
+  const uint64_t at = (uint64_t)t * E + l16;
+  if (bf16) {  // uniform
+    const uint16_t* p = static_cast<const uint16_t*>(logits) + at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = 16 * i + l16 < E ? __uint_as_float((uint32_t)p[16 * i] << 16) : -INFINITY;
+  } else {
+    const float* p = static_cast<const float*>(logits) + at;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = 16 * i + l16 < E ? p[16 * i] : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) l[i] = clean_logit(l[i]);
+}
+
+// The key of the row's largest logit.
 template <int NV>
 __device__ __forceinline__ uint32_t top_key(const float (&l)[NV]) {
-  uint32_t top = kNoKey;
+  float top = l[0];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) top = max(top, logit_key(l[i]));
-  return wave_max_u32(top);
+  for (int i = 1; i < NV; ++i) top = fmaxf(top, l[i]);
+  return dpp_row_max_u32(logit_key(top));
 }
 
-// e[i] = e^(l[i] - top), 0 where l is -inf; returns their sum (0: nothing to choose).
+// e[i] = e^(l[i] - top), 0 where l is -inf; returns the row's sum (0: nothing to choose).
 template <int NV>
 __device__ __forceinline__ float exp_logits(const float (&l)[NV], uint32_t top, float (&e)[NV]) {
   const float lmax = top == kNoKey ? 0.0f : key_logit(top);
@@ -65,7 +78,7 @@ __device__ __forceinline__ float exp_logits(const float (&l)[NV], uint32_t top, 
     e[i] = l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - lmax);
     sum += e[i];
   }
-  return wave_sum_f32(sum);
+  return dpp_row_sum_f32(sum);
 }
 
 struct BalanceArgs {
@@ -109,30 +122,39 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
   __shared__ float red[kWaves];
   uint32_t* cnt = lds;
   float* sums = reinterpret_cast<float*>(lds + a.E + 1);
-  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, row = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (uint32_t e = threadIdx.x; e <= a.E; e += kThreads) cnt[e] = 0;
   __syncthreads();
   float acc[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
-  uint32_t n = 0;
-  for (uint32_t t = blockIdx.x * kWaves + wave; t < a.T; t += gridDim.x * kWaves) {
+  uint32_t n = 0;  // of the row's tokens, those with an expert
+  for (uint64_t t0 = (uint64_t)(blockIdx.x * kWaves + wave) * 4; t0 < a.T; t0 += (uint64_t)gridDim.x * kWaves * 4) {
+    const bool live = t0 + row < a.T;  // (rows past the last token repeat it and count nothing)
+    const uint32_t t = (uint32_t)min(t0 + row, (uint64_t)a.T - 1);
     float l[NV], x[NV];
-    load_logits<NV>(a.logits, a.bf16, t, a.E, lane, l);
-    const uint32_t id = lane < a.k ? (uint32_t)a.ids[(uint64_t)t * a.k + lane] : a.E;
+    load_logits<NV>(a.logits, a.bf16, t, a.E, l16, l);
+    uint32_t id[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      id[j] = live && 16 * j + l16 < a.k ? (uint32_t)a.ids[(uint64_t)t * a.k + 16 * j + l16] : a.E;
     const float sum = exp_logits<NV>(l, top_key<NV>(l), x);
-    if (sum > 0.0f) {  // uniform
-      const float r = 1.0f / sum;
+    const float r = live && sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(x[i], r, acc[i]);
-      ++n;
-    }
-    if (id < a.E) atomicAdd(&cnt[id], 1u);
+    for (int i = 0; i < NV; ++i) acc[i] = __builtin_fmaf(x[i], r, acc[i]);
+    n += live && sum > 0.0f ? 1 : 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (id[j] < a.E) atomicAdd(&cnt[id[j]], 1u);
   }
-  if (lane == 0 && n) atomicAdd(&cnt[a.E], n);
+  if (l16 == 0 && n) atomicAdd(&cnt[a.E], n);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-    if (64 * i + lane < a.E) sums[wave * a.E + 64 * i + lane] = acc[i];
+  for (int i = 0; i < NV; ++i) {  // the four rows
+    acc[i] += __shfl_xor(acc[i], 16);
+    acc[i] += __shfl_xor(acc[i], 32);
+    if (row == 0 && 16 * i + l16 < a.E) sums[wave * a.E + 16 * i + l16] = acc[i];
+  }
   __syncthreads();
   for (uint32_t e = threadIdx.x; e < a.E; e += kThreads) {
     float s = 0.0f;
@@ -146,45 +168,48 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
   } else {
     uint32_t* out = a.part + (uint64_t)blockIdx.x * 2 * (a.E + 1);
     for (uint32_t e = threadIdx.x; e <= a.E; e += kThreads) {
-      if (e < a.E) out[e] = __float_as_uint(sums[e]);
+      out[e] = e < a.E ? __float_as_uint(sums[e]) : 0;
       out[a.E + 1 + e] = cnt[e];
     }
   }
 }
 
-// The workgroups' sums, added in order.
-__global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a) {
-  extern __shared__ uint32_t lds[];  // [E + 1] counts, [slices][E + 1] twice
+// The workgroups' sums: `slices` slices of the workgroups, each in order, then in slice
+// order.  One workgroup, bound by the latency of its loads: 32 in flight a thread.
+__global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, uint32_t slices) {
+  extern __shared__ uint32_t lds[];  // [slices][2 (E + 1)], then psum and cnt in slice 0's place
   __shared__ float red[kWaves];
-  const uint32_t EB = a.E + 1, slices = kThreads / EB ? kThreads / EB : 1;
-  uint32_t* cnt = lds;
-  float* psum = reinterpret_cast<float*>(lds + EB);
-  uint32_t* csum = lds + EB + slices * EB;
-  const uint32_t slice = threadIdx.x / EB, e = threadIdx.x % EB;
-  if (slice < slices) {
+  constexpr uint32_t kInFlight = 32;
+  const uint32_t EB = a.E + 1, R = 2 * EB;
+  for (uint32_t at = threadIdx.x; at < slices * R; at += kThreads) {
+    const uint32_t slice = at / R, c = at % R;
     float p = 0.0f;
-    uint32_t c = 0;
-    for (uint32_t b = slice; b < a.blocks; b += slices) {
-      const uint32_t* in = a.part + (uint64_t)b * 2 * EB;
-      if (e < a.E) p += __uint_as_float(in[e]);
-      c += in[EB + e];
+    uint32_t n = 0;
+    for (uint32_t b0 = slice; b0 < a.blocks; b0 += kInFlight * slices) {
+      uint32_t v[kInFlight];
+#pragma unroll
+      for (uint32_t i = 0; i < kInFlight; ++i)
+        v[i] = b0 + i * slices < a.blocks ? a.part[(uint64_t)(b0 + i * slices) * R + c] : 0;
+#pragma unroll
+      for (uint32_t i = 0; i < kInFlight; ++i) {
+        p += __uint_as_float(v[i]);
+        n += v[i];
+      }
     }
-    psum[slice * EB + e] = p;
-    csum[slice * EB + e] = c;
+    lds[at] = c < EB ? __float_as_uint(p) : n;
   }
   __syncthreads();
-  if (threadIdx.x < EB) {
+  for (uint32_t c = threadIdx.x; c < R; c += kThreads) {
     float p = 0.0f;
-    uint32_t c = 0;
+    uint32_t n = 0;
     for (uint32_t s = 0; s < slices; ++s) {
-      p += psum[s * EB + threadIdx.x];
-      c += csum[s * EB + threadIdx.x];
+      p += __uint_as_float(lds[s * R + c]);
+      n += lds[s * R + c];
     }
-    psum[threadIdx.x] = p;
-    cnt[threadIdx.x] = c;
+    lds[c] = c < EB ? __float_as_uint(p) : n;
   }
   __syncthreads();
-  finish(a, psum, cnt, red);
+  finish(a, reinterpret_cast<const float*>(lds), lds + EB, red);
 }
 
 struct RouteGradArgs {
@@ -199,50 +224,81 @@ struct RouteGradArgs {
   bool bf16, renorm;
 };
 
+constexpr uint32_t kGradWaves = 4, kGradGrid = 1024;
+
+// Keeps the compiler from moving LDS accesses across.
+__device__ __forceinline__ void lds_order() {
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
 template <int NV>
-__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
-  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(64 * kGradWaves) void route_grad_kernel(RouteGradArgs a) {
+  extern __shared__ uint32_t lds[];  // a row: [E] sums of dweights, [E] slots
+  const uint32_t lane = threadIdx.x & 63, l16 = lane & 15, row = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* dsum = reinterpret_cast<float*>(lds) + (size_t)(wave * 4 + row) * 2 * a.E;
+  uint32_t* slots = reinterpret_cast<uint32_t*>(dsum) + a.E;
   float share[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) share[i] = 0.0f;
   if (a.counts) {
     const float n = (float)a.counts[a.E];
-    if (n > 0.0f) {
-      const float f = a.coef * (float)a.E / (n * (float)a.k) / n * (a.dloss ? *a.dloss : 1.0f);
+    const float f = n > 0.0f ? a.coef * (float)a.E / (n * (float)a.k) / n * (a.dloss ? *a.dloss : 1.0f) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (64 * i + lane < a.E) share[i] = f * (float)a.counts[64 * i + lane];
+    for (int i = 0; i < NV; ++i) {
+      const float c = (float)a.counts[min(16 * i + l16, a.E - 1)];
+      share[i] = n > 0.0f && 16 * i + l16 < a.E ? f * c : 0.0f;
     }
   }
-  for (uint32_t t = blockIdx.x * 4 + wave; t < a.T; t += gridDim.x * 4) {
+  for (uint64_t t0 = (uint64_t)(blockIdx.x * kGradWaves + wave) * 4; t0 < a.T;
+       t0 += (uint64_t)gridDim.x * kGradWaves * 4) {
+    const bool live = t0 + row < a.T;  // (rows past the last token repeat it and store nothing)
+    const uint32_t t = (uint32_t)min(t0 + row, (uint64_t)a.T - 1);
     float l[NV], x[NV], g[NV];
-    load_logits<NV>(a.logits, a.bf16, t, a.E, lane, l);
-    const bool slot = a.ids && lane < a.k;
-    const uint32_t id = slot ? (uint32_t)a.ids[(uint64_t)t * a.k + lane] : a.E;
-    const float dwj = id < a.E ? a.dweights[(uint64_t)t * a.k + lane] : 0.0f;
+    load_logits<NV>(a.logits, a.bf16, t, a.E, l16, l);
+    uint32_t id[2];
+    float dwj[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool slot = a.ids && 16 * j + l16 < a.k;
+      id[j] = slot ? (uint32_t)a.ids[(uint64_t)t * a.k + 16 * j + l16] : a.E;
+      dwj[j] = id[j] < a.E ? a.dweights[(uint64_t)t * a.k + 16 * j + l16] : 0.0f;
+    }
     const uint32_t top = top_key<NV>(l);
     const float sum = exp_logits<NV>(l, top, x);
     const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) dot = __builtin_fmaf(x[i] * r, share[i], dot);
-    dot = wave_sum_f32(dot);
+    dot = dpp_row_sum_f32(dot);
 #pragma unroll
     for (int i = 0; i < NV; ++i) g[i] = x[i] * r * (share[i] - dot);
     if (a.ids) {
-      float d[NV], m[NV];  // the slots' gradients and number at this lane's experts
+      // the slots' gradients and number at their experts, through the row's part of LDS (a
+      // wave's LDS accesses are in order)
+      float d[NV], m[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = m[i] = 0.0f;
-      for (uint32_t j = 0; j < a.k; ++j) {
-        const uint32_t ej = (uint32_t)__builtin_amdgcn_readlane((int)id, (int)j);
-        const float dj = lane_f32(dwj, (int)j);
+      for (int i = 0; i < NV; ++i)
+        if (16 * i + l16 < a.E) {
+          dsum[16 * i + l16] = 0.0f;
+          if (a.renorm) slots[16 * i + l16] = 0;
+        }
+      lds_order();
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (ej == 64 * i + lane) {
-            d[i] += dj;
-            m[i] += 1.0f;
-          }
+      for (int j = 0; j < 2; ++j)
+        if (id[j] < a.E) {
+          unsafeAtomicAdd(&dsum[id[j]], dwj[j]);
+          if (a.renorm) atomicAdd(&slots[id[j]], 1u);
+        }
+      lds_order();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = 16 * i + l16 < a.E;
+        d[i] = in ? dsum[min(16 * i + l16, a.E - 1)] : 0.0f;
+        m[i] = !a.renorm ? 1.0f : in ? (float)slots[min(16 * i + l16, a.E - 1)] : 0.0f;
       }
+      lds_order();
       float rw = r;
       if (a.renorm) {
         // over the chosen slots alone, with their own maximum: chosen by another
@@ -251,28 +307,31 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) c[i] = m[i] > 0.0f ? l[i] : -INFINITY;
         const uint32_t top_c = top_key<NV>(c);
-        if (top_c != top) exp_logits<NV>(c, top_c, x);  // uniform
+        if (__builtin_amdgcn_ballot_w64(top_c != top)) exp_logits<NV>(c, top_c, x);  // (equal tops: equal values)
 #pragma unroll
         for (int i = 0; i < NV; ++i) mass = __builtin_fmaf(x[i], m[i], mass);
-        mass = wave_sum_f32(mass);
+        mass = dpp_row_sum_f32(mass);
         rw = mass > 0.0f ? 1.0f / mass : 0.0f;
       }
       float wd = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) wd = __builtin_fmaf(x[i] * rw, d[i], wd);
-      wd = wave_sum_f32(wd);
+      wd = dpp_row_sum_f32(wd);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) g[i] += x[i] * rw * (d[i] - (a.renorm ? m[i] : 1.0f) * wd);
+      for (int i = 0; i < NV; ++i) g[i] += x[i] * rw * (d[i] - m[i] * wd);
     }
+    if (live) {
+      const uint64_t at = (uint64_t)t * a.E + l16;
+      if (a.bf16) {
+        uint16_t* p = static_cast<uint16_t*>(a.dlogits) + at;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const uint32_t e = 64 * i + lane;
-      if (e < a.E) {
-        const uint64_t at = (uint64_t)t * a.E + e;
-        if (a.bf16)
-          static_cast<uint16_t*>(a.dlogits)[at] = (uint16_t)bf16_bits_rne(g[i]);
-        else
-          static_cast<float*>(a.dlogits)[at] = g[i];
+        for (int i = 0; i < NV; ++i)
+          if (16 * i + l16 < a.E) p[16 * i] = (uint16_t)bf16_bits_rne(g[i]);
+      } else {
+        float* p = static_cast<float*>(a.dlogits) + at;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (16 * i + l16 < a.E) p[16 * i] = g[i];
       }
     }
   }
@@ -287,9 +346,23 @@ hipError_t launch_balance_nv(const BalanceArgs& a, hipStream_t s) {
 
 template <int NV>
 hipError_t launch_grad_nv(const RouteGradArgs& a, hipStream_t s) {
-  const uint32_t grid = std::min((a.T + 3) / 4, 2048u);
-  route_grad_kernel<NV><<<dim3(grid), dim3(256), 0, s>>>(a);
+  const uint32_t grid = std::min((a.T + 4 * kGradWaves - 1) / (4 * kGradWaves), kGradGrid);
+  const size_t lds = a.ids ? (size_t)kGradWaves * 4 * 2 * a.E * 4 : 0;  // 64 KB at 512 experts
+  route_grad_kernel<NV><<<dim3(grid), dim3(64 * kGradWaves), lds, s>>>(a);
   return hipGetLastError();
+}
+
+// f(NV) for the logits a lane holds
+template <class F>
+hipError_t for_experts(uint32_t E, F&& f) {
+  using std::integral_constant;
+  if (E <= 32) return f(integral_constant<int, 2>{});
+  if (E <= 64) return f(integral_constant<int, 4>{});
+  if (E <= 128) return f(integral_constant<int, 8>{});
+  if (E <= 160) return f(integral_constant<int, 10>{});
+  if (E <= 192) return f(integral_constant<int, 12>{});
+  if (E <= 256) return f(integral_constant<int, 16>{});
+  return f(integral_constant<int, 32>{});
 }
 
 }  // namespace
@@ -303,15 +376,10 @@ hipError_t launch_balance(const void* logits, bool bf16, const int32_t* ids, int
                           void* workspace, float coef, uint32_t T, uint32_t E, uint32_t top_k, hipStream_t s) {
   const BalanceArgs a{logits, ids, counts, prob, loss, static_cast<uint32_t*>(workspace), coef, T, E, top_k,
                       balance_blocks(T), bf16};
-  hipError_t e;
-  if (E <= 64) e = launch_balance_nv<1>(a, s);
-  else if (E <= 128) e = launch_balance_nv<2>(a, s);
-  else if (E <= 192) e = launch_balance_nv<3>(a, s);
-  else if (E <= 256) e = launch_balance_nv<4>(a, s);
-  else e = launch_balance_nv<8>(a, s);
+  const hipError_t e = for_experts(E, [&](auto nv) { return launch_balance_nv<decltype(nv)::value>(a, s); });
   if (e != hipSuccess || a.blocks == 1) return e;
-  const uint32_t EB = E + 1, slices = kThreads / EB;  // E <= 512
-  balance_sum_kernel<<<dim3(1), dim3(kThreads), (size_t)(1 + 2 * slices) * EB * 4, s>>>(a);
+  const uint32_t R = 2 * (E + 1), slices = std::max(1u, kThreads / R);
+  balance_sum_kernel<<<dim3(1), dim3(kThreads), (size_t)slices * R * 4, s>>>(a, slices);
   return hipGetLastError();
 }
 
@@ -319,11 +387,7 @@ hipError_t launch_route_grad(const void* logits, bool bf16, const int32_t* ids, 
                              const int32_t* counts, const float* dloss, void* dlogits, float coef, uint32_t T,
                              uint32_t E, uint32_t top_k, bool renorm, hipStream_t s) {
   const RouteGradArgs a{logits, ids, dweights, counts, dloss, dlogits, coef, T, E, top_k, bf16, renorm};
-  if (E <= 64) return launch_grad_nv<1>(a, s);
-  if (E <= 128) return launch_grad_nv<2>(a, s);
-  if (E <= 192) return launch_grad_nv<3>(a, s);
-  if (E <= 256) return launch_grad_nv<4>(a, s);
-  return launch_grad_nv<8>(a, s);
+  return for_experts(E, [&](auto nv) { return launch_grad_nv<decltype(nv)::value>(a, s); });
 }
 
 }  // namespace fp8q
