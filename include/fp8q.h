@@ -787,7 +787,8 @@ fp8q_status fp8q_quant_act_dual(const uint16_t *x_bf16, uint8_t *q_e4m3, float *
  *   dx_bf16   [M,K] out
  *   workspace fp8q_gemm_dgrad_workspace_bytes(M, N, K) bytes (may be NULL when that
  *             is 0); contents undefined on return; calls in flight must not share it
- * Accumulation, reproducibility and errors as fp8q_gemm_blockscaled. */
+ * N % 128 == 0, K % 128 == 0; ceil128(M)*N, ceil128(M)*K and N*K below 2^32.  M == 0:
+ * nothing.  Accumulation, reproducibility and errors as fp8q_gemm_blockscaled. */
 fp8q_status fp8q_gemm_dgrad(const uint8_t *dy_e4m3, const float *dy_scale_km,
                             const uint8_t *w_e4m3, const float *w_scale,
                             uint16_t *dx_bf16, void *workspace, size_t workspace_bytes,
@@ -801,7 +802,7 @@ size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
  *             fp8q_quant_act_dual
  *   dw_bf16   [N,K] out (M == 0: zeros)
  *   workspace fp8q_gemm_wgrad_workspace_bytes(M, N, K) bytes, as above
- * N % 128 == 0, K % 128 == 0; element counts below 2^32.  The FP8 matrix instruction
+ * Limits as for fp8q_gemm_dgrad.  The FP8 matrix instruction
  * sums a 128-token block to about 16 bits and adds the blocks in fp32: 1.5e-5 of the
  * result's norm, a hundredth of the bf16 rounding.  Reproducible run to run. */
 fp8q_status fp8q_gemm_wgrad(const uint8_t *dy_tok, const uint8_t *dy_exp,

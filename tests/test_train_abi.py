@@ -132,11 +132,12 @@ def test_route_grad_refusals():
     assert call(T=0, lo=None, dl=None) == 0
 
 
-def test_binding_refuses_wrong_tensors():
-    """Types and shapes are checked before the device (CPU tensors here)."""
+def test_binding_refuses_cpu_tensors():
     x, w = torch.zeros(4, 256, dtype=torch.bfloat16), torch.zeros(256, dtype=torch.bfloat16)
     q, s = torch.zeros(4, 256, dtype=torch.uint8), torch.zeros(2, 16)
-    with pytest.raises(TypeError, match="x must be"):
-        fp8q.fp8q_add_rmsnorm_quant(x.float(), None, w, None, None, q, None, s, None)
+    with pytest.raises(ValueError, match="current GPU"):
+        fp8q.fp8q_add_rmsnorm_quant(x, None, w, None, None, q, None, s, None)
     with pytest.raises(ValueError, match="current GPU"):
         fp8q.fp8q_quant_act_dual(x, None, None, q, torch.zeros(1, 256, 4, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="2-d"):
+        fp8q.fp8q_quant_act_dual(x[0], None, None, q, torch.zeros(1, 256, 4, dtype=torch.uint8))

@@ -615,27 +615,39 @@ _I32 = frozenset((torch.int32,))
 _U8 = frozenset((torch.uint8,))
 
 
-def _arg(t, dtypes, shape, what) -> int:
-    """Pointer of a tensor of one of `dtypes` and of `shape`, contiguous and on the
-    current device (whose stream the call goes to)."""
+def _device(t, what) -> int:
+    """The device of a call's first tensor, which has to be the current one (the call goes
+    to its stream)."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{what} must be on the current GPU, got {t.device}")
+    return dev
+
+
+def _arg(t, dtypes, shape, what, dev) -> int:
+    """Pointer of a contiguous tensor of one of `dtypes`, of `shape` and on device `dev`."""
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtypes, shape, what, dev)
+    return t.data_ptr()
+
+
+def _refuse(t, dtypes, shape, what, dev):
     if t.dtype not in dtypes:
         _wrong_type(**{what: (t, dtypes)})
     if t.shape != shape:
         raise ValueError(f"{what} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{what} must be on the current GPU, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current GPU, cuda:{dev}, got {t.device}")
+    raise ValueError(f"{what} must be contiguous")
 
 
-def _oarg(t, dtypes, shape, what) -> int:
-    return 0 if t is None else _arg(t, dtypes, shape, what)
+def _oarg(t, dtypes, shape, what, dev) -> int:
+    return 0 if t is None else _arg(t, dtypes, shape, what, dev)
 
 
-def _work(t):
+def _work(t, dev):
     """(pointer, bytes) of a workspace."""
-    return (0, 0) if t is None else (_arg(t, _U8, t.shape, "workspace"), t.numel())
+    return (0, 0) if t is None else (_arg(t, _U8, t.shape, "workspace", dev), t.numel())
 
 
 def fp8q_add_rmsnorm_quant(x, residual, weight, h, y, q, scale_rm, scale_km, rstd, eps: float = 1e-6, stream=None):
@@ -644,12 +656,14 @@ def fp8q_add_rmsnorm_quant(x, residual, weight, h, y, q, scale_rm, scale_km, rst
     bf16, rstd [M] float32 = 1 / sqrt(mean(h^2) + eps).  residual and h go together
     (None: h is x); y, rstd and one of the scales may be None."""
     M, K = shape = _dims(x, 2)
+    dev = _device(x, "x")
     _check(lib().fp8q_add_rmsnorm_quant(
-        _arg(x, _BF16, shape, "x"), _oarg(residual, _BF16, shape, "residual"), _arg(weight, _BF16, (K,), "weight"),
-        _oarg(h, _BF16, shape, "h"), _oarg(y, _BF16, shape, "y"), _arg(q, _E4M3, shape, "q"),
-        _oarg(scale_rm, _F32, (M, K // 128), "scale_rm"),
-        _oarg(scale_km, _F32, (K // 128, (M + 15) // 16 * 16), "scale_km"), _oarg(rstd, _F32, (M,), "rstd"), eps, M, K,
-        _stream(stream)))
+        _arg(x, _BF16, shape, "x", dev), _oarg(residual, _BF16, shape, "residual", dev),
+        _arg(weight, _BF16, (K,), "weight", dev),
+        _oarg(h, _BF16, shape, "h", dev), _oarg(y, _BF16, shape, "y", dev), _arg(q, _E4M3, shape, "q", dev),
+        _oarg(scale_rm, _F32, (M, K // 128), "scale_rm", dev),
+        _oarg(scale_km, _F32, (K // 128, (M + 15) // 16 * 16), "scale_km", dev),
+        _oarg(rstd, _F32, (M,), "rstd", dev), eps, M, K, _stream(stream)))
 
 
 def fp8q_add_rmsnorm_grad_workspace_bytes(M: int, K: int) -> int:
@@ -661,11 +675,13 @@ def fp8q_add_rmsnorm_grad(dy, dh, h, weight, rstd, dx, dweight, workspace, strea
     from dy (of y) and dh (of h; None: none), dweight [K] float32; workspace: a uint8
     tensor of fp8q_add_rmsnorm_grad_workspace_bytes(M, K)."""
     M, K = shape = _dims(h, 2)
-    work, nbytes = _work(workspace)
+    dev = _device(h, "h")
+    work, nbytes = _work(workspace, dev)
     _check(lib().fp8q_add_rmsnorm_grad(
-        _arg(dy, _BF16, shape, "dy"), _oarg(dh, _BF16, shape, "dh"), _arg(h, _BF16, shape, "h"),
-        _arg(weight, _BF16, (K,), "weight"), _arg(rstd, _F32, (M,), "rstd"), _arg(dx, _BF16, shape, "dx"),
-        _arg(dweight, _F32, (K,), "dweight"), work, nbytes, M, K, _stream(stream)))
+        _arg(dy, _BF16, shape, "dy", dev), _oarg(dh, _BF16, shape, "dh", dev), _arg(h, _BF16, shape, "h", dev),
+        _arg(weight, _BF16, (K,), "weight", dev), _arg(rstd, _F32, (M,), "rstd", dev),
+        _arg(dx, _BF16, shape, "dx", dev),
+        _arg(dweight, _F32, (K,), "dweight", dev), work, nbytes, M, K, _stream(stream)))
 
 
 def fp8q_quant_act_dual(x, q, scale_km, q_tok, exp_tok, stream=None):
@@ -673,10 +689,12 @@ def fp8q_quant_act_dual(x, q, scale_km, q_tok, exp_tok, stream=None):
     both None: not wanted) and along its tokens (q_tok [M,K], exp_tok
     [ceil(M/512),K,4] uint8)."""
     M, K = shape = _dims(x, 2)
+    dev = _device(x, "x")
     _check(lib().fp8q_quant_act_dual(
-        _arg(x, _BF16, shape, "x"), _oarg(q, _E4M3, shape, "q"),
-        _oarg(scale_km, _F32, (K // 128, (M + 15) // 16 * 16), "scale_km"), _arg(q_tok, _E4M3, shape, "q_tok"),
-        _arg(exp_tok, _U8, ((M + 511) // 512, K, 4), "exp_tok"), M, K, _stream(stream)))
+        _arg(x, _BF16, shape, "x", dev), _oarg(q, _E4M3, shape, "q", dev),
+        _oarg(scale_km, _F32, (K // 128, (M + 15) // 16 * 16), "scale_km", dev),
+        _arg(q_tok, _E4M3, shape, "q_tok", dev),
+        _arg(exp_tok, _U8, ((M + 511) // 512, K, 4), "exp_tok", dev), M, K, _stream(stream)))
 
 
 def fp8q_gemm_dgrad_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -688,12 +706,13 @@ def fp8q_gemm_dgrad(dy, dy_scale_km, w, w_scale, dx, workspace, stream=None):
     the forward call reads it); workspace: a uint8 tensor of
     fp8q_gemm_dgrad_workspace_bytes(M, N, K), or None when that is 0."""
     M, N = shape = _dims(dy, 2)
+    dev = _device(dy, "dy")
     K = _dims(w, 2)[1]
-    work, nbytes = _work(workspace)
+    work, nbytes = _work(workspace, dev)
     _check(lib().fp8q_gemm_dgrad(
-        _arg(dy, _E4M3, shape, "dy"), _arg(dy_scale_km, _F32, (N // 128, (M + 15) // 16 * 16), "dy_scale_km"),
-        _arg(w, _E4M3, (N, K), "w"), _arg(w_scale, _F32, (N // 128, K // 128), "w_scale"),
-        _arg(dx, _BF16, (M, K), "dx"), work, nbytes, M, N, K, _stream(stream)))
+        _arg(dy, _E4M3, shape, "dy", dev), _arg(dy_scale_km, _F32, (N // 128, (M + 15) // 16 * 16), "dy_scale_km", dev),
+        _arg(w, _E4M3, (N, K), "w", dev), _arg(w_scale, _F32, (N // 128, K // 128), "w_scale", dev),
+        _arg(dx, _BF16, (M, K), "dx", dev), work, nbytes, M, N, K, _stream(stream)))
 
 
 def fp8q_gemm_wgrad_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -705,12 +724,14 @@ def fp8q_gemm_wgrad(dy_tok, dy_exp, x_tok, x_exp, dw, workspace, stream=None):
     fp8q_quant_act_dual's token codes and bytes; workspace: a uint8 tensor of
     fp8q_gemm_wgrad_workspace_bytes(M, N, K), or None when that is 0."""
     M, N = shape = _dims(dy_tok, 2)
+    dev = _device(dy_tok, "dy_tok")
     K = _dims(x_tok, 2)[1]
     packs = (M + 511) // 512
-    work, nbytes = _work(workspace)
+    work, nbytes = _work(workspace, dev)
     _check(lib().fp8q_gemm_wgrad(
-        _arg(dy_tok, _E4M3, shape, "dy_tok"), _arg(dy_exp, _U8, (packs, N, 4), "dy_exp"),
-        _arg(x_tok, _E4M3, (M, K), "x_tok"), _arg(x_exp, _U8, (packs, K, 4), "x_exp"), _arg(dw, _BF16, (N, K), "dw"),
+        _arg(dy_tok, _E4M3, shape, "dy_tok", dev), _arg(dy_exp, _U8, (packs, N, 4), "dy_exp", dev),
+        _arg(x_tok, _E4M3, (M, K), "x_tok", dev), _arg(x_exp, _U8, (packs, K, 4), "x_exp", dev),
+        _arg(dw, _BF16, (N, K), "dw", dev),
         work, nbytes, M, N, K, _stream(stream)))
 
 
@@ -727,12 +748,14 @@ def fp8q_moe_balance(logits, ids, counts, prob, loss, workspace, coef: float = 1
     prob [E] and loss [1] float32; workspace: a uint8 tensor of
     fp8q_moe_balance_workspace_bytes(T, E), or None when that is 0."""
     T, E = shape = _dims(logits, 2)
+    dev = _device(logits, "logits")
     k = _dims(ids, 2)[1]
-    work, nbytes = _work(workspace)
+    work, nbytes = _work(workspace, dev)
     _check(lib().fp8q_moe_balance(
-        _arg(logits, _LOGITS, shape, "logits"), logits.dtype is torch.bfloat16, _arg(ids, _I32, (T, k), "ids"),
-        _arg(counts, _I32, (E + 1,), "counts"), _arg(prob, _F32, (E,), "prob"), _arg(loss, _F32, (1,), "loss"), work,
-        nbytes, coef, T, E, k, _stream(stream)))
+        _arg(logits, _LOGITS, shape, "logits", dev), logits.dtype is torch.bfloat16,
+        _arg(ids, _I32, (T, k), "ids", dev), _arg(counts, _I32, (E + 1,), "counts", dev),
+        _arg(prob, _F32, (E,), "prob", dev), _arg(loss, _F32, (1,), "loss", dev), work, nbytes, coef, T, E, k,
+        _stream(stream)))
 
 
 def fp8q_moe_route_grad(logits, ids, dweights, counts, dloss, dlogits, renormalize: bool = True, coef: float = 1.0,
@@ -742,14 +765,15 @@ def fp8q_moe_route_grad(logits, ids, dweights, counts, dloss, dlogits, renormali
     (counts [E+1] of fp8q_moe_balance, dloss [1] float32 or None for 1; counts None:
     not).  top_k: needed where ids is None."""
     T, E = shape = _dims(logits, 2)
+    dev = _device(logits, "logits")
     k = top_k if ids is None else _dims(ids, 2)[1]
     if k is None:
         raise ValueError("top_k is needed without ids")
     _check(lib().fp8q_moe_route_grad(
-        _arg(logits, _LOGITS, shape, "logits"), logits.dtype is torch.bfloat16, _oarg(ids, _I32, (T, k), "ids"),
-        _oarg(dweights, _F32, (T, k), "dweights"), _oarg(counts, _I32, (E + 1,), "counts"),
-        _oarg(dloss, _F32, (1,), "dloss"), _arg(dlogits, (logits.dtype,), shape, "dlogits"), coef, T, E, k,
-        bool(renormalize), _stream(stream)))
+        _arg(logits, _LOGITS, shape, "logits", dev), logits.dtype is torch.bfloat16,
+        _oarg(ids, _I32, (T, k), "ids", dev), _oarg(dweights, _F32, (T, k), "dweights", dev),
+        _oarg(counts, _I32, (E + 1,), "counts", dev), _oarg(dloss, _F32, (1,), "dloss", dev),
+        _arg(dlogits, (logits.dtype,), shape, "dlogits", dev), coef, T, E, k, bool(renormalize), _stream(stream)))
 
 
 def fp8q_default_select_params(cu_count: int) -> SelectParams:

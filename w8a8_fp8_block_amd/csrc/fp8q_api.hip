@@ -621,16 +621,17 @@ fp8q_status check_norm(const char* fn, uint32_t M, uint32_t K) {
   return FP8Q_OK;
 }
 
-// dy [M,N], x and dx [M,K], w and dw [N,K]
+// dy [M,N], x and dx [M,K], w and dw [N,K].  (Whole token blocks: the kernels' 32-bit
+// offsets run to the end of the last one.)
 bool grad_shape(uint32_t M, uint32_t N, uint32_t K) {
-  const uint64_t Mp = ((uint64_t)M + 15) / 16 * 16;  // (m_pad16 would wrap for M near 2^32)
+  const uint64_t Mp = ((uint64_t)M + 127) / 128 * 128;
   return N && K && N % kGroup == 0 && K % kGroup == 0 && Mp * N <= kMaxElems && Mp * K <= kMaxElems &&
          (uint64_t)N * K <= kMaxElems;
 }
 fp8q_status check_grad(const char* fn, uint32_t M, uint32_t N, uint32_t K) {
   if (grad_shape(M, N, K)) return FP8Q_OK;
   return fail(FP8Q_ERR_SHAPE,
-              "%s: M=%u N=%u K=%u (N and K positive multiples of 128; ceil16(M)*N, ceil16(M)*K and N*K up to 2^32-1)",
+              "%s: M=%u N=%u K=%u (N and K positive multiples of 128; ceil128(M)*N, ceil128(M)*K and N*K up to 2^32-1)",
               fn, M, N, K);
 }
 

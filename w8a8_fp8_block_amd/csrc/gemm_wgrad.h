@@ -27,7 +27,7 @@
 // takes 256 accumulators a lane, so one wave a SIMD, which issues instructions of all
 // kinds by itself.  (Two waves of 128 x 64 a SIMD: 2634 TFLOP/s over 4096 x 4096 x
 // 18304 tokens against 2800; the same two taking turns between reading and computing:
-// 2546.  hipBLASLt's FP8 product with one scale for all, 8192^3: 2642.)
+// 2546.  A library's FP8 product with one scale for all, 8192^3: 2642.)
 //
 // The direct loads are issued in assembly (mfma_common.h says why: the waits that the
 // compiler would add cost half the speed).
@@ -78,7 +78,8 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
 // registers may be written two instructions later.)
 template <int OFF>
 __device__ __forceinline__ void store16_asm(uint64_t base, uint32_t voff, u32x4s v) {
-  asm volatile("global_store_dwordx4 %0, %1, %2 offset:%3\n\ts_nop 1" :: "v"(voff), "v"(v), "s"(base), "n"(OFF) : "memory");
+  asm volatile("global_store_dwordx4 %0, %1, %2 offset:%3\n\ts_nop 1" ::"v"(voff), "v"(v), "s"(base), "n"(OFF)
+               : "memory");
 }
 
 template <int TM_, int TN_>
@@ -289,7 +290,8 @@ __device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t uni
               unroll_seq(
                   [&](auto rc) {
                     constexpr int r = 4 * decltype(rc)::value;
-                    store16_asm<128 * j + 8 * r>(band, at, __builtin_bit_cast(u32x4s, v4f{c[r], c[r + 1], c[r + 2], c[r + 3]}));
+                    const v4f v{c[r], c[r + 1], c[r + 2], c[r + 3]};
+                    store16_asm<128 * j + 8 * r>(band, at, __builtin_bit_cast(u32x4s, v));
                   },
                   std::make_integer_sequence<int, 4>{});
             } else {

@@ -85,13 +85,18 @@ __device__ __forceinline__ u32x4s rsrc_words(const void* base, uint32_t bytes) {
   const uint64_t p = (uint64_t)base;
   return u32x4s{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
 }
+__device__ __forceinline__ uint32_t lds_address(void* lds) {
+  return (uint32_t)(size_t)(__attribute__((address_space(3))) void*)lds;
+}
 __device__ __forceinline__ void dma16(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(r), "s"(soff), "s"((uint32_t)(size_t)(__attribute__((address_space(3))) void*)lds) : "memory");
+               :: "v"(voff), "s"(r), "s"(soff), "s"(lds_address(lds))
+               : "memory");
 }
 __device__ __forceinline__ void dma4(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(r), "s"(soff), "s"((uint32_t)(size_t)(__attribute__((address_space(3))) void*)lds) : "memory");
+               :: "v"(voff), "s"(r), "s"(soff), "s"(lds_address(lds))
+               : "memory");
 }
 template <int AUX>
 __device__ __forceinline__ void dma16_aux(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
