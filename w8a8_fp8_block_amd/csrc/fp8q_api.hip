@@ -261,7 +261,9 @@ constexpr uint64_t kFusedKmajorMaxGroups = 1u << 19;
 constexpr uint32_t kTailRuleMinM = 512;  // the stream-K form from here
 constexpr uint32_t kRoundRuleMinM = 129;
 
-int rounds_kernel(uint32_t M, uint32_t N, uint32_t cus) {
+int gemm_auto_kernel(uint32_t M, uint32_t N, uint32_t cus) {
+  if (M <= kSkinnyAutoMaxM || (M <= kSkinnyWideMaxM && N <= kSkinnyWideMaxN)) return 2;
+  if (M < kRoundRuleMinM) return 1;
   const uint64_t c = cus ? cus : 1;
   const uint64_t nt = N / kGroup;
   const uint64_t t_pp = (M + 255) / 256 * nt, t_128 = (M + 127) / 128 * nt;
@@ -270,12 +272,6 @@ int rounds_kernel(uint32_t M, uint32_t N, uint32_t cus) {
   const uint64_t tail = t_128 % (2 * c);
   const uint64_t c_128 = 2 * (t_128 / (2 * c)) + (tail == 0 ? 0 : tail > c ? 2 : 1);
   return c_pp <= c_128 ? 5 : 1;
-}
-
-int gemm_auto_kernel(uint32_t M, uint32_t N, uint32_t cus) {
-  if (M <= kSkinnyAutoMaxM || (M <= kSkinnyWideMaxM && N <= kSkinnyWideMaxN)) return 2;
-  if (M < kRoundRuleMinM) return 1;
-  return rounds_kernel(M, N, cus);
 }
 
 // Split-K (fp8q_gemm_blockscaled_splitk).  Above kSplitMinM rows, wherever
@@ -635,24 +631,38 @@ fp8q_status check_grad(const char* fn, uint32_t M, uint32_t N, uint32_t K) {
               fn, M, N, K);
 }
 
-// Ranges of the sum (N) that fp8q_gemm_dgrad cuts: as many as fill two workgroups a CU
-// with 128 x 128 tiles, of 10 blocks at least (or 2, for up to 4 ranges) and 12 at most,
-// where the blocks saved, 0.7 us each, outweigh the second launch and the ranges' sums,
-// written and read at 4 TB/s.  Back to back over rotating inputs (256 CUs), us without ->
-// with: N = 17408, K = 5120: 138 -> 26 at M = 16, 144 -> 38 at 128, 137 -> 68 at 409; N =
-// 5120, K = 6144: 31 -> 14 at 16, 35 -> 19 at 128, 37 -> 35 at 409, 39 either way at 640;
-// N = 2048, K = 1408: 11.3 -> 7.8 at 16, 14.3 -> 14.1 at 409, 14.5 without at 640 (16.1
-// with); more ranges than fill the device were slower throughout.
-constexpr uint64_t kGradSplitMax = 12, kGradBlockNs = 700, kGradSplitNs = 2200, kGradBytesNs = 4000;
+// fp8q_gemm_dgrad's tiles (128 or 256 rows x 128 columns, one workgroup a CU) and the ranges
+// of the sum (N) that it cuts, as many as leave each workgroup a CU, of 10 blocks at least (or
+// 2, for up to 4 ranges) and 12 at most: whichever of the four takes least by the estimate
+// 0.6 or 0.85 us a block and, for ranges, the second launch and their sums, written and read
+// at 4 TB/s.  More tiles of 128 rows than CUs: 256 rows, uncut.  Back to back over rotating
+// inputs (256 CUs), us: N = 17408, K = 5120: 85 uncut, 25 in 6 ranges at M = 16; 105 and 32
+// at 128; 91 uncut, 77 in 3 ranges of 128-row tiles, 57 in 3 of 256-row ones at 409; 172 with
+// 128 rows, 123 with 256 at 1168; 450 and 349 at 4576.  N = 5120, K = 6144: 20 uncut, 12 in 4
+// ranges at 16; 27 uncut, 38 in 2 ranges (more workgroups than CUs) and 31 in 2 of 256-row
+// tiles at 409.  N = 2048, K = 1408: 9.3 and 7.9 (4 ranges) at 16, 10.8 and 12.5 (2) at 409.
+struct DgradPlan {
+  bool wide;
+  uint32_t splits;
+};
+constexpr uint64_t kGradSplitMax = 12, kGradBlockNs[2] = {600, 850}, kGradSplitNs = 5500, kGradBytesNs = 4000;
 
-uint32_t dgrad_splits(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
-  const uint64_t tiles = (uint64_t)((M + 127) / 128) * (K / kGroup), blocks = N / kGroup;
-  if (tiles == 0) return 1;
+DgradPlan dgrad_plan(uint32_t M, uint32_t N, uint32_t K, uint32_t cus) {
+  const uint64_t blocks = N / kGroup, columns = K / kGroup;
+  DgradPlan best{true, 1};
+  if (M == 0 || ((uint64_t)M + 127) / 128 * columns > cus) return best;
   const uint64_t cap = std::min(std::max(blocks / 10, std::min<uint64_t>(4, blocks / 2)), kGradSplitMax);
-  const uint64_t s = std::min<uint64_t>(2ull * cus / tiles, cap);
-  if (s < 2) return 1;
-  const uint64_t saved = kGradBlockNs * (blocks - blocks / s);
-  return saved > kGradSplitNs + s * M * K * 8 / kGradBytesNs ? (uint32_t)s : 1;
+  uint64_t least = UINT64_MAX;
+  for (int wide = 0; wide < 2; ++wide) {
+    const uint64_t rows = wide ? 256 : 128, tiles = (M + rows - 1) / rows * columns;
+    const uint64_t most = std::max<uint64_t>(std::min<uint64_t>(cus / tiles, cap), 1);
+    for (const uint64_t s : {uint64_t{1}, most}) {
+      const uint64_t sums = s < 2 ? 0 : kGradSplitNs + s * M * K * 8 / kGradBytesNs;
+      const uint64_t ns = kGradBlockNs[wide] * ((blocks + s - 1) / s) + sums;
+      if (ns < least) least = ns, best = {wide != 0, (uint32_t)s};
+    }
+  }
+  return best;
 }
 
 // Ranges of the tokens that fp8q_gemm_wgrad cuts: where 128 x 128 tiles are few, as many
@@ -1084,19 +1094,18 @@ fp8q_status fp8q_gemm_dgrad(const uint8_t* dy_e4m3, const float* dy_scale_km, co
   REQUIRE_PTR(w_e4m3);
   REQUIRE_PTR(w_scale);
   REQUIRE_PTR(dx_bf16);
-  const uint32_t cus = current_cus(), splits = dgrad_splits(M, N, K, cus);
-  st = check_workspace(fn, workspace, workspace_bytes, splitk_workspace(M, K, splits));
+  const DgradPlan plan = dgrad_plan(M, N, K, current_cus());
+  st = check_workspace(fn, workspace, workspace_bytes, splitk_workspace(M, K, plan.splits));
   if (st != FP8Q_OK) return st;
   st = check_device(fn);
   if (st != FP8Q_OK) return st;
   return launched(fn, launch_gemm_dgrad(dy_e4m3, dy_scale_km, w_e4m3, w_scale, dx_bf16,
-                                        static_cast<float*>(workspace), M, N, K, splits,
-                                        rounds_kernel(M, K, cus), cus, stream));
+                                        static_cast<float*>(workspace), M, N, K, plan.wide, plan.splits, stream));
 }
 
 size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K) {
   if (!grad_shape(M, N, K) || M == 0) return 0;
-  return (size_t)splitk_workspace(M, K, dgrad_splits(M, N, K, current_cus()));
+  return (size_t)splitk_workspace(M, K, dgrad_plan(M, N, K, current_cus()).splits);
 }
 
 fp8q_status fp8q_gemm_wgrad(const uint8_t* dy_tok, const uint8_t* dy_exp, const uint8_t* x_tok,

@@ -220,12 +220,11 @@ hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16
 hipError_t launch_quant_dual(const uint16_t* x, uint8_t* q, float* scale_km, uint8_t* q_tok, uint8_t* exp_tok,
                              uint32_t M, uint32_t K, hipStream_t s);
 // Gradients of the block-scaled product (dgrad.hip, wgrad.hip): dx [M,K] from row codes dy
-// [M,N] and w [N,K]; dw [N,K] from token codes dy [M,N] and x [M,K].  splits >= 2:
-// the sum cut into as many ranges, their fp32 results in part; else dgrad's kernel 5 is
-// the 256 x 128 ping-pong one, 1 that of 128 x 128 tiles.
+// [M,N] and w [N,K]; dw [N,K] from token codes dy [M,N] and x [M,K].  splits >= 2: the sum
+// cut into as many ranges, their fp32 results in part.  wide: dx in tiles of 256 rows, not 128.
 hipError_t launch_gemm_dgrad(const uint8_t* dy, const float* dy_s_km, const uint8_t* w, const float* w_s, uint16_t* dx,
-                             float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, int kernel,
-                             uint32_t cus, hipStream_t s);
+                             float* part, uint32_t M, uint32_t N, uint32_t K, bool wide, uint32_t splits,
+                             hipStream_t s);
 hipError_t launch_gemm_wgrad(const uint8_t* dy, const uint8_t* ey, const uint8_t* x, const uint8_t* ex, uint16_t* dw,
                              float* part, uint32_t M, uint32_t N, uint32_t K, uint32_t splits, uint32_t cus,
                              hipStream_t s);

@@ -201,9 +201,7 @@ __device__ __forceinline__ void ffn_epilogue(const v4f (&acc)[TM][TN], uint8_t* 
   ffn_codes<TN>(hb, amax, rmax, ffn, wave, lane, mrow0, ncol0, nb, M, N, pad_end);
 }
 
-// WT: as in the tiled kernel (gemm_tile.h): weights [K, N], block scales
-// [K/128, N/128], fragments through the transposing LDS read.
-template <int STAGES, bool ROW, bool FFN, class Rows, class Epi, bool WT = false>
+template <int STAGES, bool ROW, bool FFN, class Rows, class Epi>
 __device__ __forceinline__ void gemm_pp_body(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t m0, uint32_t n0, uint32_t N,
@@ -211,7 +209,6 @@ __device__ __forceinline__ void gemm_pp_body(
   using C = PpCfg<STAGES, ROW, FFN>;
   constexpr int TM = C::TM, TN = C::TN, NP = C::NP;
   constexpr int CH0 = C::CH0, CH1 = C::CH1, LW0 = C::LW0, LW1 = C::LW1;
-  static_assert(!WT || (!FFN && !ROW), "plain block-scaled weights");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
   const uint32_t tid = threadIdx.x, lane = tid & 63;
@@ -224,13 +221,13 @@ __device__ __forceinline__ void gemm_pp_body(
   const uint32_t G = K / kGroup;
   const uint32_t nb = n0 / kGroup;
 
-  const auto rA = rsrc_for<WT>(A, rows.total * K);
-  const auto rW = rsrc_for<WT>(W, N * K);
-  const auto rS = rsrc_for<WT>(As, G * Mp * 4);
-  const auto rWs = rsrc_for<WT>(Ws, ROW ? N * 4 : (N / kGroup) * G * 4);
+  const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, rows.total * K);
+  const __amdgpu_buffer_rsrc_t rW = make_rsrc(W, N * K);
+  const __amdgpu_buffer_rsrc_t rS = make_rsrc(As, G * Mp * 4);
+  const __amdgpu_buffer_rsrc_t rWs = make_rsrc(Ws, ROW ? N * 4 : (N / kGroup) * G * 4);
   // FFN mode: the up weights and their scales
-  const auto rW2 = FFN ? rsrc_for<WT>(ffn.w_up, N * K) : rW;
-  const auto rWs2 = FFN ? rsrc_for<WT>(ffn.ws_up, (N / kGroup) * G * 4) : rWs;
+  const __amdgpu_buffer_rsrc_t rW2 = FFN ? make_rsrc(ffn.w_up, N * K) : rW;
+  const __amdgpu_buffer_rsrc_t rWs2 = FFN ? make_rsrc(ffn.ws_up, (N / kGroup) * G * 4) : rWs;
 
   // Operand chunks of this wave (LDS chunk c covers 8 rows of 128 bytes:
   // activations first, then weights; FFN mode: activations 0-15, gate
@@ -264,13 +261,11 @@ __device__ __forceinline__ void gemm_pp_body(
     const uint32_t row = ch * 8 + (lane >> 3), col = lane & 7;  // row within the operand
     c_lds[j] = c;
     c_off[j] = act ? rows.src(min(m0 + row, M - 1)) * K + (col ^ swz(row)) * 16
-               : WT ? row * N + n0 + (col ^ swz_t(row)) * 16
-                    : (n0 + row) * K + (col ^ swz(row)) * 16;  // swz: low 4 bits of the LDS row
+                   : (n0 + row) * K + (col ^ swz(row)) * 16;  // swz: low 4 bits of the LDS row
   }
   const uint32_t s_off = rows.scale_slot(m0 + wm * C::WM + lane, Mp) * 4;       // own activation scales
   const uint32_t s_off_p = rows.scale_slot(m0 + (gw >> 1) * C::WM + lane, Mp) * 4;  // partner's (group 1)
-  const uint32_t ws_off = nb * (WT ? 4 : G * 4), ws_step = WT ? N / kGroup * 4 : 4;
-  const uint32_t g0_step = WT && !g0_act ? kGroup * N : kGroup;  // bytes a K block, group 0's operand
+  const uint32_t ws_off = nb * G * 4;
   const uint32_t my_sc = C::A_BYTES + C::W_BYTES + wave * C::SCW_BYTES;
   const uint32_t p_sc = C::A_BYTES + C::W_BYTES + gw * C::SCW_BYTES;
 
@@ -282,7 +277,7 @@ __device__ __forceinline__ void gemm_pp_body(
           if constexpr (FFN)
             dma16(J < 4 ? rA : rW2, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
           else
-            dma16(g0_act ? rA : rW, c_off[J], kb * g0_step, base + c_lds[J] * 1024);
+            dma16(g0_act ? rA : rW, c_off[J], kb * kGroup, base + c_lds[J] * 1024);
         },
         std::make_integer_sequence<int, CH0>{});
   };
@@ -297,8 +292,8 @@ __device__ __forceinline__ void gemm_pp_body(
     dma4(rS, s_off, kb * Mp * 4, base + my_sc);
     dma4(rS, s_off_p, kb * Mp * 4, base + p_sc);
     if constexpr (!ROW) {
-      dma4(FFN ? rWs2 : rWs, ws_off, kb * ws_step, base + my_sc + 256);  // up scales in FFN mode
-      dma4(rWs, ws_off, kb * ws_step, base + p_sc + 256);
+      dma4(FFN ? rWs2 : rWs, ws_off, kb * 4, base + my_sc + 256);  // up scales in FFN mode
+      dma4(rWs, ws_off, kb * 4, base + p_sc + 256);
     }
   };
 
@@ -307,10 +302,7 @@ __device__ __forceinline__ void gemm_pp_body(
   const uint32_t lo1 = l16 * 128 + (((c0 + 1) ^ swz(l16)) * 16);
   auto ld16 = [](const uint8_t* p) -> v4i { return *reinterpret_cast<const v4i*>(p); };
   auto ldf = [](const uint8_t* p) -> float { return *reinterpret_cast<const float*>(p); };
-  const uint32_t a_row0 = wm * C::WM * 128, w_row0 = C::A_BYTES + (WT ? 0 : wn * C::WN * 128);
-  uint32_t lt[TN];  // transposed fragments' lane offsets
-#pragma unroll
-  for (int tn = 0; tn < TN; ++tn) lt[tn] = transposed_lane(lane) ^ ((wn * TN + tn) * 16);
+  const uint32_t a_row0 = wm * C::WM * 128, w_row0 = C::A_BYTES + wn * C::WN * 128;
 
   v4f acc[TM][TN];
 #pragma unroll
@@ -338,8 +330,8 @@ __device__ __forceinline__ void gemm_pp_body(
     const uint8_t* sb = smem + decltype(slot_c)::value * C::STAGE_BYTES;
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn) {
-      bf[tn].lo = WT ? ld_transposed(sb + w_row0 + lt[tn], 0) : ld16(sb + w_row0 + tn * 2048 + lo0);
-      bf[tn].hi = WT ? ld_transposed(sb + w_row0 + lt[tn], 1) : ld16(sb + w_row0 + tn * 2048 + lo1);
+      bf[tn].lo = ld16(sb + w_row0 + tn * 2048 + lo0);
+      bf[tn].hi = ld16(sb + w_row0 + tn * 2048 + lo1);
     }
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {

@@ -94,13 +94,8 @@ struct TileCfg {
 // Rows (gemm_rows.h) says which activation rows a tile's output rows read and
 // where its rows end; Epi adds to the finished accumulators before the store
 // (NoEpilogue: nothing).  The tile is rows m0.. and columns n0.. .
-//
-// WT: the weights lie [K, N], the sum's index along their rows (the gradient's
-// product with W in its forward layout), with block scales [K/128, N/128].  A
-// stage then holds 128 of the sum's rows x BN columns of them, and the fragments
-// come through the transposing LDS read (ld_transposed).
 template <int BM, int BN, int WGM, int WGN, int STAGES, bool ROW, bool SPLIT, class Rows, class Epi,
-          int WAUX = 0, bool WT = false>
+          int WAUX = 0>
 __device__ __forceinline__ void gemm_tiled_body(
     const uint8_t* __restrict__ A, const float* __restrict__ As, const uint8_t* __restrict__ W,
     const float* __restrict__ Ws, uint16_t* __restrict__ out, uint32_t m0, uint32_t n0, uint32_t N,
@@ -109,7 +104,6 @@ __device__ __forceinline__ void gemm_tiled_body(
   using C = TileCfg<BM, BN, WGM, WGN, STAGES, ROW>;
   constexpr int TM = C::TM, TN = C::TN, NP = C::NP;
   static_assert(!(SPLIT && ROW), "split-K for block-scaled weights only");
-  static_assert(!WT || (BN == 128 && !ROW), "one 128-column panel of weights");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
   const uint32_t tid = threadIdx.x, lane = tid & 63;
@@ -124,10 +118,10 @@ __device__ __forceinline__ void gemm_tiled_body(
   const uint32_t nb = (n0 + wn * C::WN) / kGroup;  // this wave's weight-scale block row
 
   // ---- buffer resources and per-lane source offsets (K block 0) ----
-  const auto rA = rsrc_for<WT>(A, rows.total * K);
-  const auto rW = rsrc_for<WT>(W, N * K);
-  const auto rS = rsrc_for<WT>(As, GK * Mp * 4);
-  const auto rWs = rsrc_for<WT>(Ws, ROW ? N * 4 : (N / kGroup) * GK * 4);
+  const __amdgpu_buffer_rsrc_t rA = make_rsrc(A, rows.total * K);
+  const __amdgpu_buffer_rsrc_t rW = make_rsrc(W, N * K);
+  const __amdgpu_buffer_rsrc_t rS = make_rsrc(As, GK * Mp * 4);
+  const __amdgpu_buffer_rsrc_t rWs = make_rsrc(Ws, ROW ? N * 4 : (N / kGroup) * GK * 4);
   uint32_t a_off[C::DA], w_off[C::DW], s_off[C::SA];
 #pragma unroll
   for (int j = 0; j < C::DA; ++j) {
@@ -137,14 +131,13 @@ __device__ __forceinline__ void gemm_tiled_body(
 #pragma unroll
   for (int j = 0; j < C::DW; ++j) {
     const uint32_t c = (wave * C::DW + j) * 64 + lane, row = c >> 3;
-    w_off[j] = WT ? row * N + n0 + ((c & 7) ^ swz_t(row)) * 16 : (n0 + row) * K + ((c & 7) ^ swz(row)) * 16;
+    w_off[j] = (n0 + row) * K + ((c & 7) ^ swz(row)) * 16;
   }
   // activation scales of this wave's rows (rows past Mp are clamped in
   // bounds and never used; rows in [M, Mp) hold the layout's zero pad)
 #pragma unroll
   for (int j = 0; j < C::SA; ++j) s_off[j] = rows.scale_slot(m0 + wm * C::WM + j * 64 + lane, Mp) * 4;
-  const uint32_t ws_off = nb * (WT ? 4 : GK * 4);  // every lane loads the same weight scale
-  const uint32_t w_step = WT ? kGroup * N : kGroup, ws_step = WT ? N / kGroup * 4 : 4;  // bytes a K block
+  const uint32_t ws_off = nb * GK * 4;  // every lane loads the same weight scale
   const uint32_t sc_base = C::A_BYTES + C::W_BYTES + wave * C::SCW_BYTES;
   const uint32_t ws_base = sc_base + C::SA * 256;
 
@@ -156,10 +149,10 @@ __device__ __forceinline__ void gemm_tiled_body(
     for (int j = 0; j < C::DA; ++j) dma16(rA, a_off[j], kb * kGroup, base + (wave * C::DA + j) * 1024);
 #pragma unroll
     for (int j = 0; j < C::DW; ++j)
-      dma16_aux<WAUX>(rW, w_off[j], kb * w_step, base + C::A_BYTES + (wave * C::DW + j) * 1024);
+      dma16_aux<WAUX>(rW, w_off[j], kb * kGroup, base + C::A_BYTES + (wave * C::DW + j) * 1024);
 #pragma unroll
     for (int j = 0; j < C::SA; ++j) dma4(rS, s_off[j], kb * Mp * 4, base + sc_base + j * 256);
-    if constexpr (!ROW) dma4(rWs, ws_off, kb * ws_step, base + ws_base);
+    if constexpr (!ROW) dma4(rWs, ws_off, kb * 4, base + ws_base);
   };
 
   // Per-lane byte offsets of a fragment inside a 16-row slab: this lane's row
@@ -169,13 +162,7 @@ __device__ __forceinline__ void gemm_tiled_body(
   const uint32_t lo1 = l16 * 128 + (((c0 + 1) ^ swz(l16)) * 16);
   auto ld16 = [](const uint8_t* p) -> v4i { return *reinterpret_cast<const v4i*>(p); };
   auto ldf = [](const uint8_t* p) -> float { return *reinterpret_cast<const float*>(p); };
-  const uint32_t a_row0 = wm * C::WM * 128, w_row0 = C::A_BYTES + (WT ? 0 : wn * C::WN * 128);
-  // half h (16 of this lane's 32 K elements) of weight fragment tn of the stage at sb
-  const uint32_t lt = transposed_lane(lane);
-  auto ld_w = [&](const uint8_t* sb, int tn, int h) -> v4i {
-    if constexpr (WT) return ld_transposed(sb + w_row0 + (lt ^ ((wn * C::TN + tn) * 16)), h);
-    return ld16(sb + w_row0 + tn * 2048 + (h ? lo1 : lo0));
-  };
+  const uint32_t a_row0 = wm * C::WM * 128, w_row0 = C::A_BYTES + wn * C::WN * 128;
 
   v4f acc[TM][TN];
 #pragma unroll
@@ -204,8 +191,8 @@ __device__ __forceinline__ void gemm_tiled_body(
     }
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn) {
-      bf0[tn].lo = ld_w(s0, tn, 0);
-      bf0[tn].hi = ld_w(s0, tn, 1);
+      bf0[tn].lo = ld16(s0 + w_row0 + tn * 2048 + lo0);
+      bf0[tn].hi = ld16(s0 + w_row0 + tn * 2048 + lo1);
     }
     ws0 = ROW ? 1.0f : ldf(s0 + ws_base);
   }
@@ -252,8 +239,8 @@ __device__ __forceinline__ void gemm_tiled_body(
           } else {
             constexpr int Q = I - I / TN;
             if constexpr (Q < 2 * TN) {
-              if constexpr (Q & 1) bfn[Q / 2].hi = ld_w(nx, Q / 2, 1);
-              else bfn[Q / 2].lo = ld_w(nx, Q / 2, 0);
+              if constexpr (Q & 1) bfn[Q / 2].hi = ld16(nx + w_row0 + (Q / 2) * 2048 + lo1);
+              else bfn[Q / 2].lo = ld16(nx + w_row0 + (Q / 2) * 2048 + lo0);
             } else if constexpr (Q < 2 * TN + TM / 2) {
               constexpr int T2 = 2 * (Q - 2 * TN);
               asn[T2] = ldf(nx + sc_base + (T2 * 16 + l16) * 4);

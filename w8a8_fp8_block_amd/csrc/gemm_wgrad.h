@@ -5,7 +5,7 @@
 //   dw[n,k] = sum_b 2^(ey[b,n] + ex[b,k]) * sum_{m in block b} dec(dy[m,n]) * dec(x[m,k])
 //
 // The sum runs along the rows of both matrices, so their fragments come through
-// the transposing LDS read (mfma_common.h) and no transposed copy exists.  The
+// the transposing LDS read (gemm_grad.h) and no transposed copy exists.  The
 // scales are the matrix instruction's own operands, a byte a lane: the partial
 // products need no fp32 multiply of their own and add up in the instruction's
 // accumulators (as exact as scaled fp32 additions: 1.5e-5 of the result's norm over
@@ -29,7 +29,7 @@
 // 18304 tokens against 2800; the same two taking turns between reading and computing:
 // 2546.  A library's FP8 product with one scale for all, 8192^3: 2642.)
 //
-// The direct loads are issued in assembly (mfma_common.h says why: the waits that the
+// The direct loads are issued in assembly (gemm_grad.h says why: the waits that the
 // compiler would add cost half the speed).
 //
 // Fragments of 32 columns x 64 tokens: lane l holds column l % 32, tokens
@@ -38,12 +38,11 @@
 // load as zeros.
 #pragma once
 
-#include "mfma_common.h"
+#include "gemm_grad.h"
 
 namespace fp8q {
 namespace {
 
-typedef float v16f __attribute__((ext_vector_type(16)));
 struct WgradArgs {
   const uint8_t *dy, *x;     // codes [M,N], [M,K]
   const uint32_t *ey, *ex;   // [ceil(M/512)][N], [K]: four token blocks' bytes a dword
@@ -51,36 +50,6 @@ struct WgradArgs {
   float* part;               // split form: [splits][N][K]
   uint32_t M, N, K, tiles_n, tiles_k, splits;
 };
-
-// Lanes copy 16 or 4 bytes each from base + voff + soff + OFF to lds + LDS_OFF onwards (the
-// instruction adds its offset on both sides; M0 holds no other value in the kernels that
-// use these).
-template <int OFF, int LDS_OFF>
-__device__ __forceinline__ void dma16_asm(u32x4s r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen offset:%5 lds"
-               :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(LDS_OFF - OFF), "n"(OFF) : "memory", "scc");
-}
-template <int LDS_OFF>
-__device__ __forceinline__ void dma4_asm(u32x4s r, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_add_u32 m0, %3, %4\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(LDS_OFF) : "memory", "scc");
-}
-
-// Two bf16 (round to nearest even, NaN kept) in one instruction.
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
-// 16 bytes a lane to base + voff + OFF.  (In assembly for the uniform base: with an address
-// a lane, the tile's end spills, and each reload waits for the stores.  The data's
-// registers may be written two instructions later.)
-template <int OFF>
-__device__ __forceinline__ void store16_asm(uint64_t base, uint32_t voff, u32x4s v) {
-  asm volatile("global_store_dwordx4 %0, %1, %2 offset:%3\n\ts_nop 1" ::"v"(voff), "v"(v), "s"(base), "n"(OFF)
-               : "memory");
-}
 
 template <int TM_, int TN_>
 struct WgradCfg {
@@ -295,25 +264,8 @@ __device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t uni
                   },
                   std::make_integer_sequence<int, 4>{});
             } else {
-              // Lane l holds four columns in four of each row's eight places.  The halves of
-              // the wave swap (8 columns a lane), then the odd and even 16-lane rows: a store
-              // covers 16 rows x 64 bytes, not 32 x 32.
               uint32_t v[2][4];
-              unroll_seq(
-                  [&](auto rc) {
-                    constexpr int s = decltype(rc)::value, r = 8 * s;
-                    const auto s0 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r], c[r + 1]),
-                                                                     cvt_bf16x2(c[r + 4], c[r + 5]), false, false);
-                    const auto s1 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r + 2], c[r + 3]),
-                                                                     cvt_bf16x2(c[r + 6], c[r + 7]), false, false);
-                    v[s][0] = s0[0], v[s][1] = s1[0], v[s][2] = s0[1], v[s][3] = s1[1];
-                  },
-                  std::make_integer_sequence<int, 2>{});
-#pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                const auto s = __builtin_amdgcn_permlane16_swap(v[0][d], v[1][d], false, false);
-                v[0][d] = s[0], v[1][d] = s[1];
-              }
+              tile_rows_bf16(c, v);
               store16_asm<64 * j>(band, at, u32x4s{v[0][0], v[0][1], v[0][2], v[0][3]});
               store16_asm<64 * j>(band + (uint64_t)16 * K * 2, at, u32x4s{v[1][0], v[1][1], v[1][2], v[1][3]});
             }

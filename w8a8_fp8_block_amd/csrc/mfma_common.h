@@ -76,71 +76,12 @@ __device__ __forceinline__ void dma4_at(__amdgpu_buffer_rsrc_t r, uint32_t voff,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(size_t)lds,
                                            4, voff, soff, 0, 0);
 }
-// The same in assembly, on a resource's words: for kernels that read LDS through
-// ld_transposed.  The compiler takes that read for one of any LDS in flight and would
-// wait for every direct load it knows of before it; these it does not know, and every
-// wait is the kernel's own.  (M0 holds no other value in those kernels.)
-typedef uint32_t u32x4s __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ u32x4s rsrc_words(const void* base, uint32_t bytes) {
-  const uint64_t p = (uint64_t)base;
-  return u32x4s{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, bytes, 0x00020000u};
-}
-__device__ __forceinline__ uint32_t lds_address(void* lds) {
-  return (uint32_t)(size_t)(__attribute__((address_space(3))) void*)lds;
-}
-__device__ __forceinline__ void dma16(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(r), "s"(soff), "s"(lds_address(lds))
-               : "memory");
-}
-__device__ __forceinline__ void dma4(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(r), "s"(soff), "s"(lds_address(lds))
-               : "memory");
-}
-template <int AUX>
-__device__ __forceinline__ void dma16_aux(u32x4s r, uint32_t voff, uint32_t soff, void* lds) {
-  static_assert(AUX == 0, "default cache policy");
-  dma16(r, voff, soff, lds);
-}
-// a resource for either kind
-template <bool ASM>
-__device__ __forceinline__ auto rsrc_for(const void* base, uint32_t bytes) {
-  if constexpr (ASM) return rsrc_words(base, bytes);
-  else return make_rsrc(base, bytes);
-}
-
 // LDS byte address of a pointer into a __shared__ array
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(size_t)(const __attribute__((address_space(3))) void*)p;
 }
 
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r & 7u) ^ ((r >> 3) & 1u); }
-
-// Transposing LDS reads, for a matrix whose rows are the sum's index: a panel of
-// 128 rows x 128 bytes (columns), 16-byte chunk c of row r at chunk position
-// c ^ swz_t(r).  ds_read_b64_tr_b8 takes 8 bytes from each lane of a 16-lane row
-// and gives lane l byte l % 8 of the lanes 2j + l / 8, j = 0..7: with lane 2j + h
-// at row j, bytes 8h.. of a chunk, lane l gets column l of the chunk's 16 in 8
-// rows.  Four of them, 8 rows apart, fill the 32 K elements that lane group
-// q4 = lane / 16 holds of a fragment (rows 32 q4 ..), in order.  swz_t spreads the
-// 8 rows of a 16-lane row over the 8 chunk positions, and those of the lane groups
-// q4 and q4 + 1, which are read together, over chunks of different parity.
-__device__ __forceinline__ uint32_t swz_t(uint32_t r) { return (r & 7u) ^ ((r >> 5) & 1u); }
-typedef int v2i __attribute__((ext_vector_type(2)));
-
-// This lane's byte offset in a panel for chunk 0; for chunk c, the offset ^ 16c.
-__device__ __forceinline__ uint32_t transposed_lane(uint32_t lane) {
-  const uint32_t row = 32 * (lane >> 4) + ((lane & 15) >> 1);
-  return row * 128 + swz_t(row) * 16 + (lane & 1) * 8;
-}
-// half h of the fragment whose lane offset (the chunk included) p is: 16 rows
-__device__ __forceinline__ v4i ld_transposed(const uint8_t* p, int h) {
-  typedef __attribute__((address_space(3))) v2i lds_v2i;
-  const v2i a = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(p + h * 2048));
-  const v2i b = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_v2i*)(p + h * 2048 + 1024));
-  return v4i{a.x, a.y, b.x, b.y};
-}
 
 // s_waitcnt vmcnt(n) leaving expcnt/lgkmcnt unconstrained (gfx9 encoding).
 template <int N>
@@ -174,9 +115,9 @@ __device__ __forceinline__ void unroll_seq(F&& f, std::integer_sequence<int, Is.
 // Tile t of the grouped order: tile ids walk blocks of GROUP_M tile rows, N
 // fastest inside a block, so that the tiles that run together share their
 // activation rows and weight columns.
+template <uint32_t GROUP_M = 8>
 __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t tiles_m, uint32_t tiles_n,
                                              uint32_t& tmi, uint32_t& tni) {
-  constexpr uint32_t GROUP_M = 8;
   const uint32_t per_group = GROUP_M * tiles_n;
   const uint32_t group = t / per_group, first_m = group * GROUP_M;
   const uint32_t gm = min(tiles_m - first_m, GROUP_M);
@@ -188,13 +129,14 @@ __device__ __forceinline__ void grouped_tile(uint32_t t, uint32_t tiles_m, uint3
 // dealt round-robin to the 8 XCDs; each XCD gets a contiguous run of tile
 // ids so that the tiles it runs together share its L2, and tile ids follow
 // the grouped order above.
+template <uint32_t GROUP_M = 8>
 __device__ __forceinline__ void tile_coords(uint32_t tiles_m, uint32_t tiles_n, uint32_t& tmi,
                                             uint32_t& tni) {
   const uint32_t ntiles = tiles_m * tiles_n;
   const uint32_t bid = blockIdx.x, xcd = bid & 7, slot = bid >> 3;
   const uint32_t q = ntiles >> 3, r8 = ntiles & 7;
   const uint32_t t = (xcd < r8) ? xcd * (q + 1) + slot : r8 * (q + 1) + (xcd - r8) * q + slot;
-  grouped_tile(t, tiles_m, tiles_n, tmi, tni);
+  grouped_tile<GROUP_M>(t, tiles_m, tiles_n, tmi, tni);
 }
 
 // Split-K form: the grid holds splits workgroups per tile.  Workgroup ids
