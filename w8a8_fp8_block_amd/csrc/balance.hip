@@ -81,12 +81,15 @@ __device__ __forceinline__ float exp_logits(const float (&l)[NV], uint32_t top, 
   return dpp_row_sum_f32(sum);
 }
 
+// A workgroup's sums, whole 16-byte words.
+__host__ __device__ constexpr uint32_t part_words(uint32_t E) { return (2 * (E + 1) + 3) / 4 * 4; }
+
 struct BalanceArgs {
   const void* logits;
   const int32_t* ids;
   int32_t* counts;  // [E + 1], the last one n
   float *prob, *loss;
-  uint32_t* part;  // [blocks][2][E + 1]: probability sums, counts; unused by a lone workgroup
+  uint32_t* part;  // [blocks][part_words(E)]: E + 1 probability sums, E + 1 counts; not a lone workgroup's
   float coef;
   uint32_t T, E, k, blocks;
   bool bf16;
@@ -166,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
   if (a.blocks == 1) {
     finish(a, sums, cnt, red);
   } else {
-    uint32_t* out = a.part + (uint64_t)blockIdx.x * 2 * (a.E + 1);
+    uint32_t* out = a.part + (uint64_t)blockIdx.x * part_words(a.E);
     for (uint32_t e = threadIdx.x; e <= a.E; e += kThreads) {
       out[e] = e < a.E ? __float_as_uint(sums[e]) : 0;
       out[a.E + 1 + e] = cnt[e];
@@ -175,28 +178,32 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
 }
 
 // The workgroups' sums: `slices` slices of the workgroups, each in order, then in slice
-// order.  One workgroup, bound by the latency of its loads: 32 in flight a thread.
+// order.  One workgroup, bound by the latency of its loads: 24 of 16 bytes in flight a thread,
+// one round of them for 256 workgroups of 160 experts.  (Words past the counts are never used.)
 __global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, uint32_t slices) {
-  extern __shared__ uint32_t lds[];  // [slices][2 (E + 1)], then psum and cnt in slice 0's place
+  extern __shared__ uint32_t lds[];  // [slices][part_words(E)], then psum and cnt in slice 0's place
   __shared__ float red[kWaves];
-  constexpr uint32_t kInFlight = 32;
-  const uint32_t EB = a.E + 1, R = 2 * EB;
-  for (uint32_t at = threadIdx.x; at < slices * R; at += kThreads) {
-    const uint32_t slice = at / R, c = at % R;
-    float p = 0.0f;
-    uint32_t n = 0;
+  constexpr uint32_t kInFlight = 24;
+  const uint32_t EB = a.E + 1, R = part_words(a.E), V = R / 4;
+  const u32x4* part = reinterpret_cast<const u32x4*>(a.part);
+  for (uint32_t at = threadIdx.x; at < slices * V; at += kThreads) {
+    const uint32_t slice = at / V, c = at % V;
+    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 n = {0, 0, 0, 0};
     for (uint32_t b0 = slice; b0 < a.blocks; b0 += kInFlight * slices) {
-      uint32_t v[kInFlight];
+      u32x4 v[kInFlight];
 #pragma unroll
       for (uint32_t i = 0; i < kInFlight; ++i)
-        v[i] = b0 + i * slices < a.blocks ? a.part[(uint64_t)(b0 + i * slices) * R + c] : 0;
+        v[i] = b0 + i * slices < a.blocks ? part[(uint64_t)(b0 + i * slices) * V + c] : u32x4{0, 0, 0, 0};
 #pragma unroll
       for (uint32_t i = 0; i < kInFlight; ++i) {
-        p += __uint_as_float(v[i]);
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) p[j] += __uint_as_float(v[i][j]);
         n += v[i];
       }
     }
-    lds[at] = c < EB ? __float_as_uint(p) : n;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) lds[slice * R + 4 * c + j] = 4 * c + j < EB ? __float_as_uint(p[j]) : n[j];
   }
   __syncthreads();
   for (uint32_t c = threadIdx.x; c < R; c += kThreads) {
@@ -369,7 +376,7 @@ hipError_t for_experts(uint32_t E, F&& f) {
 
 uint64_t balance_workspace_bytes(uint32_t T, uint32_t E) {
   const uint32_t blocks = balance_blocks(T);
-  return blocks > 1 ? (uint64_t)blocks * 2 * (E + 1) * 4 : 0;
+  return blocks > 1 ? (uint64_t)blocks * part_words(E) * 4 : 0;
 }
 
 hipError_t launch_balance(const void* logits, bool bf16, const int32_t* ids, int32_t* counts, float* prob, float* loss,
@@ -378,7 +385,7 @@ hipError_t launch_balance(const void* logits, bool bf16, const int32_t* ids, int
                       balance_blocks(T), bf16};
   const hipError_t e = for_experts(E, [&](auto nv) { return launch_balance_nv<decltype(nv)::value>(a, s); });
   if (e != hipSuccess || a.blocks == 1) return e;
-  const uint32_t R = 2 * (E + 1), slices = std::max(1u, kThreads / R);
+  const uint32_t R = part_words(E), slices = std::max(1u, kThreads / (R / 4));
   balance_sum_kernel<<<dim3(1), dim3(kThreads), (size_t)slices * R * 4, s>>>(a, slices);
   return hipGetLastError();
 }
