@@ -17,7 +17,9 @@
 // reductions over 64 lanes, was bound by the vector instructions: 13 us a launch at 16384
 // tokens of 160 experts, twice the present.)  Probabilities are summed in registers, then
 // over a workgroup's waves and over the workgroups in a fixed order; counts are integers,
-// so their LDS atomics give the same result in any order.
+// so their LDS atomics give the same result in any order.  16384 tokens of 160 experts, bf16
+// (5 MB, in the caches): 7.7 us, the sums' kernel 5.7, the gradient's 9.4, of which a launch
+// is 2.3 each; 25 tokens of 64: 3.2 and 3.6, one launch each.
 #include <algorithm>
 
 #include "wave_common.h"
@@ -26,8 +28,9 @@ namespace fp8q {
 namespace {
 
 constexpr uint32_t kWaves = 16, kThreads = 64 * kWaves;
-// One workgroup takes up to this many tokens alone (one launch); beyond, at least
-// kBlockTokens a workgroup and at most kMaxBlocks of them, summed by a second one.
+// One workgroup takes up to this many tokens alone (one launch; 128 tokens of 160 experts: 7.5
+// us, 8.6 by two, but 256: 11.2 and 8.8); beyond, at least kBlockTokens a workgroup and at
+// most kMaxBlocks of them (128 or 512 at 16384 tokens: within 2%), summed by a second launch.
 constexpr uint32_t kLoneTokens = 128, kBlockTokens = 64, kMaxBlocks = 256;
 
 uint32_t balance_blocks(uint32_t T) {

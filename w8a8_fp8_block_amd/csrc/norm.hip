@@ -17,7 +17,9 @@
 // Both are bound by memory: each element is loaded once into registers, reduced
 // over the row and finished from there.  A row belongs to W waves, lane t
 // holding the 8-value chunks t, t + 64 W, ...: 16 consecutive lanes hold a scale
-// group, whose maximum is one DPP reduction.
+// group, whose maximum is one DPP reduction.  4576 x 5120, inputs from HBM: 39 us with
+// residual and bf16 copy (211 MB, 5.4 TB/s; a copy of 1 GiB moves 5.1), the gradient 42 us
+// (187 MB), 39 of them in its first kernel; one token of 5120: 2.8 us, an empty launch's 2.3.
 #include <algorithm>
 
 #include "wave_common.h"
@@ -172,7 +174,8 @@ struct NormGradArgs {
 
 // Row groups of W waves take the rows g, g + groups, ... and keep their share of dw in
 // registers; the row groups of a workgroup (blockDim.x / (64 W)) meet in LDS at the end.
-// T: the workgroup's threads at most.
+// T: the workgroup's threads at most.  (dh loaded behind the row's sum where a lane holds
+// three chunks or four: 4576 x 17408 138 us, with the other loads 165.)
 template <uint32_t W, uint32_t C, uint32_t T>
 __global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
   extern __shared__ float dws[];  // [K], where a workgroup holds several row groups
@@ -200,7 +203,7 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
       if (live && c < chunks) {
         dy[i] = __builtin_nontemporal_load(&a.dy[base + c]);
         h[i] = __builtin_nontemporal_load(&a.h[base + c]);
-        if (a.dh) d[i] = __builtin_nontemporal_load(&a.dh[base + c]);
+        if (C <= 2 && a.dh) d[i] = __builtin_nontemporal_load(&a.dh[base + c]);
       }
     }
     float s = 0.0f;
@@ -223,6 +226,7 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
       const uint32_t c = t + 64 * W * i;
       if (live && c < chunks) {
         const u32x4 w = a.w[c];
+        if (C > 2 && a.dh) d[i] = __builtin_nontemporal_load(&a.dh[base + c]);  // (sooner, registers spill)
         u32x4 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -320,9 +324,12 @@ hipError_t for_row(uint32_t K, uint32_t most, F&& f) {
 // Row groups of a workgroup, about 12 waves
 constexpr uint32_t group_rows(uint32_t W) { return W >= 8 ? 1 : 12 / W; }
 
-// Up to this many rows each has a workgroup and twice the waves.
+// Up to this many rows each has a workgroup and twice the waves (5120 columns, us without ->
+// with: 3.7 -> 3.3 at one row, 4.5 -> 3.6 at 25, 5.7 -> 4.8 at 256; equal from 409).
 constexpr uint32_t kNormFewRows = 256;
-constexpr uint32_t kNormGradParts = 256;  // workgroups of a gradient call: one a CU (256 CUs)
+// Workgroups of a gradient call: one a CU (256 CUs).  128 / 256 / 512, us: 12.5 / 10.6 / 10.6 at
+// 409 x 6144, 58.5 / 42.8 / 46.3 at 4576 x 5120.
+constexpr uint32_t kNormGradParts = 256;
 uint32_t norm_grad_parts(uint32_t M, uint32_t K) {
   const uint32_t rows = group_rows(row_waves(K, 2));
   return std::min((M + rows - 1) / rows, kNormGradParts);

