@@ -16,9 +16,9 @@
 // 371 us against 364).  w's fragments have two register sets; dy's are replaced in place once
 // their last product is issued, but for the last 32 rows, whose reads would end too late.
 //
-// 4576 x 17408 x 5120 (256 rows): 350-355 us, 2.3 PFLOP/s, the matrix pipes busy 66% of the
-// time at 1.8 GHz; 340 with every load from one block, so what is left is the issue of one
-// wave, a last round of 208 tiles on 256 CUs and the clock.  The same in 16 x 16 x 128
+// 4576 x 17408 x 5120 (256 rows): 350-365 us by card, 2.3 PFLOP/s, the matrix pipes busy
+// 61% of the time (69% of a tile's) at 1.8 GHz; 340 with every load from one block, so what is
+// left is the issue of one wave, a last round of 208 tiles on 256 CUs and the clock.  The same in 16 x 16 x 128
 // instructions with the fmas behind each: 385; the loads in a row at a block's start: 477;
 // the loads first and the reads behind a second barrier: 382; eight waves of 64 x 64 in
 // turns (gemm_pp.h's loop): 387.

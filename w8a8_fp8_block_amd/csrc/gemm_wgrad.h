@@ -29,6 +29,9 @@
 // 18304 tokens against 2800; the same two taking turns between reading and computing:
 // 2546.  A library's FP8 product with one scale for all, 8192^3: 2642.)
 //
+// 4576 x 17408 x 5120: 314-327 us by card, 2.5-2.6 PFLOP/s, at that library product's rate;
+// 409 x 2048 x 1408: 5.8 us.
+//
 // The direct loads are issued in assembly (gemm_grad.h says why: the waits that the
 // compiler would add cost half the speed).
 //
