@@ -137,6 +137,43 @@ def test_dgrad(M, N, K):
     assert torch.equal(dx.view(torch.int16), again.view(torch.int16))
 
 
+# Tiles of 256 rows, uncut over sums of every length that the unrolled loop can end with, and
+# cut in ranges; the reference takes some of the columns.
+@pytest.mark.parametrize("M,N,K", [(2100, 128 * g, 2048) for g in range(1, 8)]
+                         + [(250, 17408, 10240), (409, 17408, 5120), (257, 16768, 10112)])
+def test_dgrad_large_tiles(M, N, K):
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    codes = lambda *shape: torch.randint(0, 119, shape, generator=g, device="cuda",  # noqa: E731
+                                         dtype=torch.int32).to(torch.uint8).view(ref.F8)
+    y, w = codes(M, N), codes(N, K)
+    y.view(torch.uint8)[:, ::3] |= 0x80
+    skm, ws = (torch.rand(*s, generator=g, device="cuda") + 0.1 for s in ((N // 128, _mp(M)), (N // 128, K // 128)))
+    skm[:, M:] = float("nan")
+    dx = _dgrad(y, skm, w, ws, M, N, K)
+    cols = torch.cat([torch.arange(0, 70), torch.arange(K // 2 - 40, K // 2 + 40), torch.arange(K - 70, K)])
+    a, s = ref.code_values(y), skm[:, :M].t().cpu()
+    b, bs = ref.code_values(w[:, cols.cuda()].contiguous()), ws.cpu()[:, cols // 128].double()
+    a = a * s.double().repeat_interleave(128, 1)
+    b = b * bs.repeat_interleave(128, 0)
+    _check(dx[:, cols.cuda()], a @ b, a.abs() @ b, f"{M}x{N}x{K}")
+    assert torch.equal(dx, _dgrad(y, skm, w, ws, M, N, K))
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 384, 512), (2100, 640, 2048), (40, 17408, 256)])
+def test_dgrad_nan_stays_in_its_row_and_column(M, N, K):
+    o = _dual(_values(M, N, 3))
+    w, ws = (t.cuda() for t in _weights(N, K, 4))
+    a = _dgrad(o["q"], o["skm"], w, ws, M, N, K).cpu()
+    o["q"].view(torch.uint8)[M - 7, N - 5] = 0x7F
+    o["skm"][0, 9] = float("inf")
+    w.view(torch.uint8)[130, 200] = 0xFF
+    b = _dgrad(o["q"], o["skm"], w, ws, M, N, K).cpu()
+    assert torch.isnan(b[M - 7]).all() and torch.isnan(b[:, 200]).all()
+    keep = torch.ones(M, K, dtype=torch.bool)
+    keep[M - 7], keep[9], keep[:, 200] = False, False, False
+    assert torch.equal(b[keep], a[keep])
+
+
 def test_dgrad_pad_slots_are_not_used():
     M, N, K = 19, 256, 128
     o = _dual(_values(M, N, 6))
