@@ -77,44 +77,66 @@ __device__ __forceinline__ void gemm_dgrad_body(const uint8_t* dy, const float* 
   const u32x4s rAs = rsrc_words(dys + m0, (blocks * Mp - m0) * 4);
   const u32x4s rWs = rsrc_words(ws + g0, (blocks * groups - g0) * 4);
   const uint32_t l8 = lane >> 3, c8 = lane & 7;
-  uint32_t a_off[C::DA], w_off[C::DW];
+  // (Four loads share a destination, 1 KB apart by the instruction's offset, which counts in
+  // memory too: their rows are 8 apart, so what it adds can come off theirs.)
+  uint32_t a_off[C::DA], w_off[C::DW], dest = 0;
 #pragma unroll
-  for (int j = 0; j < C::DA; ++j) a_off[j] = (8 * C::DA * wave + 8 * j + l8) * N + (c8 ^ l8 ^ (j & 1)) * 16;
+  for (int j = 0; j < C::DA; ++j) a_off[j] = (8 * C::DA * wave + 8 * j + l8) * N + (c8 ^ l8 ^ (j & 1)) * 16 - j % 4 * 1024;
 #pragma unroll
-  for (int j = 0; j < C::DW; ++j) w_off[j] = (32 * wave + 8 * j + l8) * K + (c8 ^ l8 ^ (wave & 1)) * 16;
+  for (int j = 0; j < C::DW; ++j) w_off[j] = (32 * wave + 8 * j + l8) * K + (c8 ^ l8 ^ (wave & 1)) * 16 - j % 4 * 1024;
   const uint32_t as_w = wave % TM * 256, as_off = as_w + lane * 4, ws_off = 0;
   const uint32_t lds_a = lds_addr(smem) + wave * C::DA * 1024, lds_w = lds_addr(smem) + C::W_OFF + wave * 4096;
   const uint32_t lds_as = lds_addr(smem) + C::AS_OFF + as_w, lds_ws = lds_addr(smem) + C::WS_OFF + wave * 256;
   auto load_op = [&](uint32_t b, auto slot_c, auto jc) {
     constexpr int J = decltype(jc)::value, SLOT = decltype(slot_c)::value * C::SLOT_BYTES;
-    if constexpr (J < C::DA) dma16_asm<0, SLOT + J * 1024>(rA, a_off[J], b * kGroup, lds_a);
-    else if constexpr (J < C::DA + C::DW)
-      dma16_asm<0, SLOT + (J - C::DA) * 1024>(rW, w_off[J - C::DA], b * kGroup * K, lds_w);
-    else if constexpr (J == C::DA + C::DW) dma4_asm<SLOT>(rAs, as_off, b * Mp * 4, lds_as);
-    else dma4_asm<SLOT>(rWs, ws_off, b * groups * 4, lds_ws);
+    if constexpr (J < C::DA) {
+      if constexpr (J % 4 == 0) dest = dma_dest<SLOT + J * 1024>(lds_a);
+      dma16_to<J % 4 * 1024>(rA, a_off[J], b * kGroup, dest);
+    } else if constexpr (J < C::DA + C::DW) {
+      if constexpr (J == C::DA) dest = dma_dest<SLOT>(lds_w);
+      dma16_to<(J - C::DA) * 1024>(rW, w_off[J - C::DA], b * kGroup * K, dest);
+    } else if constexpr (J == C::DA + C::DW) {
+      dma4_to(rAs, as_off, b * Mp * 4, dma_dest<SLOT>(lds_as));
+    } else {
+      dma4_to(rWs, ws_off, b * groups * 4, dma_dest<SLOT>(lds_ws));
+    }
   };
 
   // ---- fragments ----
   // dy: lane l holds row l % 32, bytes 64 h + 32 (l / 32) .. of the block's half h: two chunks.
   const uint32_t l32 = lane & 31, hi = lane >> 5;
-  const uint8_t* pa[2][2];
+  // (Slots from the second pair on lie past what an LDS instruction's offset reaches from the
+  // first; their bases are registers of their own, which the compiler must not fold together.)
+  uint32_t pa[2][2][2], pw[2][TN], ps[2], pws[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      pa[h][c] = smem + (wm * 32 * TM + l32) * 128 + ((4 * h + 2 * hi + c) ^ swz(l32)) * 16;
+      pa[0][h][c] = (wm * 32 * TM + l32) * 128 + ((4 * h + 2 * hi + c) ^ swz(l32)) * 16;
   // w: column l % 32, rows 64 h + 32 (l / 32) .., transposed
   const uint32_t row = 32 * hi + ((lane & 15) >> 1);
   const uint32_t lt = row * 128 + (swz_t(row) ^ ((lane >> 4) & 1)) * 16 + (lane & 1) * 8;
-  const uint8_t* pw[TN];
 #pragma unroll
-  for (int j = 0; j < TN; ++j) pw[j] = smem + C::W_OFF + (lt ^ (wn * 64 + j * 32));
-  const uint8_t* ps = smem + C::AS_OFF + (wm * 32 * TM + l32) * 4;
-  const uint8_t* pws = smem + C::WS_OFF + wave * 256;
-  auto ld_a = [&](int base, int i, int h, int c) -> v4i {
-    return *reinterpret_cast<const v4i*>(pa[h][c] + base + i * 4096);
+  for (int j = 0; j < TN; ++j) pw[0][j] = C::W_OFF + (lt ^ (wn * 64 + j * 32));
+  ps[0] = C::AS_OFF + (wm * 32 * TM + l32) * 4;
+  pws[0] = C::WS_OFF + wave * 256;
+  auto upper = [](uint32_t lower) -> uint32_t {
+    uint32_t u = lower + 2 * C::SLOT_BYTES;
+    asm volatile("" : "+v"(u));
+    return u;
   };
-  auto ldf = [](const uint8_t* p) -> float { return *reinterpret_cast<const float*>(p); };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) pa[1][h][0] = upper(pa[0][h][0]), pa[1][h][1] = upper(pa[0][h][1]);
+#pragma unroll
+  for (int j = 0; j < TN; ++j) pw[1][j] = upper(pw[0][j]);
+  ps[1] = upper(ps[0]);
+  pws[1] = upper(pws[0]);
+  auto ld_a = [&](int sl, int i, int h, int c) -> v4i {
+    return *reinterpret_cast<const v4i*>(smem + pa[sl / 2][h][c] + (sl % 2 * C::SLOT_BYTES + i * 4096));
+  };
+  auto ldf = [&](const uint32_t (&at)[2], int sl, int off) -> float {
+    return *reinterpret_cast<const float*>(smem + at[sl / 2] + (sl % 2 * C::SLOT_BYTES + off));
+  };
 
   v8i fy[TM - 1][2], fl[2][2], fx[2][TN][2];  // dy; its last rows and w: [set]
   float as[2][TM], wsv[2], sc[2][TM];
@@ -129,26 +151,27 @@ __device__ __forceinline__ void gemm_dgrad_body(const uint8_t* dy, const float* 
     for (int r = 0; r < 16; ++r) p[q][r] = 0.0f;
   sc[1][TM - 1] = 0.0f;
 
-  // the read R of a block at LDS offset base into set F
-  auto rd_w = [&](int base, auto fc, auto rc) {  // 8: half of w's fragment
+  // the read R of the block in slot sl into set F
+  auto rd_w = [&](int sl, auto fc, auto rc) {  // 8: half of w's fragment
     constexpr int F = decltype(fc)::value, R = decltype(rc)::value, j = R / 4, h = R / 2 % 2;
-    if constexpr (R & 1) fx[F][j][h].hi = ld_transposed(pw[j] + base + h * 8192, 1);
-    else fx[F][j][h].lo = ld_transposed(pw[j] + base + h * 8192, 0);
+    const uint8_t* at = smem + pw[sl / 2][j] + (sl % 2 * C::SLOT_BYTES + h * 8192);
+    if constexpr (R & 1) fx[F][j][h].hi = ld_transposed(at, 1);
+    else fx[F][j][h].lo = ld_transposed(at, 0);
   };
-  auto rd_last = [&](int base, auto fc, auto hc) {
+  auto rd_last = [&](int sl, auto fc, auto hc) {
     constexpr int F = decltype(fc)::value, h = decltype(hc)::value;
-    fl[F][h].lo = ld_a(base, TM - 1, h, 0);
-    fl[F][h].hi = ld_a(base, TM - 1, h, 1);
+    fl[F][h].lo = ld_a(sl, TM - 1, h, 0);
+    fl[F][h].hi = ld_a(sl, TM - 1, h, 1);
   };
-  auto rd_a = [&](int base, auto ic, auto hc) {
+  auto rd_a = [&](int sl, auto ic, auto hc) {
     constexpr int i = decltype(ic)::value, h = decltype(hc)::value;
-    fy[i][h].lo = ld_a(base, i, h, 0);
-    fy[i][h].hi = ld_a(base, i, h, 1);
+    fy[i][h].lo = ld_a(sl, i, h, 0);
+    fy[i][h].hi = ld_a(sl, i, h, 1);
   };
-  auto rd_s = [&](int base, auto fc, auto rc) {
+  auto rd_s = [&](int sl, auto fc, auto rc) {
     constexpr int F = decltype(fc)::value, R = decltype(rc)::value;
-    as[F][2 * R] = ldf(ps + base + R * 256);
-    as[F][2 * R + 1] = ldf(ps + base + R * 256 + 128);
+    as[F][2 * R] = ldf(ps, sl, R * 256);
+    as[F][2 * R + 1] = ldf(ps, sl, R * 256 + 128);
   };
 #define IC(n) std::integral_constant<int, (n)>{}
 
@@ -167,12 +190,12 @@ __device__ __forceinline__ void gemm_dgrad_body(const uint8_t* dy, const float* 
              std::make_integer_sequence<int, 2 * (TM - 1)>{});
   unroll_seq([&](auto h) { rd_last(0, IC(0), h); }, std::make_integer_sequence<int, 2>{});
   unroll_seq([&](auto r) { rd_s(0, IC(0), r); }, std::make_integer_sequence<int, TM / 2>{});
-  wsv[0] = ldf(pws);
+  wsv[0] = ldf(pws, 0, 0);
 
   // block kb, in slot S with fragments in set F
   auto step = [&](uint32_t kb, auto slot_c, auto set_c) {
     constexpr int S = decltype(slot_c)::value, F = decltype(set_c)::value;
-    constexpr int nx = (S + 1) % SLOTS * C::SLOT_BYTES;
+    constexpr int nx = (S + 1) % SLOTS;
     const uint32_t lb = b0 + min(kb + SLOTS, G - 1);
     wait_lgkm0();  // this block's fragments are in registers
     sched_fence();
@@ -207,14 +230,14 @@ __device__ __forceinline__ void gemm_dgrad_body(const uint8_t* dy, const float* 
             if constexpr (I == 5) rd_w(nx, FN, IC(5)), rd_s(nx, FN, IC(1));
             if constexpr (I == 8) rd_w(nx, FN, IC(6)), rd_w(nx, FN, IC(7));
             if constexpr (I == 9) rd_last(nx, FN, IC(0));
-            if constexpr (I == 12) rd_last(nx, FN, IC(1)), wsv[1 - F] = ldf(pws + nx);
+            if constexpr (I == 12) rd_last(nx, FN, IC(1)), wsv[1 - F] = ldf(pws, nx, 0);
           } else {
             if constexpr (I == 0) rd_w(nx, FN, IC(0)), rd_w(nx, FN, IC(1)), rd_w(nx, FN, IC(2));
             if constexpr (I == 1) rd_w(nx, FN, IC(3)), rd_w(nx, FN, IC(4)), rd_s(nx, FN, IC(0));
             if constexpr (I == 2) rd_w(nx, FN, IC(5));
             if constexpr (I == 3) rd_w(nx, FN, IC(6));
             if constexpr (I == 4) rd_w(nx, FN, IC(7)), rd_last(nx, FN, IC(0));
-            if constexpr (I == 5) rd_last(nx, FN, IC(1)), wsv[1 - F] = ldf(pws + nx);
+            if constexpr (I == 5) rd_last(nx, FN, IC(1)), wsv[1 - F] = ldf(pws, nx, 0);
           }
           if constexpr (i < TM - 1 && j == TN - 1) rd_a(nx, IC(i), IC(h));
           constexpr int L0 = C::loads_before(I), L1 = C::loads_before(I + 1);

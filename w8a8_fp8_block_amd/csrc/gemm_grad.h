@@ -30,6 +30,22 @@ __device__ __forceinline__ void dma4_asm(u32x4s r, uint32_t voff, uint32_t soff,
                :: "v"(voff), "s"(r), "s"(soff), "s"(lds), "n"(LDS_OFF) : "memory", "scc");
 }
 
+// The same with the destination set apart from the loads, for several loads to one: lds + OFF.
+template <int OFF>
+__device__ __forceinline__ uint32_t dma_dest(uint32_t lds) {
+  uint32_t m0;
+  asm volatile("s_add_u32 %0, %1, %2\n\ts_nop 0" : "={m0}"(m0) : "s"(lds), "n"(OFF) : "scc");
+  return m0;
+}
+template <int OFF>
+__device__ __forceinline__ void dma16_to(u32x4s r, uint32_t voff, uint32_t soff, uint32_t dest) {
+  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen offset:%3 lds"
+               :: "v"(voff), "s"(r), "s"(soff), "n"(OFF), "{m0}"(dest) : "memory");
+}
+__device__ __forceinline__ void dma4_to(u32x4s r, uint32_t voff, uint32_t soff, uint32_t dest) {
+  asm volatile("buffer_load_dword %0, %1, %2 offen lds" :: "v"(voff), "s"(r), "s"(soff), "{m0}"(dest) : "memory");
+}
+
 // A matrix whose rows are the sum's index: a panel of rows of 128 bytes (columns), 16-byte
 // chunk c of row r at chunk position c ^ swz_t(r).  ds_read_b64_tr_b8 takes 8 bytes from
 // each lane of a 16-lane row and gives lane l byte l % 8 of the lanes 2j + l / 8, j = 0..7:
