@@ -325,12 +325,14 @@ hipError_t for_row(uint32_t K, uint32_t most, F&& f) {
 constexpr uint32_t group_rows(uint32_t W) { return W >= 8 ? 1 : 12 / W; }
 
 // Up to this many rows each has a workgroup and twice the waves (5120 columns, us without ->
-// with: 3.7 -> 3.3 at one row, 4.5 -> 3.6 at 25, 5.7 -> 4.8 at 256; equal from 409).
+// with: 3.7 -> 3.3 at one row, 4.5 -> 3.6 at 25, 5.7 -> 4.8 at 256; equal from 409.  The
+// gradient: 5.9 -> 4.9 at one row, 6.9 -> 6.2 at 64, 8.6 -> 8.1 at 200; 10.6 -> 11.0 at 409).
 constexpr uint32_t kNormFewRows = 256;
 // Workgroups of a gradient call: one a CU (256 CUs).  128 / 256 / 512, us: 12.5 / 10.6 / 10.6 at
 // 409 x 6144, 58.5 / 42.8 / 46.3 at 4576 x 5120.
 constexpr uint32_t kNormGradParts = 256;
 uint32_t norm_grad_parts(uint32_t M, uint32_t K) {
+  if (M <= kNormFewRows) return M;
   const uint32_t rows = group_rows(row_waves(K, 2));
   return std::min((M + rows - 1) / rows, kNormGradParts);
 }
@@ -361,10 +363,14 @@ hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16
                        reinterpret_cast<const u32x4*>(h), reinterpret_cast<const u32x4*>(w), rstd,
                        reinterpret_cast<u32x4*>(dx), static_cast<float*>(workspace), M, K};
   if (M > 0) {
-    const hipError_t e = for_row(K, 2, [&](auto W, auto C) {
-      constexpr uint32_t rows = group_rows(W);
-      norm_grad_kernel<W, C, 64 * W * rows><<<dim3(norm_grad_parts(M, K)), dim3(64 * W * rows),
-                                              rows > 1 ? K * 4 : 0, s>>>(a);
+    const uint32_t parts = norm_grad_parts(M, K);
+    const hipError_t e = for_row(K, M <= kNormFewRows ? 1 : 2, [&](auto W, auto C) {
+      if (M <= kNormFewRows) {
+        norm_grad_kernel<W, C, 64 * W><<<dim3(parts), dim3(64 * W), 0, s>>>(a);
+      } else {
+        constexpr uint32_t rows = group_rows(W);
+        norm_grad_kernel<W, C, 64 * W * rows><<<dim3(parts), dim3(64 * W * rows), rows > 1 ? K * 4 : 0, s>>>(a);
+      }
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;
