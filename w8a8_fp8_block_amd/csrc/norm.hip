@@ -326,12 +326,18 @@ constexpr uint32_t group_rows(uint32_t W) { return W >= 8 ? 1 : 12 / W; }
 
 // Up to this many rows each has a workgroup and twice the waves (5120 columns, us without ->
 // with: 3.7 -> 3.3 at one row, 4.5 -> 3.6 at 25, 5.7 -> 4.8 at 256; equal from 409.  The
-// gradient: 5.9 -> 4.9 at one row, 6.9 -> 6.2 at 64, 8.6 -> 8.1 at 200; 10.6 -> 11.0 at 409).
+// gradient: 6.9 -> 6.2 at 64, 8.6 -> 8.1 at 200; 10.6 -> 11.0 at 409).
 constexpr uint32_t kNormFewRows = 256;
 // Workgroups of a gradient call: one a CU (256 CUs).  128 / 256 / 512, us: 12.5 / 10.6 / 10.6 at
 // 409 x 6144, 58.5 / 42.8 / 46.3 at 4576 x 5120.
 constexpr uint32_t kNormGradParts = 256;
+// A gradient call that one workgroup does in two turns at most writes dw itself, one launch and
+// not two.  us a call from the host / in a graph, two -> one: 8 x 384: 8.5 -> 6.0 / 4.2 -> 3.7; 24
+// x 384 (two turns): 8.5 -> 6.0 / 4.3 -> 4.7; 2 x 5120: 8.5 -> 6.0 / 5.0 -> 4.1; 4 x 5120 (two): 8.5
+// -> 6.0 / 5.1 -> 5.6.
+bool norm_grad_lone(uint32_t M, uint32_t K) { return M > 0 && M <= 2 * group_rows(row_waves(K, 2)); }
 uint32_t norm_grad_parts(uint32_t M, uint32_t K) {
+  if (norm_grad_lone(M, K)) return 1;
   if (M <= kNormFewRows) return M;
   const uint32_t rows = group_rows(row_waves(K, 2));
   return std::min((M + rows - 1) / rows, kNormGradParts);
@@ -359,13 +365,14 @@ uint64_t norm_grad_workspace_bytes(uint32_t M, uint32_t K) {
 hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* w,
                             const float* rstd, uint16_t* dx, float* dw, void* workspace, uint32_t M, uint32_t K,
                             hipStream_t s) {
+  const bool lone = norm_grad_lone(M, K), few = !lone && M <= kNormFewRows;
+  const uint32_t parts = norm_grad_parts(M, K);
   const NormGradArgs a{reinterpret_cast<const u32x4*>(dy), reinterpret_cast<const u32x4*>(dh),
                        reinterpret_cast<const u32x4*>(h), reinterpret_cast<const u32x4*>(w), rstd,
-                       reinterpret_cast<u32x4*>(dx), static_cast<float*>(workspace), M, K};
+                       reinterpret_cast<u32x4*>(dx), lone ? dw : static_cast<float*>(workspace), M, K};
   if (M > 0) {
-    const uint32_t parts = norm_grad_parts(M, K);
-    const hipError_t e = for_row(K, M <= kNormFewRows ? 1 : 2, [&](auto W, auto C) {
-      if (M <= kNormFewRows) {
+    const hipError_t e = for_row(K, few ? 1 : 2, [&](auto W, auto C) {
+      if (few) {
         norm_grad_kernel<W, C, 64 * W><<<dim3(parts), dim3(64 * W), 0, s>>>(a);
       } else {
         constexpr uint32_t rows = group_rows(W);
@@ -373,9 +380,9 @@ hipError_t launch_norm_grad(const uint16_t* dy, const uint16_t* dh, const uint16
       }
       return hipGetLastError();
     });
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || lone) return e;
   }
-  norm_dw_kernel<<<dim3(K / 64), dim3(1024), 0, s>>>(a.part, dw, norm_grad_parts(M, K), K);
+  norm_dw_kernel<<<dim3(K / 64), dim3(1024), 0, s>>>(a.part, dw, parts, K);
   return hipGetLastError();
 }
 
