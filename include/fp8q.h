@@ -721,7 +721,8 @@ size_t fp8q_proj_lora_workspace_bytes(uint32_t M, uint32_t N, uint32_t K,
  *   h    = bf16_rne( x + residual )   (residual NULL: h = x)
  *   rstd = 1 / sqrt( sum_k h[m,k]^2 / K + eps )
  *   y    = h * rstd * weight          (fp32)
- *   scale[m,g] = amax|y[m,128g..]| / 448,  q = e4m3_rne_sat( y / scale )
+ *   scale[m,g] = fl(amax|y[m,128g..]| / 448),  q = e4m3_rne_sat( fl(y / scale) ), 0 where
+ *   the scale rounds to 0
  *   x_bf16, residual_bf16  [M,K], weight_bf16 [K], read only
  *   h_bf16    [M,K] out, the new residual stream: required with a residual (it may
  *             be x's or the residual's own array), NULL without

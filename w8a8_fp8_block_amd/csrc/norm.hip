@@ -30,14 +30,35 @@ namespace {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
 }
-// Scale of a group of fp32 values from its maximum's bits, amax / 448 (as
-// group_scale, within an ulp here); a NaN or infinite maximum stays one.
-__device__ __forceinline__ float group_scale_f32(uint32_t amax_bits) {
+// Scale and quotients of N of a group's fp32 values, from its maximum's bits:
+//   s = fl(amax / 448),  q = fl(y / s), at most 448 in magnitude (e4m3's saturation).
+// fl(a / 448) by a corrected product and the quotients by reciprocal are the correctly
+// rounded ones where s is normal.  (Of all finite a, those up to 2^-120 alone give another
+// scale; of all mantissas of s, the last one alone gives quotients that round to another
+// code, at y / s = 2^-10 and only if the hardware reciprocal is off by an ulp there; from s =
+// 2^-80 the residuals of quotients down to 2^-11, the least that matter, are exact.)  Other
+// scales - zero, tiny, infinite, NaN - are divided out.  The choice is uniform over the
+// wave and both ways give the same codes, so a group's do not depend on its neighbours.
+// Only a subnormal scale, a few units of 2^-149, rounds so far that y / s passes 448: by up
+// to 224 / 448, beyond what the conversion saturates by itself (it would give NaN).
+template <int N>
+__device__ __forceinline__ float scale_and_quotients(const float* y, uint32_t amax_bits, float* q) {
   const float a = __uint_as_float(amax_bits);
   constexpr float k = 1.0f / 448.0f;
-  const float q0 = a * k;
-  const float s = __builtin_fmaf(-__builtin_fmaf(q0, 448.0f, -a), k, q0);
-  return amax_bits >= 0x7F800000u ? a : s;
+  const float s0 = a * k;
+  float s = __builtin_fmaf(-__builtin_fmaf(s0, 448.0f, -a), k, s0);
+  const bool slow = !(s >= 0x1p-80f && s < INFINITY) || (__float_as_uint(s) & 0x7FFFFFu) == 0x7FFFFFu;
+  if (__builtin_amdgcn_ballot_w64(slow) == 0) {
+    quotients_by_reciprocal<N>(y, s, q);
+  } else {
+    s = a / 448.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float v = s == 0.0f ? y[i] : y[i] / s;
+      q[i] = v > 448.0f ? 448.0f : v < -448.0f ? -448.0f : v;  // a NaN stays one
+    }
+  }
+  return s;
 }
 
 // 1 / sqrt(v), v normal: the hardware's (1 ulp) and one Newton step; NaN for v
@@ -137,8 +158,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
         amax = max(amax, max(__float_as_uint(y[2 * j]) & 0x7FFFFFFFu, __float_as_uint(y[2 * j + 1]) & 0x7FFFFFFFu));
       }
       amax = dpp_row_max_u32(amax);
-      const float s = group_scale_f32(amax);
-      quotients<8>(y, s, qv);
+      const float s = scale_and_quotients<8>(y, amax, qv);
       a.q[base + c] = u32x2{encode4(qv), encode4(qv + 4)};
       if (a.y) {
         u32x4 o;

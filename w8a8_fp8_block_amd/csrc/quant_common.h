@@ -38,29 +38,35 @@ __device__ __forceinline__ u16x2 as_u16x2(uint32_t v) { return __builtin_bit_cas
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+// q[i] = fl32(x[i] / s) for a normal scale s, neither tiny nor huge: the hardware
+// reciprocal (within 1 ulp) and one Newton-Raphson step with fmas, r = r0 + r0*(1 - s*r0),
+// then a corrected product.
+template <int N>
+__device__ __forceinline__ void quotients_by_reciprocal(const float* x, float s, float* q) {
+  const float r0 = __builtin_amdgcn_rcpf(s);
+  const float r = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.0f), r0, r0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // en = q0*s - x is the negated residual; q1 = q0 - en*r.  Written this
+    // way round, x = -0 gives en = +0 and q1 = -0 + -0 = -0, keeping the sign
+    // (the residual x - q0*s would be +0 and turn q1 into +0).
+    const float q0 = x[i] * r;
+    const float en = __builtin_fmaf(q0, s, -x[i]);
+    q[i] = __builtin_fmaf(-en, r, q0);
+  }
+}
+
 // q[i] = fl32(x[i] / s), the correctly rounded quotient, for N values that
 // share the scale s (see quant.hip for why the reciprocal form is exact when
-// s >= 2^-100); a zero scale (all-zero group) keeps the signed zeros.  The
+// s >= 2^-100: from any start within one ulp of the correctly rounded reciprocal
+// the step lands on it, for every such scale that a bf16 group maximum can
+// produce); a zero scale (all-zero group) keeps the signed zeros.  The
 // choice of method is uniform over the wave, and both give the same result.
 template <int N>
 __device__ __forceinline__ void quotients(const float* x, float s, float* q) {
   const bool slow = !(s >= 0x1p-100f);  // zero or tiny scale
   if (__builtin_amdgcn_ballot_w64(slow) == 0) {
-    // r = fl32(1/s): the hardware reciprocal (within 1 ulp) and one
-    // Newton-Raphson step with fmas, r = r0 + r0*(1 - s*r0).  From any start
-    // within one ulp of the correctly rounded reciprocal the step lands on
-    // it, for every scale >= 2^-100 that a bf16 group maximum can produce.
-    const float r0 = __builtin_amdgcn_rcpf(s);
-    const float r = __builtin_fmaf(__builtin_fmaf(-s, r0, 1.0f), r0, r0);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      // en = q0*s - x is the negated residual; q1 = q0 - en*r.  Written this
-      // way round, x = -0 gives en = +0 and q1 = -0 + -0 = -0, keeping the sign
-      // (the residual x - q0*s would be +0 and turn q1 into +0).
-      const float q0 = x[i] * r;
-      const float en = __builtin_fmaf(q0, s, -x[i]);
-      q[i] = __builtin_fmaf(-en, r, q0);
-    }
+    quotients_by_reciprocal<N>(x, s, q);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) q[i] = (s == 0.0f) ? x[i] : x[i] / s;
