@@ -336,7 +336,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_grad_kernel(RouteGradAr
         uint16_t* p = static_cast<uint16_t*>(a.dlogits) + at;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (16 * i + l16 < a.E) p[16 * i] = (uint16_t)bf16_bits_rne(g[i]);
+          if (16 * i + l16 < a.E) p[16 * i] = bf16_rne(g[i]);
       } else {
         float* p = static_cast<float*>(a.dlogits) + at;
 #pragma unroll

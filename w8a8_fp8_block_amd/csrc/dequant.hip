@@ -9,22 +9,17 @@
 // hardware OCP e4m3 -> fp32 conversion (exact), multiplies by the fp32
 // scale (one IEEE rounding) and rounds to bf16 (nearest even), two 16-byte
 // stores.  Grid-stride over the N*K/16 chunks.
+#include "bf16.h"
 #include "fp8q_internal.h"
 
 namespace fp8q {
 namespace {
 
-__device__ __forceinline__ uint32_t bf16_bits(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-
 // four codes (one dword) -> two dwords of bf16 pairs, scaled
 __device__ __forceinline__ u32x2 dequant4(uint32_t c, float s) {
   const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, false);  // bytes 0, 1
   const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, true);   // bytes 2, 3
-  return u32x2{bf16_bits(lo[0] * s) | (bf16_bits(lo[1] * s) << 16),
-               bf16_bits(hi[0] * s) | (bf16_bits(hi[1] * s) << 16)};
+  return u32x2{bf16x2_rne(lo[0] * s, lo[1] * s), bf16x2_rne(hi[0] * s, hi[1] * s)};
 }
 
 __global__ __launch_bounds__(256) void dequant_kernel(const u32x4* __restrict__ w,

@@ -23,7 +23,7 @@ __device__ __forceinline__ u32x4 silu_mul_8(u32x4 g, u32x4 u) {
     const float lo = silu_mul_f32(__uint_as_float(gw[i] << 16), __uint_as_float(uw[i] << 16));
     const float hi = silu_mul_f32(__uint_as_float(gw[i] & 0xFFFF0000u),
                                   __uint_as_float(uw[i] & 0xFFFF0000u));
-    hw[i] = bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
+    hw[i] = bf16x2_rne(lo, hi);
   }
   return u32x4{hw[0], hw[1], hw[2], hw[3]};
 }

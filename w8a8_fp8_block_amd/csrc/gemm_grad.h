@@ -64,13 +64,6 @@ __device__ __forceinline__ v4i ld_transposed(const uint8_t* p, int h) {
   return v4i{a.x, a.y, b.x, b.y};
 }
 
-// Two bf16 (round to nearest even, NaN kept) in one instruction.
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
 // 16 bytes a lane to base + voff + OFF.  (In assembly for the uniform base: with an address
 // a lane, the tile's end spills, and each reload waits for the stores.  The data's
 // registers may be written two instructions later.)
@@ -88,10 +81,10 @@ __device__ __forceinline__ void tile_rows_bf16(const v16f& c, uint32_t (&v)[2][4
   unroll_seq(
       [&](auto rc) {
         constexpr int s = decltype(rc)::value, r = 8 * s;
-        const auto s0 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r], c[r + 1]),
-                                                         cvt_bf16x2(c[r + 4], c[r + 5]), false, false);
-        const auto s1 = __builtin_amdgcn_permlane32_swap(cvt_bf16x2(c[r + 2], c[r + 3]),
-                                                         cvt_bf16x2(c[r + 6], c[r + 7]), false, false);
+        const auto s0 = __builtin_amdgcn_permlane32_swap(bf16x2_rne(c[r], c[r + 1]),
+                                                         bf16x2_rne(c[r + 4], c[r + 5]), false, false);
+        const auto s1 = __builtin_amdgcn_permlane32_swap(bf16x2_rne(c[r + 2], c[r + 3]),
+                                                         bf16x2_rne(c[r + 6], c[r + 7]), false, false);
         v[s][0] = s0[0], v[s][1] = s1[0], v[s][2] = s0[1], v[s][3] = s1[1];
       },
       std::make_integer_sequence<int, 2>{});

@@ -129,7 +129,7 @@ __device__ __forceinline__ void ffn_h(const v4f (&acc)[TM][TN], const uint8_t* s
         const uint32_t g2 = up ? pw[2 * h + d] : ow[d], u2 = up ? ow[d] : pw[2 * h + d];
         const float lo = silu_mul_f32(__uint_as_float(g2 << 16), __uint_as_float(u2 << 16));
         const float hi = silu_mul_f32(__uint_as_float(g2 & 0xFFFF0000u), __uint_as_float(u2 & 0xFFFF0000u));
-        hb[i][tn][d] = bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
+        hb[i][tn][d] = bf16x2_rne(lo, hi);
       }
     }
   }

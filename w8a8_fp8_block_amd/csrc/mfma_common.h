@@ -7,6 +7,7 @@
 
 #include <utility>
 
+#include "bf16.h"
 #include "fp8q_internal.h"
 
 namespace fp8q {
@@ -16,13 +17,8 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ uint32_t bf16_rne(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-}
-
 __device__ __forceinline__ uint2 pack_bf16x4(const v4f& v) {
-  return make_uint2(bf16_rne(v[0]) | (bf16_rne(v[1]) << 16), bf16_rne(v[2]) | (bf16_rne(v[3]) << 16));
+  return make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
 }
 
 __device__ __forceinline__ v8i join(u32x4 a, u32x4 b) {

@@ -27,9 +27,6 @@
 namespace fp8q {
 namespace {
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return bf16_bits_rne(lo) | (bf16_bits_rne(hi) << 16);
-}
 // Scale and quotients of N of a group's fp32 values, from its maximum's bits:
 //   s = fl(amax / 448),  q = fl(y / s), at most 448 in magnitude (e4m3's saturation).
 // fl(a / 448) by a corrected product and the quotients by reciprocal are the correctly
@@ -128,7 +125,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
       const uint32_t c = t + 64 * W * i;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        h[i][j] = pack_bf16(bf_lo(h[i][j]) + bf_lo(r[i][j]), bf_hi(h[i][j]) + bf_hi(r[i][j]));
+        h[i][j] = bf16x2_rne(bf_lo(h[i][j]) + bf_lo(r[i][j]), bf_hi(h[i][j]) + bf_hi(r[i][j]));
       if (live && c < chunks) __builtin_nontemporal_store(h[i], &a.h[base + c]);
     }
   }
@@ -163,7 +160,7 @@ __global__ __launch_bounds__(1024) void norm_quant_kernel(NormArgs a) {
       if (a.y) {
         u32x4 o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) o[j] = bf16x2_rne(y[2 * j], y[2 * j + 1]);
         __builtin_nontemporal_store(o, &a.y[base + c]);
       }
       if ((lane & 15) == 0) {
@@ -252,7 +249,7 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
         for (int j = 0; j < 4; ++j) {
           const float l = rstd * (bf_lo(dy[i][j]) * bf_lo(w[j]) - bf_lo(h[i][j]) * rstd * s);
           const float u = rstd * (bf_hi(dy[i][j]) * bf_hi(w[j]) - bf_hi(h[i][j]) * rstd * s);
-          o[j] = pack_bf16(l + bf_lo(d[i][j]), u + bf_hi(d[i][j]));
+          o[j] = bf16x2_rne(l + bf_lo(d[i][j]), u + bf_hi(d[i][j]));
         }
         __builtin_nontemporal_store(o, &a.dx[base + c]);
       }

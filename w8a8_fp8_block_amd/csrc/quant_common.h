@@ -6,6 +6,7 @@
 // of the division are described in quant.hip.
 #pragma once
 
+#include "bf16.h"
 #include "fp8q_internal.h"
 
 namespace fp8q {
@@ -141,12 +142,6 @@ __device__ __forceinline__ float silu_mul_f32(float g, float u) {
   const float t = exp_f32(fmaxf(deep ? g + 64.0f : -g, -110.0f));  // one exp per element
   const float s = deep ? (g * t) * 1.60381089e-28f /* e^-64 */ : g * __builtin_amdgcn_rcpf(1.0f + t);
   return s * u;
-}
-
-// fp32 -> bf16 bit pattern, round to nearest even (finite values)
-__device__ __forceinline__ uint32_t bf16_bits_rne(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
 }  // namespace

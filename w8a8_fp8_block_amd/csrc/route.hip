@@ -341,10 +341,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint16_t* __restrict
     }
   }
   u32x4 o;
-  o.x = bf16_bits_rne(s[0]) | (bf16_bits_rne(s[1]) << 16);
-  o.y = bf16_bits_rne(s[2]) | (bf16_bits_rne(s[3]) << 16);
-  o.z = bf16_bits_rne(s[4]) | (bf16_bits_rne(s[5]) << 16);
-  o.w = bf16_bits_rne(s[6]) | (bf16_bits_rne(s[7]) << 16);
+  o.x = bf16x2_rne(s[0], s[1]);
+  o.y = bf16x2_rne(s[2], s[3]);
+  o.z = bf16x2_rne(s[4], s[5]);
+  o.w = bf16x2_rne(s[6], s[7]);
   *reinterpret_cast<u32x4*>(out + (uint64_t)t * H + h) = o;
 }
 
