@@ -847,7 +847,8 @@ size_t fp8q_moe_balance_workspace_bytes(uint32_t T, uint32_t E);
  *   counts         [E+1] as fp8q_moe_balance gave them (NULL: no balance loss); sums
  *                  over several ranks' tokens do as well
  *   dloss          [1] fp32, the loss's own gradient (NULL: 1)
- *   dlogits        [T,E] out, of the logits' type; 0 where an expert cannot be chosen
+ *   dlogits        [T,E] out, of the logits' type; 0 where an expert cannot be chosen,
+ *                  NaN or infinite gradients or not
  * One of ids and counts at least.  top_k as in the forward calls.  T == 0: nothing. */
 fp8q_status fp8q_moe_route_grad(const void *logits, int logits_bf16, const int32_t *ids,
                                 const float *dweights, const int32_t *counts,

@@ -330,6 +330,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void route_grad_kernel(RouteGradAr
 #pragma unroll
       for (int i = 0; i < NV; ++i) g[i] += x[i] * rw * (d[i] - m[i] * wd);
     }
+    // an expert that cannot be chosen: 0, and not 0 * (a NaN or infinite gradient)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) g[i] = l[i] == -INFINITY ? 0.0f : g[i];
     if (live) {
       const uint64_t at = (uint64_t)t * a.E + l16;
       if (a.bf16) {
