@@ -823,7 +823,7 @@ size_t fp8q_gemm_wgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
  *   logits   [T,E] fp32 (logits_bf16 = 0) or bf16 (1); ids [T,top_k] int32, ids outside
  *            0..E-1 count nowhere; read only
  *   counts   [E+1] int32 out, counts[E] = n;  prob [E] and loss [1] fp32 out (zeros
- *            where n is 0, T == 0 among it)
+ *            where n is 0, T == 0 among it); loss need only be 4-byte aligned
  *   workspace of fp8q_moe_balance_workspace_bytes(T, E) bytes (may be NULL when that is
  *            0); contents undefined on return; calls in flight must not share it
  * fp32 sums in a fixed order: results do not depend on scheduling.  Limits and errors
@@ -846,7 +846,7 @@ size_t fp8q_moe_balance_workspace_bytes(uint32_t T, uint32_t E);
  *                  slots whose id lies outside 0..E-1 are left out
  *   counts         [E+1] as fp8q_moe_balance gave them (NULL: no balance loss); sums
  *                  over several ranks' tokens do as well
- *   dloss          [1] fp32, the loss's own gradient (NULL: 1)
+ *   dloss          [1] fp32, the loss's own gradient (NULL: 1); 4-byte aligned
  *   dlogits        [T,E] out, of the logits' type; 0 where an expert cannot be chosen,
  *                  NaN or infinite gradients or not
  * One of ids and counts at least.  top_k as in the forward calls.  T == 0: nothing. */

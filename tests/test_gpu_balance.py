@@ -153,3 +153,21 @@ def test_gradient_against_differences():
             u = torch.randn(T, E, generator=g, dtype=torch.float64)
             num = (value(l.double() + 1e-5 * u) - value(l.double() - 1e-5 * u)) / 2e-5
             assert abs(float((d.double() * u).sum()) - num) <= (F32 + 1e-6) * float((size * u.abs()).sum())
+
+
+def test_scalars_anywhere():
+    """The loss and its gradient are single floats: elements of a program's own tensor of
+    losses serve, at any of its places."""
+    T, E, k = 30, 24, 4
+    l, ids, _ = _router(T, E, k, torch.float32, 12)
+    lc, ic = l.cuda(), ids.cuda()
+    losses, grads = torch.zeros(7, device="cuda"), torch.arange(1.0, 8.0, device="cuda")
+    counts, prob = torch.empty(E + 1, dtype=torch.int32, device="cuda"), torch.empty(E, device="cuda")
+    rl = ref.balance(l, ids, 0.5)[2]
+    d, first = torch.empty_like(lc), None
+    for i in range(7):
+        fp8q.fp8q_moe_balance(lc, ic, counts, prob, losses[i:i + 1], None, 0.5)
+        fp8q.fp8q_moe_route_grad(lc, None, None, counts, grads[i:i + 1], d, top_k=k)
+        first = d.clone() if i == 0 else first
+        assert ((d - (i + 1) * first).abs() <= 2.0 ** -20 * (i + 1) * first.abs().max()).all()
+    assert ((losses.cpu().double() - rl).abs() <= 4 * F32 * rl).all() and (losses == losses[0]).all()

@@ -141,3 +141,15 @@ def test_binding_refuses_cpu_tensors():
         fp8q.fp8q_quant_act_dual(x, None, None, q, torch.zeros(1, 256, 4, dtype=torch.uint8))
     with pytest.raises(ValueError, match="2-d"):
         fp8q.fp8q_quant_act_dual(x[0], None, None, q, torch.zeros(1, 256, 4, dtype=torch.uint8))
+
+
+def test_scalars_need_their_own_alignment_only():
+    """loss and dloss are single floats: any multiple of 4 passes their check (here the next
+    check refuses the call), no other address does."""
+    lib = fp8q.lib()
+    for at, want in ((0x1004, "logits"), (0x1008, "logits"), (0x100C, "logits"), (0x1002, "loss"), (0x1006, "loss")):
+        st = lib.fp8q_moe_balance(None if want == "logits" else G, 0, G, G, G, P(at), G, BIG, 1.0, 4, 8, 2, None)
+        assert st == (NULL if want == "logits" else ALIGN) and want in _err(), hex(at)
+    for at, want in ((0x1004, "dlogits"), (0x1008, "dlogits"), (0x100C, "dlogits"), (0x1002, "dloss"), (0x1006, "dloss")):
+        st = lib.fp8q_moe_route_grad(G, 0, G, G, G, P(at), None if want == "dlogits" else G, 1.0, 4, 8, 2, 1, None)
+        assert st == (NULL if want == "dlogits" else ALIGN) and want in _err(), hex(at)

@@ -46,6 +46,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
     if (!aligned16(p)) return fail(FP8Q_ERR_ALIGN, "%s: " #p " is not 16-byte aligned", fn); \
   } while (0)
 
+// A single number, which may be an element of an array of the caller's.
+#define REQUIRE_SCALAR(p)                                                           \
+  do {                                                                              \
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(FP8Q_ERR_ALIGN, "%s: " #p " is not 4-byte aligned", fn); \
+  } while (0)
+
 // An optional array.
 #define REQUIRE_ALIGNED(p)                                                          \
   do {                                                                              \
@@ -1145,7 +1151,8 @@ fp8q_status fp8q_moe_balance(const void* logits, int logits_bf16, const int32_t*
   if (st != FP8Q_OK) return st;
   REQUIRE_PTR(counts);
   REQUIRE_PTR(prob);
-  REQUIRE_PTR(loss);
+  if (!loss) return fail(FP8Q_ERR_NULL, "%s: loss is NULL", fn);
+  REQUIRE_SCALAR(loss);
   if (T > 0) {
     REQUIRE_PTR(logits);
     REQUIRE_PTR(ids);
@@ -1178,7 +1185,7 @@ fp8q_status fp8q_moe_route_grad(const void* logits, int logits_bf16, const int32
     REQUIRE_PTR(dweights);
   }
   REQUIRE_ALIGNED(counts);
-  REQUIRE_ALIGNED(dloss);
+  REQUIRE_SCALAR(dloss);
   REQUIRE_PTR(logits);
   REQUIRE_PTR(dlogits);
   st = check_device(fn);
