@@ -252,6 +252,12 @@ __device__ __forceinline__ void gemm_wgrad_body(const WgradArgs& a, uint32_t uni
                               : (lane & 15) * K * 2 + 32 * ((lane >> 4) & 1) + 16 * (lane >> 5);
     const uint64_t corner = (uint64_t)(n0 + wm * 32 * TM) * K + (k0 + wn * 32 * TN);
     const uint64_t base = SPLIT ? (uint64_t)(a.part + (uint64_t)split * N * K + corner) : (uint64_t)(a.out + corner);
+    if constexpr (SPLIT) {
+      // The stores below read the matrix instructions' results in assembly, for which the
+      // compiler keeps no wait states: 20 behind the last one's 16 passes.
+      asm volatile("s_nop 15\n\ts_nop 3" ::: "memory");
+      sched_fence();
+    }
     if (inside) {
       unroll_seq(
           [&](auto ic) {
