@@ -803,9 +803,11 @@ size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
  *             fp8q_quant_act_dual
  *   dw_bf16   [N,K] out (M == 0: zeros)
  *   workspace fp8q_gemm_wgrad_workspace_bytes(M, N, K) bytes, as above
- * Limits as for fp8q_gemm_dgrad.  The FP8 matrix instruction
- * sums a 128-token block to about 16 bits and adds the blocks in fp32: 1.5e-5 of the
- * result's norm, a hundredth of the bf16 rounding.  Reproducible run to run. */
+ * Limits as for fp8q_gemm_dgrad.  The FP8 matrix instruction sums 64 tokens' products to
+ * about 16 bits below the largest of them and adds the sum to an fp32 accumulator, which
+ * runs over all the tokens (or a range of them, the ranges added in fp32): 1.5e-5 of the
+ * result's norm, a hundredth of the bf16 rounding, from 1536 to 65536 tokens an accumulator
+ * alike.  Reproducible run to run. */
 fp8q_status fp8q_gemm_wgrad(const uint8_t *dy_tok, const uint8_t *dy_exp,
                             const uint8_t *x_tok, const uint8_t *x_exp, uint16_t *dw_bf16,
                             void *workspace, size_t workspace_bytes, uint32_t M,

@@ -7,9 +7,10 @@
 // The sum runs along the rows of both matrices, so their fragments come through
 // the transposing LDS read (gemm_grad.h) and no transposed copy exists.  The
 // scales are the matrix instruction's own operands, a byte a lane: the partial
-// products need no fp32 multiply of their own and add up in the instruction's
-// accumulators (as exact as scaled fp32 additions: 1.5e-5 of the result's norm over
-// 4608 tokens either way, the instruction's own rounding of its sum).
+// products need no fp32 multiply of their own and add up in the instruction's fp32
+// accumulators over all the tokens.  As exact as scaled fp32 additions: 1.5e-5 of the
+// result's norm either way over 4608 tokens, and the same over 65536 (2.6e-6 for products
+// of one sign); it is the instruction's rounding of its 64 products that shows.
 //
 // Pipeline.  A workgroup of four waves computes a tile of BM = 64 TM columns of dy
 // by BN = 64 TN columns of x, its waves in a 2 x 2 grid.  The tokens pass in halves
