@@ -752,7 +752,9 @@ fp8q_status fp8q_add_rmsnorm_quant(const uint16_t *x_bf16, const uint16_t *resid
  *             dh's or h's own array
  *   dweight   [K] fp32 out (M == 0: zeros)
  *   workspace fp8q_add_rmsnorm_grad_workspace_bytes(M, K) bytes; contents undefined
- *             on return; calls in flight must not share it
+ *             on return; calls in flight must not share it.  The size is this M's own and
+ *             can be larger for a smaller M (256 rows need more than 257): a buffer for
+ *             batches of several sizes takes the largest, and 1024 * K bytes serve every M
  * fp32 throughout, no atomics: results do not depend on scheduling. */
 fp8q_status fp8q_add_rmsnorm_grad(const uint16_t *dy_bf16, const uint16_t *dh_bf16,
                                   const uint16_t *h_bf16, const uint16_t *weight_bf16,
@@ -787,7 +789,10 @@ fp8q_status fp8q_quant_act_dual(const uint16_t *x_bf16, uint8_t *q_e4m3, float *
  *   w_e4m3, w_scale       [N,K] and [N/128, K/128]: the forward call's own arrays
  *   dx_bf16   [M,K] out
  *   workspace fp8q_gemm_dgrad_workspace_bytes(M, N, K) bytes (may be NULL when that
- *             is 0); contents undefined on return; calls in flight must not share it
+ *             is 0); contents undefined on return; calls in flight must not share it.
+ *             The size is this M's own and can be larger for a smaller M (long batches need
+ *             none): a buffer for batches of several sizes takes the largest, and 128 KiB a
+ *             CU (32 MiB on 256 CUs) serve every M, N and K
  * N % 128 == 0, K % 128 == 0; ceil128(M)*N, ceil128(M)*K and N*K below 2^32.  M == 0:
  * nothing.  Accumulation, reproducibility and errors as fp8q_gemm_blockscaled. */
 fp8q_status fp8q_gemm_dgrad(const uint8_t *dy_e4m3, const float *dy_scale_km,
@@ -802,7 +807,8 @@ size_t fp8q_gemm_dgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
  *   dy_tok, dy_exp, x_tok, x_exp   token codes and bytes of dy [M,N] and x [M,K] from
  *             fp8q_quant_act_dual
  *   dw_bf16   [N,K] out (M == 0: zeros)
- *   workspace fp8q_gemm_wgrad_workspace_bytes(M, N, K) bytes, as above
+ *   workspace fp8q_gemm_wgrad_workspace_bytes(M, N, K) bytes, as above, but never less
+ *             for a larger M; 64 KiB a CU serve every M, N and K
  * Limits as for fp8q_gemm_dgrad.  The FP8 matrix instruction sums 64 tokens' products to
  * about 16 bits below the largest of them and adds the sum to an fp32 accumulator, which
  * runs over all the tokens (or a range of them, the ranges added in fp32): 1.5e-5 of the
@@ -827,7 +833,8 @@ size_t fp8q_gemm_wgrad_workspace_bytes(uint32_t M, uint32_t N, uint32_t K);
  *   counts   [E+1] int32 out, counts[E] = n;  prob [E] and loss [1] fp32 out (zeros
  *            where n is 0, T == 0 among it); loss need only be 4-byte aligned
  *   workspace of fp8q_moe_balance_workspace_bytes(T, E) bytes (may be NULL when that is
- *            0); contents undefined on return; calls in flight must not share it
+ *            0); contents undefined on return; calls in flight must not share it.  Never
+ *            less for a larger T
  * fp32 sums in a fixed order: results do not depend on scheduling.  Limits and errors
  * as fp8q_moe_route. */
 fp8q_status fp8q_moe_balance(const void *logits, int logits_bf16, const int32_t *ids,

@@ -153,3 +153,40 @@ def test_scalars_need_their_own_alignment_only():
     for at, want in ((0x1004, "dlogits"), (0x1008, "dlogits"), (0x100C, "dlogits"), (0x1002, "dloss"), (0x1006, "dloss")):
         st = lib.fp8q_moe_route_grad(G, 0, G, G, G, P(at), None if want == "dlogits" else G, 1.0, 4, 8, 2, 1, None)
         assert st == (NULL if want == "dlogits" else ALIGN) and want in _err(), hex(at)
+
+
+SIZES = sorted({1, 2, 3, 5, 8, 12, 13, 24, 25, 63, 64, 100, 127, 128, 129, 200, 255, 256, 257, 300, 384, 385, 409, 511,
+                512, 513, 700, 1024, 1168, 1500, 2000, 2500, 4096, 4576, 10000, 16384, 40000, 131072})
+
+
+def test_workspaces_for_several_batch_sizes():
+    """What the header promises a program that keeps one buffer: sizes that serve every batch,
+    and which sizes never fall as the batch grows."""
+    cus = 256
+    for K in (128, 256, 384, 640, 1408, 2048, 5120, 6144, 17408, 32768):
+        need = [fp8q.fp8q_add_rmsnorm_grad_workspace_bytes(M, K) for M in SIZES]
+        assert max(need) == 1024 * K and all(need)
+        assert need[SIZES.index(256)] == 1024 * K
+        for N in (128, 512, 2048, 5120, 17408):
+            dx = [fp8q.fp8q_gemm_dgrad_workspace_bytes(M, N, K) for M in SIZES]
+            assert max(dx) <= cus * 128 * 1024
+            dw = [fp8q.fp8q_gemm_wgrad_workspace_bytes(M, N, K) for M in SIZES]
+            assert max(dw) <= cus * 64 * 1024 and dw == sorted(dw)
+    for E in (1, 8, 64, 160, 512):
+        need = [fp8q.fp8q_moe_balance_workspace_bytes(T, E) for T in SIZES]
+        assert need == sorted(need)
+    # the sizes that do fall, of which the header warns
+    assert fp8q.fp8q_add_rmsnorm_grad_workspace_bytes(256, 640) > fp8q.fp8q_add_rmsnorm_grad_workspace_bytes(257, 640)
+    assert fp8q.fp8q_gemm_dgrad_workspace_bytes(16, 5120, 6144) > fp8q.fp8q_gemm_dgrad_workspace_bytes(409, 5120, 6144) == 0
+
+
+def test_one_byte_less_is_refused():
+    """At batch sizes on both sides of the rules' borders."""
+    f = fp8q.lib().fp8q_add_rmsnorm_grad
+    for M in (1, 4, 24, 25, 256, 257, 4576):
+        need = fp8q.fp8q_add_rmsnorm_grad_workspace_bytes(M, 640)
+        assert f(*([G] * 8 + [need - 1, M, 640, None])) == SHAPE and "workspace" in _err()
+    f, size = fp8q.lib().fp8q_gemm_dgrad, fp8q.fp8q_gemm_dgrad_workspace_bytes
+    for M in (1, 16, 128, 129, 200):
+        need = size(M, 5120, 6144)
+        assert need and f(*([G] * 6 + [need - 1, M, 5120, 6144, None])) == SHAPE and "workspace" in _err()
