@@ -171,3 +171,32 @@ def test_scalars_anywhere():
         first = d.clone() if i == 0 else first
         assert ((d - (i + 1) * first).abs() <= 2.0 ** -20 * (i + 1) * first.abs().max()).all()
     assert ((losses.cpu().double() - rl).abs() <= 4 * F32 * rl).all() and (losses == losses[0]).all()
+
+
+# Both sides of every border of the numbers of logits a lane holds, and of the workgroups'
+# sums: slices cut at 16 (few experts), and fewer of them with more rounds (many).
+@pytest.mark.parametrize("E", [1, 31, 32, 33, 63, 95, 96, 97, 127, 129, 159, 161, 191, 193, 223, 224, 225, 255, 257,
+                               383, 384, 385, 511])
+@pytest.mark.parametrize("T", [129, 1100])
+def test_every_number_of_experts(T, E):
+    k = min(E, 3)
+    dtype = torch.bfloat16 if E % 2 else torch.float32
+    l, ids, dw = _router(T, E, k, dtype, T + E, masked=E // 8)
+    counts, prob, loss = _balance(l, ids, 0.5)
+    rc, rp, rl, _ = ref.balance(l, ids, 0.5)
+    assert torch.equal(counts.long(), rc)
+    assert ((prob.double() - rp).abs() <= F32 * rp).all() and abs(loss - rl) <= 4 * F32 * rl
+    if T < 1000:
+        for renorm in (True, False):
+            d = _grad(l, ids, dw, rc, 1.5, 20.0, renorm, k)
+            _near(d, *ref.route_grad(l, ids, dw, rc, 1.5, 20.0, renorm, k))
+
+
+def test_many_tokens_of_few_and_of_many_experts():
+    """256 workgroups' sums, in 16 slices and in 3."""
+    for T, E in ((20000, 8), (20000, 512)):
+        l, ids, _ = _router(T, E, 2, torch.float32, E)
+        counts, prob, loss = _balance(l, ids, 0.5)
+        rc, rp, rl, _ = ref.balance(l, ids, 0.5)
+        assert torch.equal(counts.long(), rc)
+        assert ((prob.double() - rp).abs() <= F32 * rp).all() and abs(loss - rl) <= 4 * F32 * rl

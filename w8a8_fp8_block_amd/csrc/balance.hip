@@ -32,6 +32,10 @@ constexpr uint32_t kWaves = 16, kThreads = 64 * kWaves;
 // us, 8.6 by two, but 256: 11.2 and 8.8); beyond, at least kBlockTokens a workgroup and at
 // most kMaxBlocks of them (128 or 512 at 16384 tokens: within 2%), summed by a second launch.
 constexpr uint32_t kLoneTokens = 128, kBlockTokens = 64, kMaxBlocks = 256;
+// Slices of that sum, each joined behind the one before: of 256 workgroups 16 leave a thread
+// one round of 16 loads.  (As many as the threads make, 204 at 8 experts: 9.2 us a call and not
+// 6.5 at 16384 tokens; 93 at 40: 8.0 and not 7.3.)
+constexpr uint32_t kMaxSlices = 16;
 
 uint32_t balance_blocks(uint32_t T) {
   return T <= kLoneTokens ? 1 : std::min((T + kBlockTokens - 1) / kBlockTokens, kMaxBlocks);
@@ -181,12 +185,15 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs a) {
 }
 
 // The workgroups' sums: `slices` slices of the workgroups, each in order, then in slice
-// order.  One workgroup, bound by the latency of its loads: 24 of 16 bytes in flight a thread,
-// one round of them for 256 workgroups of 160 experts.  (Words past the counts are never used.)
+// order.  One workgroup, bound by the latency of its loads: up to 16 of 16 bytes in flight a
+// thread.  (Words past the counts are never used.)  Both launches of a call, bf16 logits, us,
+// with 24 in flight -> 16: 1024 tokens of 8 experts 6.3 -> 5.8, 64: 7.1 -> 6.8, 160: 9.3 -> 8.7,
+// 256: 11.1 -> 10.5; 16384 tokens of 64: 7.9 -> 7.7, 128: 10.5 -> 10.8, 160: 11.5 -> 11.7, 192:
+// 13.5 -> 12.6, 256: 16.0 both.
 __global__ __launch_bounds__(kThreads) void balance_sum_kernel(BalanceArgs a, uint32_t slices) {
   extern __shared__ uint32_t lds[];  // [slices][part_words(E)], then psum and cnt in slice 0's place
   __shared__ float red[kWaves];
-  constexpr uint32_t kInFlight = 24;
+  constexpr uint32_t kInFlight = 16;
   const uint32_t EB = a.E + 1, R = part_words(a.E), V = R / 4;
   const u32x4* part = reinterpret_cast<const u32x4*>(a.part);
   for (uint32_t at = threadIdx.x; at < slices * V; at += kThreads) {
@@ -365,17 +372,24 @@ hipError_t launch_grad_nv(const RouteGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// f(NV) for the logits a lane holds
+// f(NV) for the logits a lane holds: 2 for each 32 experts up to 256, then 8 for each 128.  (In
+// the next larger instance, the gradient of 16384 tokens, bf16: 96 experts 5.4 us and not 5.0,
+// 224: 12.2 and not 8.5, 384: 22.9 and not 19.7.)
 template <class F>
 hipError_t for_experts(uint32_t E, F&& f) {
   using std::integral_constant;
-  if (E <= 32) return f(integral_constant<int, 2>{});
-  if (E <= 64) return f(integral_constant<int, 4>{});
-  if (E <= 128) return f(integral_constant<int, 8>{});
-  if (E <= 160) return f(integral_constant<int, 10>{});
-  if (E <= 192) return f(integral_constant<int, 12>{});
-  if (E <= 256) return f(integral_constant<int, 16>{});
-  return f(integral_constant<int, 32>{});
+  if (E > 384) return f(integral_constant<int, 32>{});
+  if (E > 256) return f(integral_constant<int, 24>{});
+  switch ((E + 31) / 32) {
+    case 1: return f(integral_constant<int, 2>{});
+    case 2: return f(integral_constant<int, 4>{});
+    case 3: return f(integral_constant<int, 6>{});
+    case 4: return f(integral_constant<int, 8>{});
+    case 5: return f(integral_constant<int, 10>{});
+    case 6: return f(integral_constant<int, 12>{});
+    case 7: return f(integral_constant<int, 14>{});
+    default: return f(integral_constant<int, 16>{});
+  }
 }
 
 }  // namespace
@@ -391,7 +405,7 @@ hipError_t launch_balance(const void* logits, bool bf16, const int32_t* ids, int
                       balance_blocks(T), bf16};
   const hipError_t e = for_experts(E, [&](auto nv) { return launch_balance_nv<decltype(nv)::value>(a, s); });
   if (e != hipSuccess || a.blocks == 1) return e;
-  const uint32_t R = part_words(E), slices = std::max(1u, kThreads / (R / 4));
+  const uint32_t R = part_words(E), slices = std::clamp(kThreads / (R / 4), 1u, kMaxSlices);
   balance_sum_kernel<<<dim3(1), dim3(kThreads), (size_t)slices * R * 4, s>>>(a, slices);
   return hipGetLastError();
 }
