@@ -733,8 +733,10 @@ size_t fp8q_proj_lora_workspace_bytes(uint32_t M, uint32_t N, uint32_t K,
  *   rstd      [M] fp32 out or NULL: what fp8q_add_rmsnorm_grad reads
  * Sums, rstd and y are fp32; y is quantized from fp32, not from its bf16 copy.  A
  * row with a NaN or an infinity, or whose squares leave fp32's range, gets NaN
- * scales.  K % 128 == 0, K <= FP8Q_MAX_NORM_K; eps from 2^-126 up, finite, else
- * FP8Q_ERR_VARIANT.  M == 0: nothing.  Otherwise as fp8q_quant_act. */
+ * scales.  A row's results do not depend on the rows beside it, but calls of up to 256 rows
+ * add its squares in another order than larger ones: between the two rstd may differ in its
+ * last bits, and a code by a step.  K % 128 == 0, K <= FP8Q_MAX_NORM_K; eps from 2^-126 up,
+ * finite, else FP8Q_ERR_VARIANT.  M == 0: nothing.  Otherwise as fp8q_quant_act. */
 #define FP8Q_MAX_NORM_K 32768
 fp8q_status fp8q_add_rmsnorm_quant(const uint16_t *x_bf16, const uint16_t *residual_bf16,
                                    const uint16_t *weight_bf16, uint16_t *h_bf16,

@@ -223,3 +223,46 @@ def test_gradient_against_differences():
         size = float(((BF16 * dx.double().abs() + F32 * sx) * u.abs()).sum())
         assert abs(float((dx.double() * u).sum()) - nx) <= size + 1e-6 * float((sx * u.abs()).sum())
         assert abs(float((dw.double() * v).sum()) - nw) <= (F32 + 1e-6) * float((sw * v.abs()).sum())
+
+
+@pytest.mark.parametrize("K", [384, 5120, 17408])
+def test_a_row_alone_and_in_a_batch(K):
+    """Calls of up to 256 rows add a row's squares in one order and larger ones in another,
+    since a row has twice the waves there: within each kind a row's results are the same bits
+    in every batch, and between the two they agree as two results within the tolerances
+    do."""
+    x, r, w = _inputs(600, K, K + 1)
+    many, more, few, one = (_forward(x[:n], r[:n], w) for n in (300, 600, 200, 1))
+    for a, b, n in ((one, few, 1), (many, more, 300)):
+        for k in ("h", "y", "q", "srm", "rstd"):
+            assert torch.equal(a[k][:n].contiguous().view(torch.uint8), b[k][:n].contiguous().view(torch.uint8)), k
+    last = _forward(x[199:200], r[199:200], w)
+    for k in ("h", "y", "q", "srm", "rstd"):
+        assert torch.equal(last[k].view(torch.uint8), few[k][199:].contiguous().view(torch.uint8)), k
+    _, _, y, scale, q = ref.norm(x[:200], r[:200], w, EPS)
+    for o in (few, {k: v[:200] for k, v in many.items()}):
+        assert ((o["y"].double() - y).abs() <= (BF16 + F32) * y.abs()).all()
+        assert ((o["srm"].double() - scale).abs() <= F32 * scale).all()
+        assert ((ref.code_values(o["q"]) - q).abs() <= q.abs() * (2.0 ** -4 + F32) + 2.0 ** -10).all()
+    assert torch.equal(few["h"], many["h"][:200])
+    assert ((few["rstd"].double() - many["rstd"][:200].double()).abs() <= 2 * F32 * few["rstd"].double()).all()
+    assert ((few["y"].double() - many["y"][:200].double()).abs() <= 2 * (BF16 + F32) * y.abs()).all()
+    assert ((few["srm"].double() - many["srm"][:200].double()).abs() <= 2 * F32 * scale).all()
+    off = (ref.code_values(few["q"]) - ref.code_values(many["q"][:200])).abs()
+    assert (off <= 2 * (q.abs() * (2.0 ** -4 + F32) + 2.0 ** -10)).all()
+    # a code moves where the two values lie on two sides of a border: 2^-17 of the value apart,
+    # the borders 2^-4 of it, so one in 2^13
+    assert (off != 0).double().mean() < 1e-3
+
+
+def test_gradient_of_a_row_alone_and_in_a_batch():
+    """dx in the same way: the same bits within a kind of launch."""
+    K = 5120
+    h, dh, w = _inputs(600, K, 9)
+    dy, _, _ = _inputs(600, K, 10, False)
+    rstd = (h.double().square().mean(1) + EPS).rsqrt().float()
+    dx = {n: _backward(dy[:n], dh[:n], h[:n], w, rstd[:n])[0] for n in (20, 200, 300, 600)}
+    assert torch.equal(dx[20], dx[200][:20]) and torch.equal(dx[300], dx[600][:300])
+    rx, _, sx, _ = ref.norm_grad(dy[:200], dh[:200], h[:200], w, rstd[:200])
+    for n in (200, 600):
+        assert ((dx[n][:200].double() - rx).abs() <= BF16 * rx.abs() + F32 * sx).all()
