@@ -14,12 +14,14 @@
 //
 // A wave takes four tokens at a time, one a 16-lane row, lane l of it holding the logits
 // l, l + 16, ...: a reduction is four DPP steps for all four.  (One token a wave, its
-// reductions over 64 lanes, was bound by the vector instructions: 13 us a launch at 16384
-// tokens of 160 experts, twice the present.)  Probabilities are summed in registers, then
+// reductions over 64 lanes: 13 us a launch at 16384 tokens of 160 experts, twice the
+// present.)  Probabilities are summed in registers, then
 // over a workgroup's waves and over the workgroups in a fixed order; counts are integers,
 // so their LDS atomics give the same result in any order.  16384 tokens of 160 experts, bf16
-// (5 MB, in the caches): 7.7 us, the sums' kernel 5.7, the gradient's 9.4, of which a launch
-// is 2.3 each; 25 tokens of 64: 3.2 and 3.6, one launch each.
+// (5 MB, in the caches): 7.7 us, the sums' kernel 5.8, the gradient's 9.4, of which a launch
+// is 2.3 each; 25 tokens of 64: 3.1 and 3.6, one launch each.  Bound by the latency of the
+// loads: at 16384 tokens a wave makes one pass of its loop, and of its cycles 71% wait in the
+// loss's kernel and 64% in the gradient's, where 18% and 22% issue.
 #include <algorithm>
 
 #include "wave_common.h"

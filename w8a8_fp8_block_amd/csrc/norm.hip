@@ -19,7 +19,7 @@
 // holding the 8-value chunks t, t + 64 W, ...: 16 consecutive lanes hold a scale
 // group, whose maximum is one DPP reduction.  4576 x 5120, inputs from HBM: 39 us with
 // residual and bf16 copy (211 MB, 5.4 TB/s; a copy of 1 GiB moves 5.1), the gradient 42 us
-// (187 MB), 39 of them in its first kernel; one token of 5120: 2.8 us, an empty launch's 2.3.
+// (187 MB), 39 of them in its first kernel; one token of 5120: 2.7 us, an empty launch's 2.3.
 #include <algorithm>
 
 #include "wave_common.h"
@@ -192,7 +192,9 @@ struct NormGradArgs {
 // Row groups of W waves take the rows g, g + groups, ... and keep their share of dw in
 // registers; the row groups of a workgroup (blockDim.x / (64 W)) meet in LDS at the end.
 // T: the workgroup's threads at most.  (dh loaded behind the row's sum where a lane holds
-// three chunks or four: 4576 x 17408 138 us, with the other loads 165.)
+// three chunks or four: 4576 x 17408 131 us, with the other loads 165.  128 registers a lane do
+// not hold three or four chunks of it all: a few spill at three, 40 of them at four, where 2000
+// x 32768 takes 209 us, 2.5 TB/s.)
 template <uint32_t W, uint32_t C, uint32_t T>
 __global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
   extern __shared__ float dws[];  // [K], where a workgroup holds several row groups
@@ -243,7 +245,7 @@ __global__ __launch_bounds__(T) void norm_grad_kernel(NormGradArgs a) {
       const uint32_t c = t + 64 * W * i;
       if (live && c < chunks) {
         const u32x4 w = a.w[c];
-        if (C > 2 && a.dh) d[i] = __builtin_nontemporal_load(&a.dh[base + c]);  // (sooner, registers spill)
+        if (C > 2 && a.dh) d[i] = __builtin_nontemporal_load(&a.dh[base + c]);  // (sooner, more registers spill)
         u32x4 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -345,13 +347,16 @@ constexpr uint32_t group_rows(uint32_t W) { return W >= 8 ? 1 : 12 / W; }
 // with: 3.7 -> 3.3 at one row, 4.5 -> 3.6 at 25, 5.7 -> 4.8 at 256; equal from 409.  The
 // gradient: 6.9 -> 6.2 at 64, 8.6 -> 8.1 at 200; 10.6 -> 11.0 at 409).
 constexpr uint32_t kNormFewRows = 256;
-// Workgroups of a gradient call: one a CU (256 CUs).  128 / 256 / 512, us: 12.5 / 10.6 / 10.6 at
-// 409 x 6144, 58.5 / 42.8 / 46.3 at 4576 x 5120.
+// Workgroups of a gradient call: one a CU (256 CUs).  At most 128 / 256 / 512, us in a graph: 11.8
+// / 11.5 / 11.5 at 512 x 6144 (256 workgroups' rows), 19.9 / 17.6 / 19.4 at 1168 x 6144, 13.0 /
+// 11.7 / 14.5 at 4576 x 640, 47.9 / 35.0 / 38.0 at 4576 x 5120.
 constexpr uint32_t kNormGradParts = 256;
 // A gradient call that one workgroup does in two turns at most writes dw itself, one launch and
-// not two.  us a call from the host / in a graph, two -> one: 8 x 384: 8.5 -> 6.0 / 4.2 -> 3.7; 24
-// x 384 (two turns): 8.5 -> 6.0 / 4.3 -> 4.7; 2 x 5120: 8.5 -> 6.0 / 5.0 -> 4.1; 4 x 5120 (two): 8.5
-// -> 6.0 / 5.1 -> 5.6.
+// not two.  In one turn that saves time on both sides; the second turn saves it on the host
+// and costs some on the device.  us a call from the host / in a graph, two launches -> one:
+// one turn: 8 x 384 8.5 -> 6.0 / 4.2 -> 3.6, 2 x 5120 8.5 -> 6.0 / 5.0 -> 3.8; two turns: 24 x 384 9.7
+// -> 6.8 / 4.1 -> 4.5, 12 x 2048 9.5 -> 6.6 / 4.5 -> 5.7 (the worst), 4 x 5120 9.9 -> 6.8 / 4.9 -> 5.1,
+// 2 x 17408 9.8 -> 7.1 / 7.5 -> 7.1.
 bool norm_grad_lone(uint32_t M, uint32_t K) { return M > 0 && M <= 2 * group_rows(row_waves(K, 2)); }
 uint32_t norm_grad_parts(uint32_t M, uint32_t K) {
   if (norm_grad_lone(M, K)) return 1;
