@@ -266,3 +266,25 @@ def test_gradient_of_a_row_alone_and_in_a_batch():
     rx, _, sx, _ = ref.norm_grad(dy[:200], dh[:200], h[:200], w, rstd[:200])
     for n in (200, 600):
         assert ((dx[n][:200].double() - rx).abs() <= BF16 * rx.abs() + F32 * sx).all()
+
+
+@pytest.mark.parametrize("M,K", [(1, 384), (30, 17408), (300, 8320), (300, 17408), (270, 32768)])
+def test_in_place_at_every_kind_of_row(M, K):
+    """dx over dy, dh or h, and h over x or the residual, where a row takes one launch or two,
+    a workgroup or a part of one, and where dh is loaded behind the row's sum."""
+    x, r, w = _inputs(M, K, M + K)
+    dy, dh, _ = _inputs(M, K, M + K + 1)
+    o = _forward(x, r, w)
+    dx, dw = _backward(dy, dh, o["h"], w, o["rstd"])
+    work = torch.empty(fp8q.fp8q_add_rmsnorm_grad_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    for over in range(3):
+        t = [v.cuda() for v in (dy, dh, o["h"])]
+        dw2 = torch.empty(K, device="cuda")
+        fp8q.fp8q_add_rmsnorm_grad(*t, w.cuda(), o["rstd"].cuda(), t[over], dw2, work)
+        assert torch.equal(t[over].cpu(), dx) and torch.equal(dw2.cpu(), dw)
+    for over in range(2):
+        t = [x.cuda(), r.cuda()]
+        q, s = torch.empty(M, K, dtype=torch.uint8, device="cuda"), torch.empty(K // 128, _mp(M), device="cuda")
+        fp8q.fp8q_add_rmsnorm_quant(t[0], t[1], w.cuda(), t[over], None, q, None, s, None, EPS)
+        assert torch.equal(t[over].cpu(), o["h"]) and torch.equal(q.cpu(), o["q"].view(torch.uint8))
+        assert torch.equal(s.cpu(), o["skm"])
