@@ -31,9 +31,10 @@ namespace {
 //   s = fl(amax / 448),  q = fl(y / s), at most 448 in magnitude (e4m3's saturation).
 // fl(a / 448) by a corrected product and the quotients by reciprocal are the correctly
 // rounded ones where s is normal.  (Of all finite a, those up to 2^-120 alone give another
-// scale; of all mantissas of s, the last one alone gives quotients that round to another
-// code, at y / s = 2^-10 and only if the hardware reciprocal is off by an ulp there; from s =
-// 2^-80 the residuals of quotients down to 2^-11, the least that matter, are exact.)  Other
+// scale.  Of all mantissas of s, with y on both sides of every border between two codes, the
+// last one alone gives a quotient that rounds to another code, at y / s = 2^-10 and only if
+// the hardware reciprocal is off by an ulp there; it is divided out too.  From s = 2^-80 the
+// residuals of quotients down to 2^-11, the least that matter, are exact.)  Other
 // scales - zero, tiny, infinite, NaN - are divided out.  The choice is uniform over the
 // wave and both ways give the same codes, so a group's do not depend on its neighbours.
 // Only a subnormal scale, a few units of 2^-149, rounds so far that y / s passes 448: by up
